@@ -21,6 +21,7 @@ TABLE_BF16, TABLE_FP8_E8M0, TABLE_Q2K = 0, 1, 2
 WKV_BF16, WKV_MXFP8 = 0, 1
 TABLE_FORMATS = {"bf16": TABLE_BF16, "fp8": TABLE_FP8_E8M0, "q2k": TABLE_Q2K}
 ERR_RAW_ID, ERR_ROW_ID, ERR_PIPE_TIMEOUT = 1, 2, 4
+ERR_SLOT, ERR_PAGE, ERR_POSITION, ERR_SEQ_LEN = 8, 16, 32, 64
 NOALLOC_SCRATCH_BYTES = 32 << 20   # ENGRAM_NOALLOC_SCRATCH_BYTES
 INT64_MAX = (1 << 63) - 1
 
@@ -114,6 +115,13 @@ def lib() -> C.CDLL:
         L.engram_set_gather_order.argtypes = [I32]
         L.engram_set_gather_order.restype = None
         L.engram_project_plan.argtypes = [I64, I32, I32, I32, I32, P]
+        L.engram_qk_norm_rope.argtypes = [P, I64, I32, P, P, P, P, P, P, P]
+        L.engram_kv_write.argtypes = [P, I64, P, P, P, P, P]
+        L.engram_kv_read.argtypes = [P, I64, P, P, P, P, P]
+        L.engram_attention_workspace_bytes.argtypes = [P, I32, I32]
+        L.engram_attention_workspace_bytes.restype = SZ
+        L.engram_paged_attention.argtypes = [P, P, P, C.c_float, I32, P, P, P, SZ, P, P]
+        L.engram_attention_step.argtypes = [P, P, P, P, P, P, P, P, C.c_float, I32, P, P, P, SZ, P, P]
         _lib = L
     return _lib
 

@@ -156,10 +156,16 @@ int engram_sync_status(const int32_t* err_flag, engram_stream_t stream) {
     return ENGRAM_ECUDA;
   }
   if (v != 0) {
-    set_error("engram_sync_status: err_flag 0x%x:%s%s%s", v,
+    constexpr int32_t known = ENGRAM_ERR_RAW_ID | ENGRAM_ERR_ROW_ID | ENGRAM_ERR_SLOT | ENGRAM_ERR_PAGE |
+                              ENGRAM_ERR_POSITION | ENGRAM_ERR_SEQ_LEN;
+    set_error("engram_sync_status: err_flag 0x%x:%s%s%s%s%s%s%s", v,
               (v & ENGRAM_ERR_RAW_ID) ? " raw id outside the token map (hashed as pad_id);" : "",
               (v & ENGRAM_ERR_ROW_ID) ? " row id outside the table (zero row);" : "",
-              (v & ~(ENGRAM_ERR_RAW_ID | ENGRAM_ERR_ROW_ID)) ? " unknown bits;" : "");
+              (v & ENGRAM_ERR_SLOT) ? " slot past the cache (skipped, or zero rows);" : "",
+              (v & ENGRAM_ERR_PAGE) ? " page number outside the cache (its keys hidden);" : "",
+              (v & ENGRAM_ERR_POSITION) ? " position outside the rotation table (clamped);" : "",
+              (v & ENGRAM_ERR_SEQ_LEN) ? " sequence length outside its page table (clamped);" : "",
+              (v & ~known) ? " unknown bits;" : "");
     return ENGRAM_EDATA;
   }
   return ENGRAM_OK;

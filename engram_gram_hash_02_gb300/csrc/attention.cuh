@@ -1,0 +1,815 @@
+// Attention of one new token per sequence over a paged cache of keys and values.
+//
+// For query head h of sequence b and the attended keys j (the last `window` of its `len` tokens, or all):
+//   s_j = scale * q_h . k_j,   o_h = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse_h = log sum_j exp(s_j)
+// in one pass with a running maximum (kept in units of log 2, so that every exponential is one ex2). Heads
+// that share a key head are computed together, up to 16, so a key or value row is read from HBM once.
+//
+// What bounds it: those rows' bytes. Per 16 keys a warp computes two small products on the tensor cores
+// (mma.sync m16n8k16, keys or values on the 16 rows, query heads on the 8 columns, fp32 accumulation):
+//   S^T[keys, heads] = K Q^T      and      O^T[values, heads] += V^T P^T
+// With one token per sequence the heads of a group are the only rows there are; the tensor pipe stays
+// mostly idle, and operands in registers (no tensor memory to set up, drain and rescale through) keep a
+// warp's chain from a landed copy to the next one short.
+//
+// Work is cut at keys, not at sequences: the tiles (64 keys of bf16, 128 of FP8) of all sequences and key
+// heads form one row, sequence by sequence, and each CTA takes an equal run of it, so a batch of any mix of
+// lengths keeps every SM busy to the end. Each of a CTA's four warps owns a quarter of every tile and a
+// private ring of shared-memory stages filled by 16-byte cp.async (rows at the addresses their page gives;
+// any page size, stride or tail): no barrier joins the warps until a sequence's run ends. There the four
+// partial results are joined in shared memory. A run that is cut between CTAs is written to the workspace as
+// (unnormalised o, maximum, sum); the last CTA to arrive joins the parts in order of their keys, so results
+// do not depend on timing.
+//
+// FP8 rows (codes, one power-of-two scale per 32 values) are converted to f16 in registers (exact). A key
+// block's scale multiplies that block's fp32 partial product. The value scales join the weights before those
+// are rounded: with 2^e_j the largest scale of value row j, a second running maximum M (of s_j + e_j) gives
+// weights 2^(s_j + e_j - M + 15) that fill f16's range, and a block's own scale enters as 2^(scale - e_j), a
+// half that is exact down to 2^-24. So no spread of the rows' sizes overflows, and a weight loses bits only
+// 2^-29 below its head's largest contribution.
+//
+// Roundings below 32 bits: with bf16 rows P is fed as the sum of two bf16 (hi + lo, 16 bits: 2^-17); with
+// FP8 rows as f16 (2^-12, an eighth of the output's own rounding). bf16 queries enter as they are; fp32
+// queries as two bf16 or two f16; for f16 each query row is first scaled by a power of two (its largest
+// value below 2^14). Scores, maxima, sums and o are fp32.
+#pragma once
+
+#include "attn.cuh"
+
+namespace engram {
+namespace attn {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 bytes to shared memory, or 16 zero bytes (nothing is read then)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (kHalf)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// exp2(x - m) for m = max(x, ...): a maximum of -inf (nothing attended yet) gives 0
+__device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
+
+template <int DP_, bool kFp8_, int NQ_, bool kSplit_>
+struct Cfg {
+  static constexpr int DP = DP_;                      // head_dim rounded up to 64, 128 or 256
+  static constexpr bool kFp8 = kFp8_;
+  static constexpr int NQ = NQ_;                      // tiles of 8 query heads
+  static constexpr bool kSplit = kSplit_;             // fp32 queries: high and low parts
+  static constexpr int kStep = kFp8 ? 32 : 16;        // keys per warp and step
+  static constexpr int kTile = kWarps * kStep;
+  static constexpr int kRowB = kFp8 ? DP : 2 * DP;
+  static constexpr int kWords = (DP + 127) / 128;     // scale words per row
+  static constexpr int kStageB = 2 * kStep * kRowB + (kFp8 ? 2 * kStep * kWords * 4 : 0);
+  static constexpr int kCtas = DP == 64 ? 3 : DP == 128 ? 2 : 1;
+  static constexpr int kStages = DP == 64 ? 4 : 3;
+  static constexpr int kRingB = kWarps * kStages * kStageB;
+  static constexpr int kQPitch = DP + 8;              // 16-bit values
+  static constexpr int kQB = NQ * 8 * kQPitch * 2;    // per part (high, low)
+  static constexpr int kMetaB = kWarps * kStages * 32;
+  static constexpr int kSmall = 1024;                 // maxima, sums, query scales, scan words
+  static constexpr int kSmemB = kRingB + kQB * (kSplit ? 2 : 1) + kMetaB + kSmall;
+  static constexpr bool kQRegs = DP / 16 * 2 * NQ * (kSplit ? 2 : 1) <= 32;
+  static_assert(NQ * 8 * DP * 4 <= kStageB, "a warp's result is joined in its own last stage");
+};
+
+// byte offset of 16-byte chunk c of row r: eight rows at one chunk lie in eight different bank groups
+template <int kRowB>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if (kRowB >= 128) return (uint32_t)(r * kRowB + ((c ^ (r & 7)) << 4));
+  return (uint32_t)(r * kRowB + ((c ^ ((r >> 1) & 3)) << 4));   // 64-byte rows
+}
+
+// what a warp knows of one step when it consumes it
+struct Meta {
+  uint32_t mask;               // keys of the step that are attended
+  int32_t seq, hc, tile, tiles;// sequence, head * chunks + chunk, tile of the run and tiles it has
+  int32_t pad[3];
+};
+
+__device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : len > cap ? cap : len; }
+__device__ __forceinline__ int attended(int len, int window) { return window > 0 && len > window ? window : len; }
+
+template <typename C>
+__global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const AttnParams p) {
+  constexpr int DP = C::DP, NQ = C::NQ, kStages = C::kStages, kStep = C::kStep, kRowB = C::kRowB;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, j = lane & 3;             // fragment row and column pair
+  uint8_t* ring = smem + warp * kStages * C::kStageB;
+  uint8_t* qs = smem + C::kRingB;
+  Meta* meta = reinterpret_cast<Meta*>(qs + C::kQB * (C::kSplit ? 2 : 1)) + warp * kStages;
+  float* small = reinterpret_cast<float*>(qs + C::kQB * (C::kSplit ? 2 : 1) + C::kMetaB);
+  float* sm_m = small;                               // [warp][16] maxima (log2 units)
+  float* sm_l = small + 64;                          // [warp][16] sums
+  float* sm_c = small + 128;                         // [16] softmax scale of each query row, log2 units
+  int* sm_i = reinterpret_cast<int*>(small + 160);   // scan and broadcast words
+  const int heads = p.Hk * p.chunks;
+
+  // ---- this CTA's run of tiles ---------------------------------------------------------------
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = tid * per, b1 = min(p.B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int raw = __ldg(p.lens + b);
+    if (blockIdx.x == 0 && (raw < 0 || raw > p.cap) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
+    mine += (attended(clamp_len(raw, p.cap), p.window) + C::kTile - 1) / C::kTile * heads;
+  }
+  int scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += y;
+  }
+  if (lane == 31) sm_i[warp] = scan;
+  __syncthreads();
+  int total = 0, before = scan - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sm_i[w];
+    total += sm_i[w];
+  }
+  const int per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+  const int t0 = min(total, (int)blockIdx.x * per_cta), t1 = min(total, t0 + per_cta);
+  if (t0 < t1 && t0 >= before && t0 < before + mine) {
+    int at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int tiles = (attended(clamp_len(__ldg(p.lens + b), p.cap), p.window) + C::kTile - 1) / C::kTile;
+      if (t0 < at + tiles * heads) {
+        sm_i[8] = b;
+        sm_i[9] = (t0 - at) / tiles;
+        sm_i[10] = (t0 - at) % tiles;
+        break;
+      }
+      at += tiles * heads;
+    }
+  }
+  __syncthreads();
+  pdl_wait();
+
+  // ---- the producer's place: step i is tile t0 + i ----------------------------------------------
+  int seq = sm_i[8], hc = sm_i[9], tile = sm_i[10], first = 0, end = 0, tiles = 0;
+  auto enter = [&] {                                  // seq is new
+    const int len = clamp_len(__ldg(p.lens + seq), p.cap);
+    const int n = attended(len, p.window);
+    first = len - n;
+    end = len;
+    tiles = (n + C::kTile - 1) / C::kTile;
+  };
+  auto advance = [&] {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++hc < heads) return;
+    hc = 0;
+    do {
+      if (++seq >= p.B) return;                       // past the last tile: never fetched
+      enter();
+    } while (tiles == 0);
+  };
+  // the page of this lane's row, requested one step before its copies
+  int page = -1, at = 0;
+  bool inside = false;
+  auto request = [&] {
+    const int pos = first + tile * C::kTile + warp * kStep + (lane & (kStep - 1));
+    inside = pos < end;
+    page = -1;
+    if (inside) {
+      const int n = (int)fast_div((uint32_t)pos, p.cache.div_page);
+      at = pos - n * p.cache.page_size;
+      page = __ldg(p.table + (int64_t)seq * p.table_stride + n);
+    }
+  };
+  auto issue = [&](int stage) {
+    const bool live = inside && page >= 0 && page < p.cache.num_pages;
+    if (inside && !live && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
+    uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
+    if (kStep == 16) mask &= 0xFFFFu;
+    if (lane == 0) {
+      Meta m;
+      m.mask = mask; m.seq = seq; m.hc = hc; m.tile = tile; m.tiles = tiles;
+      meta[stage] = m;
+    }
+    if (mask == 0) return;                            // no keys for this warp: the stage is not read
+    const int head = p.chunks == 1 ? hc : hc / p.chunks;
+    const int64_t off = live ? page * p.cache.page_b + head * p.cache.head_b + at * p.cache.tok_b : 0;
+    const uint32_t dst = smem_u32(ring + stage * C::kStageB);
+    constexpr int kChunks = kRowB / 16, kRows = 32 / kChunks;   // 16-byte chunks of a row, rows per pass
+    const int c = lane & (kChunks - 1), sub = lane / kChunks;
+    const bool in_row = c * 16 < (C::kFp8 ? p.D : 2 * p.D);
+#pragma unroll
+    for (int r0 = 0; r0 < kStep; r0 += kRows) {
+      const int r = r0 + sub;
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + c * 16;
+      const bool row_live = (mask >> r) & 1u;
+      if (in_row) {
+        cp_async16(dst + swz<kRowB>(r, c), p.cache.k + o, row_live);
+        cp_async16(dst + kStep * kRowB + swz<kRowB>(r, c), p.cache.v + o, row_live);
+      }
+    }
+    if (C::kFp8) {
+      const int64_t so = live ? page * p.cache.spage_b + head * p.cache.shead_b + at * p.cache.stok_b : 0;
+      const uint32_t sd = dst + 2 * kStep * kRowB + lane * C::kWords * 4;
+#pragma unroll
+      for (int w = 0; w < C::kWords; ++w) {
+        cp_async4(sd + 4 * w, p.cache.ks + so + 4 * w, live);
+        cp_async4(sd + kStep * C::kWords * 4 + 4 * w, p.cache.vs + so + 4 * w, live);
+      }
+    }
+  };
+
+  const int n = t1 - t0;
+  int ahead = 0;                                      // steps requested so far
+  if (n > 0) {
+    enter();
+    request();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (ahead < n) {
+        issue(s);
+        advance();
+        if (++ahead < n) request();
+      }
+      cp_async_commit();
+    }
+  }
+
+  // ---- the consumer ----------------------------------------------------------------------------
+  float o[DP / 16][NQ][4];
+  float m_run[NQ][2], l_run[NQ][2];
+  float u_run[NQ][2];                                 // FP8: running maximum of s + e, the units of o
+  uint32_t qf[C::kQRegs ? NQ : 1][C::kQRegs ? DP / 16 : 1][C::kSplit ? 4 : 2];
+  int rows = 0;                                       // query heads of this run
+  const int total_first = t0;
+
+  auto q_frag = [&](int nq, int ks, uint32_t (&b)[4]) {
+    const uint8_t* row = qs + ((nq * 8 + g) * C::kQPitch + ks * 16) * 2;
+    if (C::kFp8) {                                    // the pairs of values a lane's four codes hold
+      const uint2 hi = *reinterpret_cast<const uint2*>(row + 8 * j);
+      b[0] = hi.x; b[1] = hi.y;
+      if (C::kSplit) {
+        const uint2 lo = *reinterpret_cast<const uint2*>(row + C::kQB + 8 * j);
+        b[2] = lo.x; b[3] = lo.y;
+      }
+    } else {
+      b[0] = *reinterpret_cast<const uint32_t*>(row + 4 * j);
+      b[1] = *reinterpret_cast<const uint32_t*>(row + 4 * j + 16);
+      if (C::kSplit) {
+        b[2] = *reinterpret_cast<const uint32_t*>(row + C::kQB + 4 * j);
+        b[3] = *reinterpret_cast<const uint32_t*>(row + C::kQB + 4 * j + 16);
+      }
+    }
+  };
+
+  int stage = 0;
+  for (int i = 0; i < n; ++i) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    const Meta me = meta[stage];
+
+    if (i == 0 || me.tile == 0) {
+      // a new run: its query rows to shared memory (16-bit, zero rows and columns as padding)
+      const int chunk = p.chunks == 1 ? 0 : me.hc % p.chunks;
+      const int head = p.chunks == 1 ? me.hc : me.hc / p.chunks;
+      rows = min(8 * NQ, p.G - chunk * 8 * NQ);
+      const int h0 = head * p.G + chunk * 8 * NQ;
+      for (int r = warp; r < 8 * NQ; r += kWarps) {
+        float x[DP / 32];
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e) {
+          const int d = lane + 32 * e;
+          x[e] = 0.f;
+          if (r < rows && d < p.D) {
+            const int64_t at_q = (int64_t)me.seq * p.q.ts + (int64_t)(h0 + r) * p.q.hs + d;
+            x[e] = C::kSplit ? static_cast<const float*>(p.q.data)[at_q]
+                             : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.q.data)[at_q] << 16);
+          }
+          amax = fmaxf(amax, fabsf(x[e]));
+        }
+        int up = 0;                                   // x * 2^up in f16
+        if (C::kFp8) {
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, s));
+          const int field = (int)(__float_as_uint(amax) >> 23);
+          if (amax > 0.f && field < 255) up = 140 - max(field, 1);   // amax * 2^up in [2^13, 2^14)
+          if (lane == 0) sm_c[r] = ldexpf(p.scale_log2, -up);
+        }
+        uint16_t* dst = reinterpret_cast<uint16_t*>(qs) + r * C::kQPitch + lane;
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e) {
+          if (C::kFp8) {
+            const float y = ldexpf(x[e], up);
+            const __half hi = __float2half_rn(y);
+            dst[32 * e] = __half_as_ushort(hi);
+            if (C::kSplit) {
+              const float lo = y - __half2float(hi);                 // inf - inf: the high part says it all
+              dst[32 * e + C::kQB / 2] = __half_as_ushort(__float2half_rn(lo == lo ? lo : 0.f));
+            }
+          } else {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(x[e]);
+            dst[32 * e] = __bfloat16_as_ushort(hi);
+            if (C::kSplit) {
+              const float lo = x[e] - __bfloat162float(hi);
+              dst[32 * e + C::kQB / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(lo == lo ? lo : 0.f));
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (C::kQRegs) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int ks = 0; ks < DP / 16; ++ks) {
+            uint32_t b[4];
+            q_frag(nq, ks, b);
+#pragma unroll
+            for (int e = 0; e < (C::kSplit ? 4 : 2); ++e) qf[nq][ks][e] = b[e];
+          }
+      }
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) { m_run[nq][e] = u_run[nq][e] = -INFINITY; l_run[nq][e] = 0.f; }
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nq][e] = 0.f;
+      }
+    }
+
+    // the stage consumed in the last step is refilled while this one is computed
+    if (ahead < n) {
+      issue(stage == 0 ? kStages - 1 : stage - 1);
+      advance();
+      if (++ahead < n) request();
+    }
+    cp_async_commit();
+
+    if (me.mask != 0) {
+      const uint32_t ks_addr = smem_u32(ring + stage * C::kStageB);
+      const uint32_t vs_addr = ks_addr + kStep * kRowB;
+      constexpr int KT = kStep / 16;
+      uint32_t pb[KT][NQ][C::kFp8 ? 2 : 4];            // P as the second product's operand (bf16: high, low)
+      float t[KT][NQ][4];
+      uint32_t* kw = reinterpret_cast<uint32_t*>(ring + stage * C::kStageB + 2 * kStep * kRowB);
+      const uint32_t* vw = kw + kStep * C::kWords;
+
+      // S^T = K Q^T
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const int row = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        if (C::kFp8) {
+          uint32_t w0[C::kWords], w1[C::kWords];
+#pragma unroll
+          for (int w = 0; w < C::kWords; ++w) {
+            w0[w] = kw[(kt * 16 + g) * C::kWords + w];
+            w1[w] = kw[(kt * 16 + g + 8) * C::kWords + w];
+          }
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[kt][nq][e] = 0.f;
+#pragma unroll
+          for (int b = 0; b < DP / 32; ++b) {
+            if (b * 32 >= p.D) break;
+            uint32_t a[4];                             // codes: keys g, g + 8 (values 0..15), g, g + 8 (16..31)
+            ldsm4(a, ks_addr + swz<kRowB>(row, 2 * b + (lane >> 4)));
+            const float s0 = __uint_as_float(((w0[b / 4] >> (8 * (b & 3))) & 0xFFu) << 23);
+            const float s1 = __uint_as_float(((w1[b / 4] >> (8 * (b & 3))) & 0xFFu) << 23);
+            uint32_t f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] = e4m3x2_to_f16x2(a[e] & 0xFFFFu);
+              f[2 * e + 1] = e4m3x2_to_f16x2(a[e] >> 16);
+            }
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t q4[4];
+                if (C::kQRegs) {
+#pragma unroll
+                  for (int x = 0; x < (C::kSplit ? 4 : 2); ++x) q4[x] = qf[nq][2 * b + e][x];
+                } else {
+                  q_frag(nq, 2 * b + e, q4);
+                }
+                mma<true>(acc, f[4 * e], f[4 * e + 2], f[4 * e + 1], f[4 * e + 3], q4[0], q4[1]);
+                if (C::kSplit) mma<true>(acc, f[4 * e], f[4 * e + 2], f[4 * e + 1], f[4 * e + 3], q4[2], q4[3]);
+              }
+              t[kt][nq][0] += acc[0] * s0;
+              t[kt][nq][1] += acc[1] * s0;
+              t[kt][nq][2] += acc[2] * s1;
+              t[kt][nq][3] += acc[3] * s1;
+            }
+          }
+        } else {
+          float acc[NQ][2][4];                         // two chains: even and odd steps
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nq][0][e] = acc[nq][1][e] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < DP / 16; ++ks) {
+            if (ks * 16 >= p.D) break;
+            uint32_t a[4];
+            ldsm4(a, ks_addr + swz<kRowB>(row, 2 * ks + (lane >> 4)));
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+              uint32_t q4[4];
+              if (C::kQRegs) {
+#pragma unroll
+                for (int x = 0; x < (C::kSplit ? 4 : 2); ++x) q4[x] = qf[nq][ks][x];
+              } else {
+                q_frag(nq, ks, q4);
+              }
+              mma<false>(acc[nq][ks & 1], a[0], a[1], a[2], a[3], q4[0], q4[1]);
+              if (C::kSplit) mma<false>(acc[nq][ks & 1], a[0], a[1], a[2], a[3], q4[2], q4[3]);
+            }
+          }
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[kt][nq][e] = acc[nq][0][e] + acc[nq][1][e];
+        }
+      }
+
+      // this lane's key: e = its largest value scale, and its blocks' scales relative to that as halves, which
+      // take the place of the step's scale words ([key][2 * kWords] words). A block that holds an infinity
+      // (bytes 254 and 255) has an infinite factor and no part in e: it spoils its own 32 values only.
+      float e_own = 0.f;
+      if (C::kFp8) {
+        uint32_t w[C::kWords], f[2 * C::kWords];
+        int top = 0;
+#pragma unroll
+        for (int b = 0; b < DP / 32; ++b) {
+          if ((b & 3) == 0) w[b / 4] = vw[lane * C::kWords + b / 4];
+          const int by = (int)((w[b / 4] >> (8 * (b & 3))) & 0xFFu);
+          if (b * 32 < p.D && by < 254) top = max(top, by);
+        }
+        e_own = (float)(top - 127);
+#pragma unroll
+        for (int x = 0; x < 2 * C::kWords; ++x) {
+          float y[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int by = (int)((w[x / 2] >> (16 * (x & 1) + 8 * z)) & 0xFFu);
+            y[z] = __uint_as_float(by >= 254 ? 0x7F800000u : (uint32_t)max(127 + by - top, 0) << 23);
+          }
+          f[x] = pack_f16(y[0], y[1]);
+        }
+        __syncwarp();                                 // every lane has read the scale words
+#pragma unroll
+        for (int x = 0; x < 2 * C::kWords; ++x) kw[lane * 2 * C::kWords + x] = f[x];
+        __syncwarp();
+      }
+
+      // softmax over the step's keys, for each of this lane's two heads per tile
+      bool moved = false;
+      float alpha[NQ][2];                             // what o is multiplied by
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        float mx[2] = {-INFINITY, -INFINITY}, ux[2] = {-INFINITY, -INFINITY};
+        float u[KT][4];
+        const float c0 = C::kFp8 ? sm_c[nq * 8 + 2 * j] : p.scale_log2;
+        const float c1 = C::kFp8 ? sm_c[nq * 8 + 2 * j + 1] : p.scale_log2;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+          const bool v0 = (me.mask >> (kt * 16 + g)) & 1u, v1 = (me.mask >> (kt * 16 + g + 8)) & 1u;
+          float(&x)[4] = t[kt][nq];
+          x[0] = v0 ? x[0] * c0 : -INFINITY;
+          x[1] = v0 ? x[1] * c1 : -INFINITY;
+          x[2] = v1 ? x[2] * c0 : -INFINITY;
+          x[3] = v1 ? x[3] * c1 : -INFINITY;
+          mx[0] = fmaxf(mx[0], fmaxf(x[0], x[2]));
+          mx[1] = fmaxf(mx[1], fmaxf(x[1], x[3]));
+          if (C::kFp8) {
+            const float e0 = __shfl_sync(0xFFFFFFFFu, e_own, kt * 16 + g), e1 = __shfl_sync(0xFFFFFFFFu, e_own, kt * 16 + g + 8);
+            u[kt][0] = x[0] + e0; u[kt][1] = x[1] + e0; u[kt][2] = x[2] + e1; u[kt][3] = x[3] + e1;
+            ux[0] = fmaxf(ux[0], fmaxf(u[kt][0], u[kt][2]));
+            ux[1] = fmaxf(ux[1], fmaxf(u[kt][1], u[kt][3]));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) {
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], s));
+            if (C::kFp8) ux[e] = fmaxf(ux[e], __shfl_xor_sync(0xFFFFFFFFu, ux[e], s));
+          }
+          const float m = fmaxf(m_run[nq][e], mx[e]);
+          const float fade = ex2_rel(m_run[nq][e], m);
+          if (!C::kFp8) {
+            alpha[nq][e] = fade;
+            moved |= m != m_run[nq][e];
+          }
+          m_run[nq][e] = m;
+          const float base = m == -INFINITY ? 0.f : m;
+          float sum = 0.f;
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            t[kt][nq][e] = ex2(t[kt][nq][e] - base);
+            t[kt][nq][e + 2] = ex2(t[kt][nq][e + 2] - base);
+            sum += t[kt][nq][e] + t[kt][nq][e + 2];
+          }
+          l_run[nq][e] = l_run[nq][e] * fade + sum;
+          if (C::kFp8) {
+            const float um = fmaxf(u_run[nq][e], ux[e]);
+            alpha[nq][e] = ex2_rel(u_run[nq][e], um);
+            moved |= um != u_run[nq][e];
+            u_run[nq][e] = um;
+            const float ubase = um == -INFINITY ? 0.f : um - 15.f;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+              t[kt][nq][e] = ex2(u[kt][e] - ubase);
+              t[kt][nq][e + 2] = ex2(u[kt][e + 2] - ubase);
+            }
+          }
+        }
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+          const float(&x)[4] = t[kt][nq];
+          if (C::kFp8) {
+            pb[kt][nq][0] = transpose8(pack_f16(x[0], x[1]));
+            pb[kt][nq][1] = transpose8(pack_f16(x[2], x[3]));
+          } else {
+            const uint32_t h0 = pack_bf16(x[0], x[1]), h1 = pack_bf16(x[2], x[3]);
+            pb[kt][nq][0] = transpose8(h0);
+            pb[kt][nq][1] = transpose8(h1);
+            pb[kt][nq][C::kFp8 ? 0 : 2] = transpose8(pack_bf16(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0)));
+            pb[kt][nq][C::kFp8 ? 0 : 3] = transpose8(pack_bf16(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1)));
+          }
+        }
+      }
+
+      // o in the new units
+      if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq) {
+            o[mt][nq][0] *= alpha[nq][0];
+            o[mt][nq][1] *= alpha[nq][1];
+            o[mt][nq][2] *= alpha[nq][0];
+            o[mt][nq][3] *= alpha[nq][1];
+          }
+      }
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        if (C::kFp8) {
+          const int row = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+          uint32_t s0[2][2 * C::kWords], s1[2][2 * C::kWords];   // block scales of keys 2j, 2j + 1 (+ 0 and + 8)
+#pragma unroll
+          for (int x = 0; x < 2 * C::kWords; ++x) {
+            s0[0][x] = kw[(kt * 16 + 2 * j) * 2 * C::kWords + x];
+            s0[1][x] = kw[(kt * 16 + 2 * j + 1) * 2 * C::kWords + x];
+            s1[0][x] = kw[(kt * 16 + 2 * j + 8) * 2 * C::kWords + x];
+            s1[1][x] = kw[(kt * 16 + 2 * j + 9) * 2 * C::kWords + x];
+          }
+#pragma unroll
+          for (int b = 0; b < DP / 32; ++b) {
+            if (b * 32 >= p.D) break;
+            uint32_t a[4];                             // pairs of values: keys 0..7, 8..15 (values 0..15), the same of 16..31
+            ldsm4t(a, vs_addr + swz<kRowB>(row, 2 * b + (lane >> 4)));
+            const uint32_t y0 = __byte_perm(s0[0][b / 2], s0[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
+            const uint32_t y1 = __byte_perm(s1[0][b / 2], s1[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
+            uint32_t f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = __byte_perm(a[e], 0u, 0x3120);   // (value 2g of both keys, value 2g + 1 of both)
+              f[2 * e] = e4m3x2_to_f16x2(x & 0xFFFFu);
+              f[2 * e + 1] = e4m3x2_to_f16x2(x >> 16);
+            }
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+              const __half2 p0 = __hmul2(*reinterpret_cast<const __half2*>(&pb[kt][nq][0]), *reinterpret_cast<const __half2*>(&y0));
+              const __half2 p1 = __hmul2(*reinterpret_cast<const __half2*>(&pb[kt][nq][1]), *reinterpret_cast<const __half2*>(&y1));
+              const uint32_t b0w = *reinterpret_cast<const uint32_t*>(&p0), b1w = *reinterpret_cast<const uint32_t*>(&p1);
+              mma<true>(o[2 * b][nq], f[0], f[1], f[2], f[3], b0w, b1w);
+              mma<true>(o[2 * b + 1][nq], f[4], f[5], f[6], f[7], b0w, b1w);
+            }
+          }
+        } else {
+          const int row = kt * 16 + (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+          for (int mt = 0; mt < DP / 16; ++mt) {
+            if (mt * 16 >= p.D) break;
+            uint32_t a[4];
+            ldsm4t(a, vs_addr + swz<kRowB>(row, 2 * mt + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+              mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[kt][nq][0], pb[kt][nq][1]);
+              mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[kt][nq][C::kFp8 ? 0 : 2], pb[kt][nq][C::kFp8 ? 1 : 3]);
+            }
+          }
+        }
+      }
+    }
+
+    if (me.tile + 1 == me.tiles || i + 1 == n) {
+      // ---- the run ends here, or this CTA's part of it: join the four warps -----------------------
+      __syncwarp();                                   // the stage is read: it takes this warp's o
+      float* mine_o = reinterpret_cast<float*>(ring + stage * C::kStageB);
+      // FP8: o from units of 2^(u_run - 15) to those of the weights, 2^m_run
+      float frac[NQ][2];
+      int units[NQ][2];
+      if (C::kFp8) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float d = u_run[nq][e] == -INFINITY ? 0.f : u_run[nq][e] - m_run[nq][e];
+            const float whole = floorf(d);
+            frac[nq][e] = ex2(d - whole);
+            units[nq][e] = (int)whole - 15;
+          }
+      }
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float l = l_run[nq][e];
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
+          if (g == 0) {
+            sm_m[warp * 16 + nq * 8 + 2 * j + e] = m_run[nq][e];
+            sm_l[warp * 16 + nq * 8 + 2 * j + e] = l;
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int q = nq * 8 + 2 * j + (e & 1);
+            // rows of a fragment: values g and g + 8 (bf16), 2g and 2g + 1 (FP8)
+            const int d = mt * 16 + (C::kFp8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
+            float x = o[mt][nq][e];
+            if (C::kFp8) x = ldexpf(x * frac[nq][e & 1], units[nq][e & 1]);
+            mine_o[q * DP + (d ^ (((q >> 1) & 3) << 3))] = x;
+          }
+        }
+      }
+      __syncthreads();
+
+      const int run0 = total_first + i - me.tile;     // the run's first tile
+      const int c_first = run0 / per_cta, c_last = (run0 + me.tiles - 1) / per_cta;
+      const bool whole = c_first == c_last;
+      const int chunk = p.chunks == 1 ? 0 : me.hc % p.chunks;
+      const int h0 = (p.chunks == 1 ? me.hc : me.hc / p.chunks) * p.G + chunk * 8 * NQ;
+      const int q_heads = p.Hk * p.G;
+      const int slot_floats = 8 * NQ * (DP + 2);
+      // a CTA has at most two parts of cut runs: the one it starts in, and the one it ends in
+      const int slot = 2 * blockIdx.x + (run0 >= t0 && run0 != t0 ? 1 : 0);
+      float* part = p.part + (int64_t)slot * slot_floats;
+      auto emit = [&](int q, int d, const float (&x)[4], float m, float l) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint2 w;
+        w.x = pack_bf16(x[0] * inv, x[1] * inv);
+        w.y = pack_bf16(x[2] * inv, x[3] * inv);
+        *reinterpret_cast<uint2*>(p.out + (int64_t)me.seq * p.out_ts + (int64_t)(h0 + q) * p.out_hs + d) = w;
+        if (d == 0 && p.lse != nullptr)
+          p.lse[(int64_t)me.seq * q_heads + h0 + q] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+      };
+      for (int e = tid; e < rows * (DP / 4); e += kThreads) {
+        const int q = e / (DP / 4), d = (e % (DP / 4)) * 4;
+        if (d >= p.D) continue;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w * 16 + q]);
+        float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2_rel(sm_m[w * 16 + q], m);
+          l += sm_l[w * 16 + q] * f;
+          const float4 y = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + (w * kStages + stage) * C::kStageB) + q * DP + (d ^ (((q >> 1) & 3) << 3)));
+          x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
+        }
+        if (whole) {
+          emit(q, d, x, m, l);
+        } else {
+          __stcg(reinterpret_cast<float4*>(part + q * DP + d), make_float4(x[0], x[1], x[2], x[3]));
+          if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NQ * DP + 2 * q), make_float2(m, l));
+        }
+      }
+      if (!whole) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          const uint32_t arrived = atomicAdd(p.counters + c_first, 1u);
+          const int last = arrived == (uint32_t)(c_last - c_first);
+          if (last) p.counters[c_first] = 0;          // the next call finds it zero
+          __threadfence();
+          sm_i[11] = last;
+        }
+        __syncthreads();
+        if (sm_i[11]) {
+          // the first part lies in its CTA's second slot unless that CTA starts with the run
+          const float* base = p.part + (int64_t)2 * c_first * slot_floats;
+          const int lead = run0 != c_first * per_cta ? slot_floats : 0;
+          const int parts = c_last - c_first + 1;
+          for (int e = tid; e < rows * (DP / 4); e += kThreads) {
+            const int q = e / (DP / 4), d = (e % (DP / 4)) * 4;
+            if (d >= p.D) continue;
+            float m = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int c = 0; c < parts; ++c) {
+              const float* s = base + (int64_t)2 * c * slot_floats + (c == 0 ? lead : 0);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + 8 * NQ * DP + 2 * q));
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(s + q * DP + d));
+              const float mn = fmaxf(m, ml.x);
+              const float fo = ex2_rel(m, mn), fn = ex2_rel(ml.x, mn);
+              m = mn;
+              l = l * fo + ml.y * fn;
+              x[0] = x[0] * fo + y.x * fn; x[1] = x[1] * fo + y.y * fn;
+              x[2] = x[2] * fo + y.z * fn; x[3] = x[3] * fo + y.w * fn;
+            }
+            emit(q, d, x, m, l);
+          }
+        }
+      }
+      __syncthreads();                                // the stages and maxima are read: they may be refilled
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+
+  // ---- sequences with nothing to attend to -----------------------------------------------------
+  const int q_heads = p.Hk * p.G;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (clamp_len(__ldg(p.lens + b), p.cap) > 0) continue;
+    for (int e = tid; e < q_heads * (p.D / 4); e += kThreads) {
+      const int h = e / (p.D / 4), d = (e % (p.D / 4)) * 4;
+      *reinterpret_cast<uint2*>(p.out + (int64_t)b * p.out_ts + (int64_t)h * p.out_hs + d) = make_uint2(0, 0);
+      if (d == 0 && p.lse != nullptr) p.lse[(int64_t)b * q_heads + h] = -INFINITY;
+    }
+  }
+}
+
+template <typename C>
+cudaError_t launch(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
+  static PerContextOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemB);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t grid = max_tiles < plan.grid_max ? max_tiles : plan.grid_max;
+  return launch_k(attention_kernel<C>, dim3((unsigned)grid), dim3(kThreads), C::kSmemB, stream, pdl, p);
+}
+
+template <int DP, bool kFp8>
+cudaError_t launch_nq(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
+  if (plan.nq == 1)
+    return p.q.f32 ? launch<Cfg<DP, kFp8, 1, true>>(p, plan, max_tiles, stream, pdl)
+                   : launch<Cfg<DP, kFp8, 1, false>>(p, plan, max_tiles, stream, pdl);
+  return p.q.f32 ? launch<Cfg<DP, kFp8, 2, true>>(p, plan, max_tiles, stream, pdl)
+                 : launch<Cfg<DP, kFp8, 2, false>>(p, plan, max_tiles, stream, pdl);
+}
+
+template <bool kFp8>
+cudaError_t launch_any(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
+  return p.D <= 64    ? launch_nq<64, kFp8>(p, plan, max_tiles, stream, pdl)
+         : p.D <= 128 ? launch_nq<128, kFp8>(p, plan, max_tiles, stream, pdl)
+                      : launch_nq<256, kFp8>(p, plan, max_tiles, stream, pdl);
+}
+
+}  // namespace attn
+}  // namespace engram

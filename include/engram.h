@@ -24,7 +24,7 @@
  *   - Data-dependent faults found on the device (an id outside its range) never trap: the
  *     kernel substitutes the documented value and ORs a bit into the caller's `err_flag`
  *     word (device int32, may be NULL to skip reporting). The caller reads it when it likes.
- *   - T == 0 is a no-op that returns ENGRAM_OK.
+ *   - T == 0 (for the attention calls also B == 0) is a no-op that returns ENGRAM_OK.
  */
 #ifndef ENGRAM_H_
 #define ENGRAM_H_
@@ -45,6 +45,10 @@ extern "C" {
 #define ENGRAM_ERR_RAW_ID 1        /* raw input id outside [0, raw_vocab): used pad_id */
 #define ENGRAM_ERR_ROW_ID 2        /* row id outside [0, num_rows): wrote a zero row */
 #define ENGRAM_ERR_PIPE_TIMEOUT 4  /* a pipeline wait (GEMM, gate) ran past its time limit */
+#define ENGRAM_ERR_SLOT 8          /* cache slot past the cache: not written, read as zeros */
+#define ENGRAM_ERR_PAGE 16         /* page number outside [0, num_pages): its keys are not attended */
+#define ENGRAM_ERR_POSITION 32     /* position outside the rotation table: the nearest row was used */
+#define ENGRAM_ERR_SEQ_LEN 64      /* sequence length below 0 or past its page table: clamped */
 
 typedef void* engram_stream_t; /* a cudaStream_t */
 
@@ -90,8 +94,9 @@ const char* engram_version(void);
  *   ENGRAM_OK     the word is 0;
  *   ENGRAM_EDATA  (-3) a data-dependent bit is set: ENGRAM_ERR_RAW_ID (a raw input id outside the
  *                 token map, hashed as pad_id, as [NeMo] DeepseekV41NgramHash.forward pads what it
- *                 cannot look back at) or ENGRAM_ERR_ROW_ID (a row id outside the table, read as a
- *                 zero row, as [vLLM] _engram_lookup_kernel reads the rows a rank does not own).
+ *                 cannot look back at), ENGRAM_ERR_ROW_ID (a row id outside the table, read as a
+ *                 zero row, as [vLLM] _engram_lookup_kernel reads the rows a rank does not own), or
+ *                 one of the attention calls' bits (ENGRAM_ERR_SLOT, _PAGE, _POSITION, _SEQ_LEN).
  *                 The results are defined; the inputs were not what the model expects;
  *   ENGRAM_ECUDA  (-2) ENGRAM_ERR_PIPE_TIMEOUT is set (the results are invalid), or a CUDA call
  *                 failed, including an error left by earlier asynchronous work on the stream.
@@ -435,6 +440,154 @@ int engram_forward_noalloc(const EngramDims* dims, const EngramHashTables* table
                            const EngramLayerWeights* layers, const EngramTokens* tokens,
                            float* const* streams, int32_t* out_ids, int32_t* err_flag,
                            engram_stream_t stream);
+
+/*
+ * ---- Attention of a decoder layer over a paged key-value cache --------------------------------
+ *
+ * The operators that stand next to an Engram layer when its model is served (no page counterpart;
+ * the formulas are stated at each call): per-head norms of queries and keys with the position
+ * rotation, rows written to a paged cache (bf16, or the FP8 tables' own format) and read back, and
+ * attention of one new token per sequence over that cache. Inference only.
+ */
+
+/* Value types of rows of heads. */
+enum EngramValueType { ENGRAM_BF16 = 0, ENGRAM_F32 = 1 };
+
+/* Formats of a cache's rows. */
+enum EngramCacheFmt {
+  ENGRAM_CACHE_BF16 = 0,     /* bf16 [head_dim]; head_dim % 16 == 0 */
+  ENGRAM_CACHE_FP8_E8M0 = 1  /* e4m3 codes [head_dim] + one E8M0 byte per 32 values, in ceil(head_dim/128)
+                                32-bit words (unused bytes are ignored); head_dim % 32 == 0 */
+};
+
+/* Rows of heads in caller memory: value (t, h, d) at data + t*token_stride + h*head_stride + d, the
+ * strides in values. data and both strides are multiples of 16 bytes (head_dim is one of 8 values).
+ * Outputs must not overlap themselves; an output may be its input (same data, type and strides). */
+typedef struct EngramHeads {
+  void* data;                /* device */
+  int64_t token_stride, head_stride;
+  int32_t heads;
+  int32_t type;              /* EngramValueType */
+} EngramHeads;
+
+/*
+ * A paged cache of keys and values. Slot s is place s % page_size of page s / page_size. The row of
+ * (page, head, place) is at k (or v) + page*page_stride + head*head_stride + place*token_stride, strides
+ * in values (bf16 or codes), the same for k and v; its scale words likewise with the scale strides in
+ * bytes. Any order of the axes, any padding: k, v and the strides are multiples of 16 bytes, scales and
+ * their strides multiples of 4. Offsets are 64-bit.
+ */
+typedef struct EngramKVCache {
+  int32_t format;            /* EngramCacheFmt */
+  int32_t kv_heads, head_dim, page_size;   /* head_dim <= 256 */
+  int64_t num_pages;
+  void *k, *v;               /* device */
+  int64_t page_stride, head_stride, token_stride;
+  uint8_t *k_scales, *v_scales;            /* device, FP8_E8M0 only */
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+} EngramKVCache;
+
+/*
+ * Norm and rotation of query and key rows x of head_dim D:
+ *     y = x / sqrt(mean(x^2) + eps) * w            (w = q_weight or k_weight, bf16 [D])
+ * then pairs (a, b) of y[rope_start .. rope_start + rope_dim) are turned by their position's angle i:
+ *     a' = a cos_i - b sin_i,  b' = b cos_i + a sin_i
+ * with (a, b) = values i and i + rope_dim/2 of that part, or 2i and 2i + 1 (interleaved != 0).
+ *   q_weight, k_weight  device, 16-byte aligned, both or neither (NULL: no norm)
+ *   table               device fp32 [table_rows, rope_dim], 16-byte aligned: a position's rope_dim/2
+ *                       cosines, then its sines. rope_dim 0: no rotation (table is not read)
+ * rope_start % 8 == 0; rope_dim % 16 == 0 (interleaved: % 8); rope_start + rope_dim <= D.
+ */
+typedef struct EngramNormRope {
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const float* table;
+  int64_t table_rows;
+  int32_t rope_dim, rope_start, interleaved;
+} EngramNormRope;
+
+/*
+ * Norm and rotation of T tokens' query and key rows, in one pass and one launch; fp32 inside, rounded
+ * once to the outputs' type.
+ *   q, k          rows [T, heads, head_dim] of one type; either may be NULL (with its output)
+ *   q_out, k_out  as q and k, of either type; in place is fine
+ *   positions     device int32 [T]; outside [0, table_rows): nearest row, ENGRAM_ERR_POSITION. May be
+ *                 NULL when rope_dim is 0
+ * head_dim % 8 == 0, 8 <= head_dim <= 256.
+ */
+int engram_qk_norm_rope(const EngramNormRope* nr, int64_t T, int32_t head_dim, const EngramHeads* q,
+                        const EngramHeads* k, const int32_t* positions, const EngramHeads* q_out,
+                        const EngramHeads* k_out, int32_t* err_flag, engram_stream_t stream);
+
+/*
+ * Key and value rows [T, kv_heads, head_dim] of one type to their slots of the cache. bf16: rounded to
+ * nearest even. FP8_E8M0: per 32 values the scale is the smallest power of two 2^e >= 2^-126 with
+ * max|x| / 2^e <= 448 (byte 127 + e; 127 for an all-zero block) and each code is x / 2^e rounded to the
+ * nearest e4m3 value, ties to even. NaN stays NaN; an infinity reads back as infinite (and the finite
+ * values of its block as zero).
+ *   slots  device int64 [T]: < 0 is skipped; past the cache is skipped and sets ENGRAM_ERR_SLOT. Two
+ *          tokens with one slot leave one of the rows (which one is not defined)
+ */
+int engram_kv_write(const EngramKVCache* cache, int64_t T, const EngramHeads* k, const EngramHeads* v,
+                    const int64_t* slots, int32_t* err_flag, engram_stream_t stream);
+
+/*
+ * The rows at T slots, dequantised: code * float(bits = scale_byte << 23), rounded once to the output's
+ * type (bf16 holds every e4m3 code times a power of two in its range exactly).
+ *   slots         device int64 [T]: < 0 gives zero rows; past the cache too, and sets ENGRAM_ERR_SLOT
+ *   k_out, v_out  rows [T, kv_heads, head_dim], either type
+ */
+int engram_kv_read(const EngramKVCache* cache, int64_t T, const int64_t* slots, const EngramHeads* k_out,
+                   const EngramHeads* v_out, int32_t* err_flag, engram_stream_t stream);
+
+/* One step's sequences: their page numbers and lengths (with the new token). Device memory. */
+typedef struct EngramPagedSeqs {
+  int32_t batch;              /* B, sequences */
+  const int32_t* block_table; /* [B, width]: page of tokens [i*page_size, (i+1)*page_size) of a sequence */
+  int64_t table_stride;       /* entries from one sequence's row to the next */
+  int32_t table_width;
+  const int32_t* seq_lens;    /* [B] */
+} EngramPagedSeqs;
+
+/* Workspace bytes of engram_paged_attention and engram_attention_step for q_heads query heads over this
+ * cache on the current device; for any batch up to `batch` and any lengths. 0 on bad sizes. */
+size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int32_t batch);
+
+/*
+ * Attention of one new token per sequence over its cached tokens. Query head h reads key head
+ * h / (q_heads / kv_heads). Over the tokens j in [max(0, len - window), len) (window 0: [0, len)):
+ *     s_j = scale * <q_h, k_j>,  out_h = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse_h = log sum_j exp(s_j)
+ * A sequence with no tokens, or whose scores are all -inf, gives zeros and lse -inf. What lies in the
+ * cache outside the attended tokens is not read into the result, whatever it holds.
+ *   q          rows [B, q_heads, head_dim], bf16 or fp32; q_heads a multiple of kv_heads
+ *   seqs       lengths outside [0, table_width * page_size] are clamped (ENGRAM_ERR_SEQ_LEN); a page
+ *              number outside the cache hides its tokens (ENGRAM_ERR_PAGE)
+ *   out        bf16 rows [B, q_heads, head_dim]       lse  device fp32 [B, q_heads], or NULL
+ *   workspace  device, 256-byte aligned, engram_attention_workspace_bytes. Its first 4096 bytes must
+ *              be zero before the first use; every call leaves them zero. Calls that may overlap need
+ *              workspaces of their own; calls in order may share one, whatever their shapes.
+ * Products take 16-bit operands with fp32 accumulation; scores, sums and lse are fp32. The work is cut
+ * evenly over the GPU at token granularity and joined in the order of the tokens: results do not depend
+ * on timing. One launch.
+ */
+int engram_paged_attention(const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q,
+                           float scale, int32_t window, const EngramHeads* out, float* lse, void* workspace,
+                           size_t ws_bytes, int32_t* err_flag, engram_stream_t stream);
+
+/*
+ * One decode step of a layer: norm and rotation of the new tokens' queries and keys, their keys and
+ * values written to the cache, attention over the cache (the new token included when seq_lens counts
+ * it). Two launches, chained with programmatic dependent launch; the turned queries stay in the
+ * workspace, in fp32. Equal to engram_qk_norm_rope with fp32 outputs, engram_kv_write and
+ * engram_paged_attention one after another, bit for bit.
+ *   q          rows [B, q_heads, head_dim]; k, v rows [B, kv_heads, head_dim]; one type for all three
+ *   positions  device int32 [B]       slots  device int64 [B]
+ */
+int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs,
+                          const EngramHeads* q, const EngramHeads* k, const EngramHeads* v,
+                          const int32_t* positions, const int64_t* slots, float scale, int32_t window,
+                          const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes,
+                          int32_t* err_flag, engram_stream_t stream);
 
 #ifdef __cplusplus
 }
