@@ -21,6 +21,7 @@ import torch
 from .binding import _check, _ptr, _shape, _stream, lib
 
 CACHE_BF16, CACHE_FP8_E8M0 = 0, 1
+ATTENTION_ZERO_BYTES = 16384   # ENGRAM_ATTENTION_ZERO_BYTES
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
@@ -242,13 +243,14 @@ def attention_workspace_bytes(cache: KVCache, q_heads: int, batch: int) -> int:
 
 
 def attention_workspace(cache: KVCache, q_heads: int, batch: int) -> torch.Tensor:
-    """A workspace of the attention calls on this cache for up to `batch` sequences. Its first 4096 bytes
-    are zero, and every call leaves them so: a program keeps one for calls that run in order."""
+    """A workspace of the attention calls on this cache for up to `batch` sequences. Its start
+    (ATTENTION_ZERO_BYTES) is zero, and every call leaves it so: a program keeps one for calls that run in
+    order."""
     n = attention_workspace_bytes(cache, q_heads, batch)
     if n == 0:
         raise ValueError(f"no workspace for {q_heads} query heads over {cache.kv_heads} key heads of {cache.head_dim}")
     ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-    ws[:4096].zero_()
+    ws[:ATTENTION_ZERO_BYTES].zero_()
     return ws
 
 

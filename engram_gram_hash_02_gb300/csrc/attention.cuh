@@ -41,14 +41,18 @@ namespace attn {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kGroup = 16;                            // parts of a cut run that one CTA joins
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes to shared memory, or 16 zero bytes (nothing is read then)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -103,23 +107,26 @@ struct Cfg {
   static constexpr int kQB = NQ * 8 * kQPitch * 2;    // per part (high, low)
   static constexpr int kMetaB = kWarps * kStages * 32;
   static constexpr int kSmall = 1024;                 // maxima, sums, query scales, scan words
-  static constexpr int kSmemB = kRingB + kQB * (kSplit ? 2 : 1) + kMetaB + kSmall;
+  static constexpr int kAlign = 512;                  // a row's XORed bits are zero in its stage's address
+  static constexpr int kSmemB = kAlign + kRingB + kQB * (kSplit ? 2 : 1) + kMetaB + kSmall;
   static constexpr bool kQRegs = DP / 16 * 2 * NQ * (kSplit ? 2 : 1) <= 32;
   static_assert(NQ * 8 * DP * 4 <= kStageB, "a warp's result is joined in its own last stage");
+  static_assert(kStageB % (kRowB < kAlign ? kRowB : kAlign) == 0, "stages keep the rows' alignment");
 };
 
-// byte offset of 16-byte chunk c of row r: eight rows at one chunk lie in eight different bank groups
+// Rows lie in a stage one after another; 16-byte chunk c of row r is at place c ^ key(r), so that eight rows
+// at one chunk fall into eight different bank groups. key(r) as a byte offset:
 template <int kRowB>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  if (kRowB >= 128) return (uint32_t)(r * kRowB + ((c ^ (r & 7)) << 4));
-  return (uint32_t)(r * kRowB + ((c ^ ((r >> 1) & 3)) << 4));   // 64-byte rows
+__host__ __device__ constexpr uint32_t swz(int r) {
+  return (uint32_t)(kRowB >= 128 ? (r & 7) << 4 : ((r >> 1) & 3) << 4);
 }
 
 // what a warp knows of one step when it consumes it
 struct Meta {
   uint32_t mask;               // keys of the step that are attended
+  uint32_t ends;               // bit 0: first tile of its run, bit 1: last
   int32_t seq, hc, tile, tiles;// sequence, head * chunks + chunk, tile of the run and tiles it has
-  int32_t pad[3];
+  int32_t pad[2];
 };
 
 __device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : len > cap ? cap : len; }
@@ -128,7 +135,8 @@ __device__ __forceinline__ int attended(int len, int window) { return window > 0
 template <typename C>
 __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const AttnParams p) {
   constexpr int DP = C::DP, NQ = C::NQ, kStages = C::kStages, kStep = C::kStep, kRowB = C::kRowB;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & (C::kAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, j = lane & 3;             // fragment row and column pair
   uint8_t* ring = smem + warp * kStages * C::kStageB;
@@ -184,6 +192,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 
   // ---- the producer's place: step i is tile t0 + i ----------------------------------------------
   int seq = sm_i[8], hc = sm_i[9], tile = sm_i[10], first = 0, end = 0, tiles = 0;
+  int64_t head_off = 0, shead_off = 0;
+  auto enter_head = [&] {
+    const int head = p.chunks == 1 ? hc : hc / p.chunks;
+    head_off = head * p.cache.head_b;
+    if (C::kFp8) shead_off = head * p.cache.shead_b;
+  };
   auto enter = [&] {                                  // seq is new
     const int len = clamp_len(__ldg(p.lens + seq), p.cap);
     const int n = attended(len, p.window);
@@ -194,12 +208,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   auto advance = [&] {
     if (++tile < tiles) return;
     tile = 0;
-    if (++hc < heads) return;
-    hc = 0;
-    do {
-      if (++seq >= p.B) return;                       // past the last tile: never fetched
-      enter();
-    } while (tiles == 0);
+    if (++hc == heads) {
+      hc = 0;
+      do {
+        if (++seq >= p.B) return;                     // past the last tile: never fetched
+        enter();
+      } while (tiles == 0);
+    }
+    enter_head();
   };
   // the page of this lane's row, requested one step before its copies
   int page = -1, at = 0;
@@ -214,48 +230,89 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       page = __ldg(p.table + (int64_t)seq * p.table_stride + n);
     }
   };
+  // a lane copies chunk c of rows sub, sub + kRows, ...
+  constexpr int kChunks = kRowB / 16, kRows = 32 / kChunks;
+  const int c = lane & (kChunks - 1), sub = lane / kChunks;
+  const bool in_row = c * 16 < (C::kFp8 ? p.D : 2 * p.D);
+  const uint32_t lane_dst = (uint32_t)(sub * kRowB) + ((uint32_t)(c << 4) ^ swz<kRowB>(sub));
+  const uint32_t ring_u = smem_u32(ring);
   auto issue = [&](int stage) {
     const bool live = inside && page >= 0 && page < p.cache.num_pages;
     if (inside && !live && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
-    uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
-    if (kStep == 16) mask &= 0xFFFFu;
+    constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live) & kAll;
     if (lane == 0) {
       Meta m;
-      m.mask = mask; m.seq = seq; m.hc = hc; m.tile = tile; m.tiles = tiles;
+      m.mask = mask; m.ends = (tile == 0 ? 1u : 0u) | (tile + 1 == tiles ? 2u : 0u);
+      m.seq = seq; m.hc = hc; m.tile = tile; m.tiles = tiles;
       meta[stage] = m;
     }
     if (mask == 0) return;                            // no keys for this warp: the stage is not read
-    const int head = p.chunks == 1 ? hc : hc / p.chunks;
-    const int64_t off = live ? page * p.cache.page_b + head * p.cache.head_b + at * p.cache.tok_b : 0;
-    const uint32_t dst = smem_u32(ring + stage * C::kStageB);
-    constexpr int kChunks = kRowB / 16, kRows = 32 / kChunks;   // 16-byte chunks of a row, rows per pass
-    const int c = lane & (kChunks - 1), sub = lane / kChunks;
-    const bool in_row = c * 16 < (C::kFp8 ? p.D : 2 * p.D);
-#pragma unroll
-    for (int r0 = 0; r0 < kStep; r0 += kRows) {
-      const int r = r0 + sub;
-      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + c * 16;
-      const bool row_live = (mask >> r) & 1u;
+    const uint32_t dst = ring_u + stage * C::kStageB;
+    const uint32_t to = dst + lane_dst;
+    const int64_t off = live ? page * p.cache.page_b + at * p.cache.tok_b + head_off : 0;
+    // all rows attended and in one page: equal steps from the first one
+    const int at0 = __shfl_sync(0xFFFFFFFFu, at, 0);
+    if (mask == kAll && at0 + kStep <= p.cache.page_size) {
+      const uint8_t* kp = p.cache.k + (__shfl_sync(0xFFFFFFFFu, off, 0) + sub * p.cache.tok_b + c * 16);
+      const uint8_t* vp = kp + (p.cache.v - p.cache.k);
       if (in_row) {
-        cp_async16(dst + swz<kRowB>(r, c), p.cache.k + o, row_live);
-        cp_async16(dst + kStep * kRowB + swz<kRowB>(r, c), p.cache.v + o, row_live);
+        if (p.cache.tok_b == kRowB) {                 // the steps are immediates
+#pragma unroll
+          for (int r0 = 0; r0 < kStep; r0 += kRows) {
+            cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp + r0 * kRowB);
+            cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp + r0 * kRowB);
+          }
+        } else {
+          const int64_t step = kRows * p.cache.tok_b;
+#pragma unroll
+          for (int r0 = 0; r0 < kStep; r0 += kRows) {
+            cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp);
+            cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp);
+            kp += step;
+            vp += step;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r0 = 0; r0 < kStep; r0 += kRows) {
+        const int r = r0 + sub;
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + c * 16;
+        const bool row_live = (mask >> r) & 1u;
+        if (in_row) {
+          cp_async16_or_zero((to ^ swz<kRowB>(r0)) + r0 * kRowB, p.cache.k + o, row_live);
+          cp_async16_or_zero((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, p.cache.v + o, row_live);
+        }
       }
     }
-    if (C::kFp8) {
-      const int64_t so = live ? page * p.cache.spage_b + head * p.cache.shead_b + at * p.cache.stok_b : 0;
+    if (C::kFp8 && lane < kStep) {
+      const int64_t so = live ? page * p.cache.spage_b + at * p.cache.stok_b + shead_off : 0;
       const uint32_t sd = dst + 2 * kStep * kRowB + lane * C::kWords * 4;
 #pragma unroll
       for (int w = 0; w < C::kWords; ++w) {
-        cp_async4(sd + 4 * w, p.cache.ks + so + 4 * w, live);
-        cp_async4(sd + kStep * C::kWords * 4 + 4 * w, p.cache.vs + so + 4 * w, live);
+        cp_async4_or_zero(sd + 4 * w, p.cache.ks + so + 4 * w, live);
+        cp_async4_or_zero(sd + kStep * C::kWords * 4 + 4 * w, p.cache.vs + so + 4 * w, live);
       }
     }
   };
+  // rows narrower than DP: the products run over their pad, which is zero in every stage
+  auto clear_pad = [&](int stage) {
+    for (int r = sub; r < 2 * kStep; r += kRows)
+      if (!in_row) *reinterpret_cast<uint4*>(ring + stage * C::kStageB + r * kRowB + ((uint32_t)(c << 4) ^ swz<kRowB>(r))) = make_uint4(0, 0, 0, 0);
+  };
+  const bool padded = p.D < DP;
+  const uint32_t scale_bytes = p.D % 128 == 0 ? 0xFFFFFFFFu : (1u << (8 * (p.D % 128 / 32))) - 1u;   // of the last word
 
   const int n = t1 - t0;
   int ahead = 0;                                      // steps requested so far
   if (n > 0) {
+    if (padded) {
+      for (int s = 0; s < kStages; ++s) clear_pad(s);
+      __syncwarp();
+    }
     enter();
+    enter_head();
     request();
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
@@ -274,7 +331,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   float u_run[NQ][2];                                 // FP8: running maximum of s + e, the units of o
   uint32_t qf[C::kQRegs ? NQ : 1][C::kQRegs ? DP / 16 : 1][C::kSplit ? 4 : 2];
   int rows = 0;                                       // query heads of this run
-  const int total_first = t0;
 
   auto q_frag = [&](int nq, int ks, uint32_t (&b)[4]) {
     const uint8_t* row = qs + ((nq * 8 + g) * C::kQPitch + ks * 16) * 2;
@@ -299,10 +355,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   for (int i = 0; i < n; ++i) {
     cp_async_wait<kStages - 2>();
     __syncwarp();
-    const Meta me = meta[stage];
+    const uint32_t mask = meta[stage].mask, ends = meta[stage].ends;
 
-    if (i == 0 || me.tile == 0) {
+    if (i == 0 || (ends & 1u)) {
       // a new run: its query rows to shared memory (16-bit, zero rows and columns as padding)
+      const Meta me = meta[stage];
       const int chunk = p.chunks == 1 ? 0 : me.hc % p.chunks;
       const int head = p.chunks == 1 ? me.hc : me.hc / p.chunks;
       rows = min(8 * NQ, p.G - chunk * 8 * NQ);
@@ -381,9 +438,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     }
     cp_async_commit();
 
-    if (me.mask != 0) {
-      const uint32_t ks_addr = smem_u32(ring + stage * C::kStageB);
-      const uint32_t vs_addr = ks_addr + kStep * kRowB;
+    if (mask != 0) {
+      // this lane's row and chunk of every ldmatrix: rows 0..7 and 8..15, chunks 2x and 2x + 1
+      constexpr int kHi = C::kFp8 ? 4 : 3, kRow8 = C::kFp8 ? 3 : 4;
+      const int lrow = ((lane >> kRow8) & 1) * 8 + (lane & 7);
+      const uint32_t tiles_u = (ring_u + stage * C::kStageB + lrow * kRowB) + ((((lane >> kHi) & 1) << 4) ^ swz<kRowB>(lrow));
       constexpr int KT = kStep / 16;
       uint32_t pb[KT][NQ][C::kFp8 ? 2 : 4];            // P as the second product's operand (bf16: high, low)
       float t[KT][NQ][4];
@@ -393,13 +452,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       // S^T = K Q^T
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const int row = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
         if (C::kFp8) {
           uint32_t w0[C::kWords], w1[C::kWords];
 #pragma unroll
           for (int w = 0; w < C::kWords; ++w) {
-            w0[w] = kw[(kt * 16 + g) * C::kWords + w];
-            w1[w] = kw[(kt * 16 + g + 8) * C::kWords + w];
+            w0[w] = kw[(kt * 16 + g) * C::kWords + w] & (w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
+            w1[w] = kw[(kt * 16 + g + 8) * C::kWords + w] & (w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
           }
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
@@ -407,17 +465,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             for (int e = 0; e < 4; ++e) t[kt][nq][e] = 0.f;
 #pragma unroll
           for (int b = 0; b < DP / 32; ++b) {
-            if (b * 32 >= p.D) break;
             uint32_t a[4];                             // codes: keys g, g + 8 (values 0..15), g, g + 8 (16..31)
-            ldsm4(a, ks_addr + swz<kRowB>(row, 2 * b + (lane >> 4)));
+            ldsm4(a, (tiles_u ^ (b << 5)) + kt * 16 * kRowB);
             const float s0 = __uint_as_float(((w0[b / 4] >> (8 * (b & 3))) & 0xFFu) << 23);
             const float s1 = __uint_as_float(((w1[b / 4] >> (8 * (b & 3))) & 0xFFu) << 23);
             uint32_t f[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[2 * e] = e4m3x2_to_f16x2(a[e] & 0xFFFFu);
-              f[2 * e + 1] = e4m3x2_to_f16x2(a[e] >> 16);
-            }
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2(a[e], f[2 * e], f[2 * e + 1]);
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
               float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -447,9 +501,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             for (int e = 0; e < 4; ++e) acc[nq][0][e] = acc[nq][1][e] = 0.f;
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks) {
-            if (ks * 16 >= p.D) break;
-            uint32_t a[4];
-            ldsm4(a, ks_addr + swz<kRowB>(row, 2 * ks + (lane >> 4)));
+            uint32_t a[4];                             // keys 0..7 (values 0..7, 8..15), keys 8..15
+            ldsm4(a, tiles_u ^ (ks << 5));
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
               uint32_t q4[4];
@@ -459,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
               } else {
                 q_frag(nq, ks, q4);
               }
-              mma<false>(acc[nq][ks & 1], a[0], a[1], a[2], a[3], q4[0], q4[1]);
-              if (C::kSplit) mma<false>(acc[nq][ks & 1], a[0], a[1], a[2], a[3], q4[2], q4[3]);
+              mma<false>(acc[nq][ks & 1], a[0], a[2], a[1], a[3], q4[0], q4[1]);
+              if (C::kSplit) mma<false>(acc[nq][ks & 1], a[0], a[2], a[1], a[3], q4[2], q4[3]);
             }
           }
 #pragma unroll
@@ -479,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         int top = 0;
 #pragma unroll
         for (int b = 0; b < DP / 32; ++b) {
-          if ((b & 3) == 0) w[b / 4] = vw[lane * C::kWords + b / 4];
+          if ((b & 3) == 0) w[b / 4] = vw[lane * C::kWords + b / 4] & (b / 4 + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
           const int by = (int)((w[b / 4] >> (8 * (b & 3))) & 0xFFu);
-          if (b * 32 < p.D && by < 254) top = max(top, by);
+          if (by < 254) top = max(top, by);
         }
         e_own = (float)(top - 127);
 #pragma unroll
@@ -511,12 +564,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         const float c1 = C::kFp8 ? sm_c[nq * 8 + 2 * j + 1] : p.scale_log2;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-          const bool v0 = (me.mask >> (kt * 16 + g)) & 1u, v1 = (me.mask >> (kt * 16 + g + 8)) & 1u;
           float(&x)[4] = t[kt][nq];
-          x[0] = v0 ? x[0] * c0 : -INFINITY;
-          x[1] = v0 ? x[1] * c1 : -INFINITY;
-          x[2] = v1 ? x[2] * c0 : -INFINITY;
-          x[3] = v1 ? x[3] * c1 : -INFINITY;
+          x[0] *= c0; x[1] *= c1; x[2] *= c0; x[3] *= c1;
+          if (mask != (kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+            if (!((mask >> (kt * 16 + g)) & 1u)) x[0] = x[1] = -INFINITY;
+            if (!((mask >> (kt * 16 + g + 8)) & 1u)) x[2] = x[3] = -INFINITY;
+          }
           mx[0] = fmaxf(mx[0], fmaxf(x[0], x[2]));
           mx[1] = fmaxf(mx[1], fmaxf(x[1], x[3]));
           if (C::kFp8) {
@@ -595,7 +648,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         if (C::kFp8) {
-          const int row = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
           uint32_t s0[2][2 * C::kWords], s1[2][2 * C::kWords];   // block scales of keys 2j, 2j + 1 (+ 0 and + 8)
 #pragma unroll
           for (int x = 0; x < 2 * C::kWords; ++x) {
@@ -606,17 +658,15 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
           }
 #pragma unroll
           for (int b = 0; b < DP / 32; ++b) {
-            if (b * 32 >= p.D) break;
             uint32_t a[4];                             // pairs of values: keys 0..7, 8..15 (values 0..15), the same of 16..31
-            ldsm4t(a, vs_addr + swz<kRowB>(row, 2 * b + (lane >> 4)));
+            ldsm4t(a, (tiles_u ^ (b << 5)) + (kStep + kt * 16) * kRowB);
             const uint32_t y0 = __byte_perm(s0[0][b / 2], s0[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
             const uint32_t y1 = __byte_perm(s1[0][b / 2], s1[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
             uint32_t f[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t x = __byte_perm(a[e], 0u, 0x3120);   // (value 2g of both keys, value 2g + 1 of both)
-              f[2 * e] = e4m3x2_to_f16x2(x & 0xFFFFu);
-              f[2 * e + 1] = e4m3x2_to_f16x2(x >> 16);
+              // (value 2g of both keys, value 2g + 1 of both)
+              e4m3x4_to_f16x2(__byte_perm(a[e], 0u, 0x3120), f[2 * e], f[2 * e + 1]);
             }
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
@@ -628,12 +678,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             }
           }
         } else {
-          const int row = kt * 16 + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
           for (int mt = 0; mt < DP / 16; ++mt) {
-            if (mt * 16 >= p.D) break;
-            uint32_t a[4];
-            ldsm4t(a, vs_addr + swz<kRowB>(row, 2 * mt + ((lane >> 3) & 1)));
+            uint32_t a[4];                             // values 0..7, 8..15 (keys 0..7), the same of keys 8..15
+            ldsm4t(a, (tiles_u ^ (mt << 5)) + kStep * kRowB);
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
               mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[kt][nq][0], pb[kt][nq][1]);
@@ -644,8 +692,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       }
     }
 
-    if (me.tile + 1 == me.tiles || i + 1 == n) {
+    if ((ends & 2u) || i + 1 == n) {
       // ---- the run ends here, or this CTA's part of it: join the four warps -----------------------
+      const Meta me = meta[stage];
       __syncwarp();                                   // the stage is read: it takes this warp's o
       float* mine_o = reinterpret_cast<float*>(ring + stage * C::kStageB);
       // FP8: o from units of 2^(u_run - 15) to those of the weights, 2^m_run
@@ -689,16 +738,15 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       }
       __syncthreads();
 
-      const int run0 = total_first + i - me.tile;     // the run's first tile
+      const int run0 = t0 + i - me.tile;              // the run's first tile
       const int c_first = run0 / per_cta, c_last = (run0 + me.tiles - 1) / per_cta;
       const bool whole = c_first == c_last;
       const int chunk = p.chunks == 1 ? 0 : me.hc % p.chunks;
       const int h0 = (p.chunks == 1 ? me.hc : me.hc / p.chunks) * p.G + chunk * 8 * NQ;
       const int q_heads = p.Hk * p.G;
-      const int slot_floats = 8 * NQ * (DP + 2);
-      // a CTA has at most two parts of cut runs: the one it starts in, and the one it ends in
-      const int slot = 2 * blockIdx.x + (run0 >= t0 && run0 != t0 ? 1 : 0);
-      float* part = p.part + (int64_t)slot * slot_floats;
+      constexpr int kSlot = 8 * NQ * (DP + 2);        // floats of a part: o, then (maximum, sum) per head
+      // a CTA has at most two parts of cut runs: slot 0 for the one it starts in, slot 1 for the one it ends in
+      auto slot_of = [&](int cta) { return p.part + (int64_t)(2 * cta + (cta == c_first && run0 != cta * per_cta ? 1 : 0)) * kSlot; };
       auto emit = [&](int q, int d, const float (&x)[4], float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint2 w;
@@ -707,6 +755,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         *reinterpret_cast<uint2*>(p.out + (int64_t)me.seq * p.out_ts + (int64_t)(h0 + q) * p.out_hs + d) = w;
         if (d == 0 && p.lse != nullptr)
           p.lse[(int64_t)me.seq * q_heads + h0 + q] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+      };
+      auto put = [&](float* part, int q, int d, const float (&x)[4], float m, float l) {
+        __stcg(reinterpret_cast<float4*>(part + q * DP + d), make_float4(x[0], x[1], x[2], x[3]));
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NQ * DP + 2 * q), make_float2(m, l));
       };
       for (int e = tid; e < rows * (DP / 4); e += kThreads) {
         const int q = e / (DP / 4), d = (e % (DP / 4)) * 4;
@@ -723,50 +775,89 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
               reinterpret_cast<const float*>(smem + (w * kStages + stage) * C::kStageB) + q * DP + (d ^ (((q >> 1) & 3) << 3)));
           x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
         }
-        if (whole) {
+        if (whole)
           emit(q, d, x, m, l);
-        } else {
-          __stcg(reinterpret_cast<float4*>(part + q * DP + d), make_float4(x[0], x[1], x[2], x[3]));
-          if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NQ * DP + 2 * q), make_float2(m, l));
-        }
+        else
+          put(slot_of(blockIdx.x), q, d, x, m, l);
       }
       if (!whole) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const uint32_t arrived = atomicAdd(p.counters + c_first, 1u);
-          const int last = arrived == (uint32_t)(c_last - c_first);
-          if (last) p.counters[c_first] = 0;          // the next call finds it zero
+        // The last CTA to arrive of each group of kGroup joins the group's parts into the group's first slot,
+        // the last group to be joined joins the groups: 2 * sqrt(parts) reads in a row instead of all of them
+        // through one SM. A counter belongs to its group by the group's first CTA; a run's first group may
+        // share that CTA with the end of another run, so it has an array of its own.
+        auto arrive_last = [&](uint32_t* counter, int parties) {
           __threadfence();
-          sm_i[11] = last;
-        }
-        __syncthreads();
-        if (sm_i[11]) {
-          // the first part lies in its CTA's second slot unless that CTA starts with the run
-          const float* base = p.part + (int64_t)2 * c_first * slot_floats;
-          const int lead = run0 != c_first * per_cta ? slot_floats : 0;
-          const int parts = c_last - c_first + 1;
-          for (int e = tid; e < rows * (DP / 4); e += kThreads) {
+          __syncthreads();
+          if (tid == 0) {
+            const int last = atomicAdd(counter, 1u) == (uint32_t)(parties - 1);
+            if (last) *counter = 0;                   // the next call finds it zero
+            __threadfence();
+            sm_i[11] = last;
+          }
+          __syncthreads();
+          return sm_i[11] != 0;
+        };
+        auto join = [&](int from, int step, int parts, bool final) {
+          for (int e0 = 0; e0 < rows * (DP / 4); e0 += kThreads) {
+            const int e = e0 + tid;
             const int q = e / (DP / 4), d = (e % (DP / 4)) * 4;
-            if (d >= p.D) continue;
+            const bool mine = e < rows * (DP / 4) && d < p.D;
             float m = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (int c = 0; c < parts; ++c) {
-              const float* s = base + (int64_t)2 * c * slot_floats + (c == 0 ? lead : 0);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + 8 * NQ * DP + 2 * q));
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(s + q * DP + d));
-              const float mn = fmaxf(m, ml.x);
-              const float fo = ex2_rel(m, mn), fn = ex2_rel(ml.x, mn);
-              m = mn;
-              l = l * fo + ml.y * fn;
-              x[0] = x[0] * fo + y.x * fn; x[1] = x[1] * fo + y.y * fn;
-              x[2] = x[2] * fo + y.z * fn; x[3] = x[3] * fo + y.w * fn;
+            if (mine) {
+              constexpr int kBatch = 8;               // parts in flight per thread
+              for (int k0 = 0; k0 < parts; k0 += kBatch) {
+                float2 ml[kBatch];
+                float4 y[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                  ml[k] = make_float2(-INFINITY, 0.f);
+                  y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (k0 + k < parts) {
+                    const float* s = slot_of(from + (k0 + k) * step);
+                    ml[k] = __ldcg(reinterpret_cast<const float2*>(s + 8 * NQ * DP + 2 * q));
+                    y[k] = __ldcg(reinterpret_cast<const float4*>(s + q * DP + d));
+                  }
+                }
+                float mn = m;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+                const float fo = ex2_rel(m, mn);
+                m = mn;
+                l *= fo;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) x[z] *= fo;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                  const float f = ex2_rel(ml[k].x, mn);
+                  l += ml[k].y * f;
+                  x[0] += y[k].x * f; x[1] += y[k].y * f; x[2] += y[k].z * f; x[3] += y[k].w * f;
+                }
+              }
+              if (final) emit(q, d, x, m, l);
             }
-            emit(q, d, x, m, l);
+            if (!final) {
+              __syncthreads();                        // a head's (maximum, sum) is read by all its threads
+              if (mine) put(slot_of(from), q, d, x, m, l);
+            }
+          }
+        };
+        const int parts = c_last - c_first + 1;
+        if (parts <= kGroup) {
+          if (arrive_last(p.counters + c_first, parts)) join(c_first, 1, parts, true);
+        } else {
+          const int group = ((int)blockIdx.x - c_first) / kGroup, from = c_first + group * kGroup;
+          const int size = min(kGroup, c_last + 1 - from), groups = (parts + kGroup - 1) / kGroup;
+          if (arrive_last(p.counters + (group == 0 ? 1 : 2) * kMaxAttnCtas + from, size)) {
+            join(from, 1, size, false);
+            if (arrive_last(p.counters + c_first, groups)) join(c_first, kGroup, groups, true);
           }
         }
       }
       __syncthreads();                                // the stages and maxima are read: they may be refilled
+      if (padded) {
+        clear_pad(stage);
+        __syncwarp();
+      }
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }

@@ -17,7 +17,7 @@ AttnPlan attn_plan(int32_t G, int32_t D, bool fp8, int sms) {
 
 size_t attn_workspace_bytes(int32_t G, int32_t D, bool fp8, int sms) {
   const AttnPlan a = attn_plan(G, D, fp8, sms);
-  return kMaxAttnCtas * sizeof(uint32_t) + (size_t)2 * a.grid_max * a.slot_floats * sizeof(float);
+  return kAttnZeroBytes + (size_t)2 * a.grid_max * a.slot_floats * sizeof(float);
 }
 
 cudaError_t launch_attention_bf16(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {

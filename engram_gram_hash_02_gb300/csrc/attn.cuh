@@ -76,11 +76,13 @@ struct AttnParams {
   uint16_t* out;               // bf16
   int64_t out_ts, out_hs;
   float* lse;                  // [B, Hq] or NULL
-  uint32_t* counters;          // kMaxAttnCtas words, zero between calls
+  uint32_t* counters;          // 3 * kMaxAttnCtas words, zero between calls
   float* part;                 // partial results, two slots per CTA
   int32_t* err;
 };
 constexpr int kMaxAttnCtas = 1024;
+constexpr size_t kAttnZeroBytes = ENGRAM_ATTENTION_ZERO_BYTES;
+static_assert(3 * kMaxAttnCtas * sizeof(uint32_t) <= kAttnZeroBytes, "the counters lie in the zeroed part");
 // how a shape runs: its kernel's query tiles per CTA, CTAs and partial floats per slot
 struct AttnPlan {
   int32_t nq, chunks, grid_max, slot_floats;
@@ -104,11 +106,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// two e4m3 codes (the low 16 bits) as two halves: exact
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(r) : "r"(codes));
-  return r;
+// four e4m3 codes as two pairs of halves: exact
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+      : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 
 }  // namespace engram

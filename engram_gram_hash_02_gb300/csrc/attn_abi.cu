@@ -180,7 +180,7 @@ int check_attention(const char* fn, const EngramKVCache* cache, const EngramPage
   a->plan = attn_plan(p.G, p.D, p.cache.fp8, num_sms());
   p.chunks = a->plan.chunks;
   p.counters = static_cast<uint32_t*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxAttnCtas * sizeof(uint32_t));
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnZeroBytes);
   const int64_t longest = window > 0 && window < p.cap ? window : p.cap;
   const int64_t tile = attn_tile_keys(p.cache.fp8);
   const __int128 tiles = (__int128)p.B * p.Hk * p.chunks * ((longest + tile - 1) / tile);

@@ -262,11 +262,12 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
       const uint2 codes = __ldg(reinterpret_cast<const uint2*>(row + d0));
       const uint8_t byte = __ldg((is_v ? c.vs : c.ks) + page * c.spage_b + h * c.shead_b + at * c.stok_b + (d0 >> 5));
       const float scale = __uint_as_float((uint32_t)byte << 23);
-      const uint32_t pairs[4] = {codes.x, codes.x >> 16, codes.y, codes.y >> 16};
+      uint32_t hh[4];
+      e4m3x4_to_f16x2(codes.x, hh[0], hh[1]);
+      e4m3x4_to_f16x2(codes.y, hh[2], hh[3]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t hh = e4m3x2_to_f16x2(pairs[i] & 0xFFFFu);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[i]));
         x[2 * i] = f.x * scale;
         x[2 * i + 1] = f.y * scale;
       }

@@ -549,6 +549,8 @@ typedef struct EngramPagedSeqs {
   const int32_t* seq_lens;    /* [B] */
 } EngramPagedSeqs;
 
+#define ENGRAM_ATTENTION_ZERO_BYTES 16384   /* start of the workspace: zero between calls */
+
 /* Workspace bytes of engram_paged_attention and engram_attention_step for q_heads query heads over this
  * cache on the current device; for any batch up to `batch` and any lengths. 0 on bad sizes. */
 size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int32_t batch);
@@ -563,8 +565,8 @@ size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_he
  *   seqs       lengths outside [0, table_width * page_size] are clamped (ENGRAM_ERR_SEQ_LEN); a page
  *              number outside the cache hides its tokens (ENGRAM_ERR_PAGE)
  *   out        bf16 rows [B, q_heads, head_dim]       lse  device fp32 [B, q_heads], or NULL
- *   workspace  device, 256-byte aligned, engram_attention_workspace_bytes. Its first 4096 bytes must
- *              be zero before the first use; every call leaves them zero. Calls that may overlap need
+ *   workspace  device, 256-byte aligned, engram_attention_workspace_bytes. Its first
+ *              ENGRAM_ATTENTION_ZERO_BYTES must be zero before the first use; every call leaves them zero. Calls that may overlap need
  *              workspaces of their own; calls in order may share one, whatever their shapes.
  * Products take 16-bit operands with fp32 accumulation; scores, sums and lse are fp32. The work is cut
  * evenly over the GPU at token granularity and joined in the order of the tokens: results do not depend

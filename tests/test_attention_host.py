@@ -130,7 +130,7 @@ def test_what_a_program_keeps_is_checked_when_it_is_made(E):
     with pytest.raises(ValueError):
         E.attention_workspace(cache, 3, 1)
     assert E.attention_workspace_bytes(cache, 4, 8) % 256 == 0
-    assert not E.attention_workspace(cache, 4, 8)[:4096].any()
+    assert not E.attention_workspace(cache, 4, 8)[:16384].any()
 
 
 # --------------------------------------------------------------------------------------- the C ABI
@@ -253,7 +253,7 @@ def test_no_tokens_is_no_work(E):
 def test_workspace_covers_the_join_and_the_turned_queries(E):
     a = Abi(E)
     small, big = (a.L.engram_attention_workspace_bytes(C.byref(a.cache()), 4, b) for b in (1, 1000))
-    assert big - small >= 999 * 4 * 64 * 4 and small > 4096
+    assert big - small >= 999 * 4 * 64 * 4 and small > 16384
     assert a.L.engram_attention_workspace_bytes(C.byref(a.cache()), 3, 1) == 0
     assert a.L.engram_attention_workspace_bytes(None, 4, 1) == 0
 

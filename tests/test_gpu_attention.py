@@ -10,6 +10,7 @@ from tests import _attention as H
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ZERO = 16384            # ENGRAM_ATTENTION_ZERO_BYTES
 
 
 def E():
@@ -252,19 +253,19 @@ def test_paged_attention_matches_the_formula(lens, Hk, G, D, page, window, tq, l
     out = torch.full((B, Hq, D), float("nan"), dtype=torch.bfloat16, device=DEV)
     lse = torch.full((B, Hq), float("nan"), device=DEV)
     ws = E().attention_workspace(cache, Hq, B)
-    ws[4096:] = 0xFF                                         # only the first words need to be zero
+    ws[ZERO:] = 0xFF                                          # only the first words need to be zero
     err = word()
     scale = D ** -0.5
     plan = E().PagedAttentionPlan(cache, q, torch.from_numpy(table).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
                                   window=window, out=out, lse=lse, workspace=ws, err=err)
     plan.run()
-    assert int(err) == 0 and not ws[:4096].any()
+    assert int(err) == 0 and not ws[:ZERO].any()
     H.check_attention(cache, table, lens, q, out, lse, scale, window)
     # once more: the same bits
     first = out.clone(), lse.clone()
     out.fill_(float("nan"))
     plan.run()
-    assert torch.equal(out, first[0]) and torch.equal(lse, first[1]) and not ws[:4096].any()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1]) and not ws[:ZERO].any()
 
 
 def test_attention_strided_rows_default_outputs_and_scales():
@@ -485,7 +486,7 @@ def test_decode_loop_in_a_cuda_graph_on_a_side_stream():
         q32 = torch.empty(q.shape, dtype=torch.float32, device=DEV)
         E().engram_qk_norm_rope(nr, q, None, pos, q32)
         H.check_attention(cache, table, lens, q32, plan.out, plan.lse, D ** -0.5)
-        assert not plan.workspace[:4096].any()
+        assert not plan.workspace[:ZERO].any()
 
 
 def test_two_streams_at_once_with_workspaces_of_their_own():
