@@ -46,8 +46,10 @@ struct QkvParams {
   const int64_t* slots;        // [T] (with a cache)
   CacheRef cache;              // cache.k == NULL: nothing is written to a cache
   int32_t* err;
-  int32_t nq, nk, nv;          // row groups per token of each kind (filled by the launcher)
-  FastDiv div_token;           // division by nq + nk + nv
+  // filled by the launcher: the first blocks of keys and values, division by a token's row groups, 1 / D
+  uint32_t first_k, first_v;
+  FastDiv div_q, div_kv;
+  float inv_d;
 };
 cudaError_t launch_qkv(const QkvParams& p, cudaStream_t stream);
 

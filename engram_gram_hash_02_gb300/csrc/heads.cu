@@ -88,113 +88,109 @@ __device__ __forceinline__ float pow2(int e) {
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (149 + e));
 }
 
-// one row's 8 values of this thread to the cache; the four lanes of a block of 32 values share its scale
-__device__ __forceinline__ void cache_store(const CacheRef& c, uint8_t* rows, uint8_t* scales, int64_t page, int64_t at,
-                                            int h, int d0, bool live, unsigned group, const float (&x)[8]) {
-  if (!c.fp8) {
-    if (live) *reinterpret_cast<uint4*>(rows + page * c.page_b + h * c.head_b + at * c.tok_b + 2 * d0) = pack8(x);
-    return;
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-  amax = fmaxf(amax, __shfl_xor_sync(group, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(group, amax, 2));
-  // amax = 1.m * 2^(field - 127) is at most 448 * 2^e = 1.75 * 2^(8 + e) from e = field - 135 on, one more
-  // when 1.m > 1.75. An infinity gets 2^127: 448 * 2^127 reads back as infinite.
+// The exponent of a block's scale: amax = 1.m * 2^(field - 127) is at most 448 * 2^e = 1.75 * 2^(8 + e) from
+// e = field - 135 on, one more when 1.m > 1.75. An infinity gets 2^127: 448 * 2^127 reads back as infinite.
+__device__ __forceinline__ int block_exponent(float amax) {
   const uint32_t bits = __float_as_uint(amax);
   const int field = (int)(bits >> 23);
-  int e = field - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  e = max(e, -126);
-  if (field == 255) e = 127;
-  if (amax == 0.f) e = 0;
-  const float inv = pow2(-e);                  // e <= 127: 2^-127 is a subnormal, exact
-  if (live) {
-    uint2 w;
-    w.x = code4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    w.y = code4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-    *reinterpret_cast<uint2*>(rows + page * c.page_b + h * c.head_b + at * c.tok_b + d0) = w;
-    if ((d0 & 31) == 0)
-      scales[page * c.spage_b + h * c.shead_b + at * c.stok_b + (d0 >> 5)] = (uint8_t)(127 + e);
-  }
+  const int e = max(field - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
+  return amax == 0.f ? 0 : field == 255 ? 127 : e;
 }
 
-// kLanes lanes hold one row (8 values each); a group of lanes takes kRows heads of one token
+// kLanes lanes hold one row (8 values each); a group of lanes takes kRows heads of one token. A block's rows
+// are all queries, all keys or all values, so what is done to them is uniform and every shuffle has the whole
+// warp; rows past the end are computed on zeros and not stored.
 template <int kLanes, bool kF32, int kRows>
-__global__ void __launch_bounds__(kThreads) qkv_kernel(const QkvParams p) {
+__global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvParams p) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int sub = lane & (kLanes - 1);
-  const unsigned group = (kLanes == 32 ? 0xFFFFFFFFu : ((1u << (kLanes & 31)) - 1u)) << (lane - sub);
-  const int per_token = p.nq + p.nk + p.nv;
-  const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
-  if (item >= p.T * per_token) return;
-  const int64_t t = item < ((int64_t)1 << 31) ? fast_div((uint32_t)item, p.div_token) : item / per_token;
-  int c = (int)(item - t * per_token);
-  const bool is_q = c < p.nq;
-  const bool is_v = c >= p.nq + p.nk;
-  if (!is_q) c -= is_v ? p.nq + p.nk : p.nq;
-  const HeadRows& in = is_q ? p.q : is_v ? p.v : p.k;
-  const int h0 = c * kRows;
+  constexpr unsigned kWarp = 0xFFFFFFFFu;
+  const bool is_q = blockIdx.x < p.first_k, is_v = blockIdx.x >= p.first_v;
+  const HeadRows in = is_q ? p.q : is_v ? p.v : p.k;
+  const HeadRows out = is_q ? p.q_out : is_v ? HeadRows{} : p.k_out;
+  const uint16_t* wp = is_q ? p.nr.qw : is_v ? nullptr : p.nr.kw;
+  const bool turn = !is_v && p.nr.R > 0;
+  const bool to_cache = !is_q && p.cache.k != nullptr;
+  const int sub = threadIdx.x & (kLanes - 1);
+  const uint32_t block = blockIdx.x - (is_q ? 0u : is_v ? p.first_v : p.first_k);
+  const int64_t item = (int64_t)block * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const int groups = (in.heads + kRows - 1) / kRows;
+  const FastDiv div = is_q ? p.div_q : p.div_kv;
+  int64_t t = item < ((int64_t)1 << 31) ? fast_div((uint32_t)item, div) : item / groups;
+  const int h0 = (int)(item - t * groups) * kRows;
+  const bool there = t < p.T;
+  if (!there) t = 0;
   const int d0 = sub * 8;
-  const bool live = d0 < p.D;
+  const bool live = there && d0 < p.D;
 
   Raw<kF32> raw[kRows];
+  const uint8_t* src = static_cast<const uint8_t*>(in.data) + (kF32 ? 4 : 2) * (t * in.ts + h0 * in.hs + d0);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (live && h0 + r < in.heads)
-      raw[r].load(static_cast<const uint8_t*>(in.data) + (kF32 ? 4 : 2) * (t * in.ts + (h0 + r) * in.hs + d0));
+      raw[r].load(src + (kF32 ? 4 : 2) * (r * in.hs));
     else
       raw[r].zero();
   }
 
-  // the token's angles for this thread's 8 values
-  const NormRope& nr = p.nr;
-  const int half = nr.R >> 1;
-  const int r0 = d0 - nr.start;
-  const bool turn = !is_v && nr.R > 0;
-  const bool turned = turn && r0 >= 0 && r0 < nr.R;
-  const bool second = r0 >= half;
+  // the token's angles for this thread's 8 values; values outside the turned part get angle 0. A value of a
+  // second half takes + sin times its partner, one of a first half - sin.
+  const int half = p.nr.R >> 1;
+  const int r0 = d0 - p.nr.start;
+  const bool turned = turn && r0 >= 0 && r0 < p.nr.R;
+  const bool pairs = p.nr.interleaved;
+  int other = sub;
   float cs[8], sn[8];
-  if (turned) {
-    int64_t pos = __ldg(p.positions + t);
-    if (pos < 0 || pos >= nr.rows) {
-      if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_POSITION);
-      pos = pos < 0 ? 0 : nr.rows - 1;
-    }
-    const float* row = nr.table + pos * nr.R;
-    if (nr.interleaved) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + (r0 >> 1)));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + (r0 >> 1)));
-      cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
-      sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
-    } else {
-      const int i = second ? r0 - half : r0;
-      load8(row + i, cs);
-      load8(row + half + i, sn);
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
+    if (turned) {
+      int64_t pos = __ldg(p.positions + t);
+      if (pos < 0 || pos >= p.nr.rows) {
+        if (there && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_POSITION);
+        pos = pos < 0 ? 0 : p.nr.rows - 1;
+      }
+      const float* row = p.nr.table + pos * p.nr.R;
+      if (pairs) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(row + (r0 >> 1)));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + (r0 >> 1)));
+        cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
+        sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
+      } else {
+        const bool second = r0 >= half;
+        const int i = second ? r0 - half : r0;
+        load8(row + i, cs);
+        load8(row + half + i, sn);
+        other = second ? sub - (half >> 3) : sub + (half >> 3);
+        if (!second) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sn[k] = -sn[k];
+        }
+      }
     }
   }
-  const uint16_t* wp = is_v ? nullptr : is_q ? nr.qw : nr.kw;
   float w[8];
-  if (wp != nullptr && live) {
+  if (wp != nullptr) {
     Raw<false> rw;
-    rw.load(wp + d0);
+    rw.zero();
+    if (d0 < p.D) rw.load(wp + d0);
     rw.get(w);
   }
-  int64_t page = 0, at = 0;
-  const bool to_cache = !is_q && p.cache.k != nullptr;
-  bool stored = false;
+  uint8_t *rows = nullptr, *scales = nullptr;         // the token's place in the cache
   if (to_cache) {
     const int64_t slot = __ldg(p.slots + t);
-    stored = place(p.cache, slot, &page, &at);
-    if (slot >= p.cache.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
+    int64_t page, at;
+    if (place(p.cache, slot, &page, &at) && there) {
+      rows = (is_v ? p.cache.v : p.cache.k) + page * p.cache.page_b + at * p.cache.tok_b;
+      scales = (is_v ? p.cache.vs : p.cache.ks) + page * p.cache.spage_b + at * p.cache.stok_b;
+    }
+    if (there && slot >= p.cache.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
   }
 
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const int h = h0 + r;
-    if (h >= in.heads) break;
+    const bool mine = live && h < in.heads;
     float x[8];
     raw[r].get(x);
     if (wp != nullptr) {
@@ -202,96 +198,130 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const QkvParams p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-      const float inv = rsqrtf(ss / (float)p.D + nr.eps);
-      if (live) {
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kWarp, ss, o);
+      const float inv = rsqrtf(ss * p.inv_d + p.nr.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
-      }
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
     }
     if (turn) {
-      if (nr.interleaved) {
-        if (turned) {
+      if (pairs) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * cs[i] - b * sn[i];
-            x[2 * i + 1] = b * cs[i] + a * sn[i];
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[2 * i], b = x[2 * i + 1];
+          x[2 * i] = a * cs[i] - b * sn[i];
+          x[2 * i + 1] = b * cs[i] + a * sn[i];
         }
       } else {
-        const int other = turned ? (second ? sub - (half >> 3) : sub + (half >> 3)) : sub;
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = __shfl_sync(group, x[i], other, kLanes);
-          if (turned) x[i] = second ? x[i] * cs[i] + y * sn[i] : x[i] * cs[i] - y * sn[i];
-        }
+        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kWarp, x[i], other, kLanes);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + y[i] * sn[i];
       }
     }
-    if (is_q) {
-      if (live) store8(p.q_out, t, h, d0, x);
-    } else {
-      if (!is_v && p.k_out.data != nullptr && live) store8(p.k_out, t, h, d0, x);
-      if (stored)
-        cache_store(p.cache, is_v ? p.cache.v : p.cache.k, is_v ? p.cache.vs : p.cache.ks, page, at, h, d0, live, group, x);
+    if (out.data != nullptr && mine) store8(out, t, h, d0, x);
+    if (to_cache) {
+      if (!p.cache.fp8) {
+        if (mine && rows != nullptr) *reinterpret_cast<uint4*>(rows + h * p.cache.head_b + 2 * d0) = pack8(x);
+      } else {
+        // the four lanes of a block of 32 values share its scale
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+        amax = fmaxf(amax, __shfl_xor_sync(kWarp, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kWarp, amax, 2));
+        const int e = block_exponent(amax);
+        const float inv = pow2(-e);            // e <= 127: 2^-127 is a subnormal, exact
+        if (mine && rows != nullptr) {
+          uint2 codes;
+          codes.x = code4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+          codes.y = code4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+          *reinterpret_cast<uint2*>(rows + h * p.cache.head_b + d0) = codes;
+          if ((d0 & 31) == 0) scales[h * p.cache.shead_b + (d0 >> 5)] = (uint8_t)(127 + e);
+        }
+      }
     }
   }
 }
 
-// rows of the cache by slot: 8 values per thread, rounded once to the output's type; a slot below 0 or
-// past the cache reads as zeros
-template <int kLanes, bool kFp8>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p) {
+// Rows of the cache by slot, rounded once to the output's type; a slot below 0 or past the cache reads as
+// zeros. A thread takes 16 bytes of kRows heads of a token (16 codes or 8 bf16): with the slot known, that
+// is kRows loads in flight.
+template <int kLanes, bool kFp8, int kRows>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvReadParams p) {
+  constexpr int kVals = kFp8 ? 16 : 8;
   const int sub = threadIdx.x & (kLanes - 1);
   const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
-  const int per_token = 2 * p.heads;
-  if (item >= p.T * per_token) return;
-  const int64_t t = item < ((int64_t)1 << 31) ? fast_div((uint32_t)item, p.div_token) : item / per_token;
-  int h = (int)(item - t * per_token);
-  const bool is_v = h >= p.heads;
-  if (is_v) h -= p.heads;
-  const int d0 = sub * 8;
+  const int groups = (p.heads + kRows - 1) / kRows;
+  const int64_t t = item < ((int64_t)1 << 31) ? fast_div((uint32_t)item, p.div_token) : item / (2 * groups);
+  if (t >= p.T) return;
+  const int group = (int)(item - t * 2 * groups);
+  const bool is_v = group >= groups;
+  const int h0 = (group - (is_v ? groups : 0)) * kRows;
+  const int d0 = sub * kVals;
   if (d0 >= p.D) return;
   const CacheRef& c = p.cache;
   const int64_t slot = __ldg(p.slots + t);
-  int64_t page, at;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (place(c, slot, &page, &at)) {
-    const uint8_t* row = (is_v ? c.v : c.k) + page * c.page_b + h * c.head_b + at * c.tok_b;
-    if (kFp8) {
-      const uint2 codes = __ldg(reinterpret_cast<const uint2*>(row + d0));
-      const uint8_t byte = __ldg((is_v ? c.vs : c.ks) + page * c.spage_b + h * c.shead_b + at * c.stok_b + (d0 >> 5));
-      const float scale = __uint_as_float((uint32_t)byte << 23);
-      uint32_t hh[4];
-      e4m3x4_to_f16x2(codes.x, hh[0], hh[1]);
-      e4m3x4_to_f16x2(codes.y, hh[2], hh[3]);
+  int64_t page = 0, at = 0;
+  const bool ok = place(c, slot, &page, &at);
+  if (slot >= c.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
+  const uint8_t* row = (is_v ? c.v : c.k) + page * c.page_b + at * c.tok_b + h0 * c.head_b + sub * 16;
+  const uint8_t* scale = (is_v ? c.vs : c.ks) + page * c.spage_b + at * c.stok_b + h0 * c.shead_b + (d0 >> 5);
+  uint4 raw[kRows];
+  uint32_t byte[kRows];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[i]));
-        x[2 * i] = f.x * scale;
-        x[2 * i + 1] = f.y * scale;
+  for (int r = 0; r < kRows; ++r) {
+    raw[r] = make_uint4(0, 0, 0, 0);
+    byte[r] = 0;
+    if (ok && h0 + r < p.heads) {
+      raw[r] = __ldg(reinterpret_cast<const uint4*>(row + r * c.head_b));
+      if (kFp8) byte[r] = __ldg(scale + r * c.shead_b);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (h0 + r >= p.heads) break;
+    float x[8];
+    if (kFp8) {
+      const float f = __uint_as_float(byte[r] << 23);
+      const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t hh[4];
+        e4m3x4_to_f16x2(w[2 * half], hh[0], hh[1]);
+        e4m3x4_to_f16x2(w[2 * half + 1], hh[2], hh[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hh[i]));
+          x[2 * i] = v.x * f;
+          x[2 * i + 1] = v.y * f;
+        }
+        store8(is_v ? p.v_out : p.k_out, t, h0 + r, d0 + 8 * half, x);
       }
     } else {
-      Raw<false> r;
-      r.load(row + 2 * d0);
-      r.get(x);
+      Raw<false> b;
+      b.a = raw[r];
+      b.get(x);
+      store8(is_v ? p.v_out : p.k_out, t, h0 + r, d0, x);
     }
-  } else if (slot >= c.slots && sub == 0 && p.err != nullptr) {
-    atomicOr(p.err, ENGRAM_ERR_SLOT);
   }
-  store8(is_v ? p.v_out : p.k_out, t, h, d0, x);
 }
 
 template <int kLanes, bool kF32, int kRows>
 cudaError_t go(QkvParams p, cudaStream_t stream) {
-  p.nq = (p.q.heads + kRows - 1) / kRows;
-  p.nk = (p.k.heads + kRows - 1) / kRows;
-  p.nv = (p.v.heads + kRows - 1) / kRows;
-  const int per_token = p.nq + p.nk + p.nv;
-  p.div_token = make_fastdiv((uint32_t)per_token);
-  const int64_t blocks = (p.T * per_token * kLanes + kThreads - 1) / kThreads;
-  if (blocks >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-  return launch_k(qkv_kernel<kLanes, kF32, kRows>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, false, p);
+  const int64_t per_block = kThreads / kLanes;
+  auto blocks = [&](const HeadRows& r) {
+    const int64_t items = p.T * ((r.heads + kRows - 1) / kRows);
+    return (items + per_block - 1) / per_block;
+  };
+  const int64_t nq = blocks(p.q), nk = blocks(p.k), nv = blocks(p.v);
+  if (nq + nk + nv >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+  p.first_k = (uint32_t)nq;
+  p.first_v = (uint32_t)(nq + nk);
+  p.div_q = make_fastdiv((uint32_t)max((p.q.heads + kRows - 1) / kRows, 1));
+  p.div_kv = make_fastdiv((uint32_t)max((p.k.heads + kRows - 1) / kRows, 1));   // v has k's heads
+  p.inv_d = 1.f / (float)p.D;
+  return launch_k(qkv_kernel<kLanes, kF32, kRows>, dim3((unsigned)(nq + nk + nv)), dim3(kThreads), 0, stream, false, p);
 }
 
 template <int kLanes, bool kF32>
@@ -307,13 +337,22 @@ cudaError_t go_lanes(const QkvParams& p, cudaStream_t stream) {
   return p.D <= 64 ? go_rows<8, kF32>(p, stream) : p.D <= 128 ? go_rows<16, kF32>(p, stream) : go_rows<32, kF32>(p, stream);
 }
 
-template <int kLanes>
+template <int kLanes, bool kFp8, int kRows>
 cudaError_t go_read(KvReadParams p, cudaStream_t stream) {
-  p.div_token = make_fastdiv((uint32_t)(2 * p.heads));
-  const int64_t blocks = (p.T * 2 * p.heads * kLanes + kThreads - 1) / kThreads;
+  const int groups = (p.heads + kRows - 1) / kRows;
+  p.div_token = make_fastdiv((uint32_t)(2 * groups));
+  const int64_t blocks = (p.T * 2 * groups * kLanes + kThreads - 1) / kThreads;
   if (blocks >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-  return launch_k(p.cache.fp8 ? kv_read_kernel<kLanes, true> : kv_read_kernel<kLanes, false>, dim3((unsigned)blocks),
-                  dim3(kThreads), 0, stream, false, p);
+  return launch_k(kv_read_kernel<kLanes, kFp8, kRows>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, false, p);
+}
+
+template <bool kFp8, int kRows>
+cudaError_t go_read_lanes(const KvReadParams& p, cudaStream_t stream) {
+  const int bytes = kFp8 ? p.D : 2 * p.D;              // 16 per lane
+  return bytes <= 64    ? go_read<4, kFp8, kRows>(p, stream)
+         : bytes <= 128 ? go_read<8, kFp8, kRows>(p, stream)
+         : bytes <= 256 ? go_read<16, kFp8, kRows>(p, stream)
+                        : go_read<32, kFp8, kRows>(p, stream);
 }
 
 }  // namespace
@@ -324,7 +363,10 @@ cudaError_t launch_qkv(const QkvParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {
-  return p.D <= 64 ? go_read<8>(p, stream) : p.D <= 128 ? go_read<16>(p, stream) : go_read<32>(p, stream);
+  // as above: four rows per thread once every resident thread has that many
+  const bool many = p.T * p.heads * p.D / 8 > (int64_t)num_sms() * 2048 * 4;
+  if (p.cache.fp8) return many ? go_read_lanes<true, 4>(p, stream) : go_read_lanes<true, 1>(p, stream);
+  return many ? go_read_lanes<false, 4>(p, stream) : go_read_lanes<false, 1>(p, stream);
 }
 
 }  // namespace engram
