@@ -119,6 +119,11 @@ def _alloc(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+# a plan's run() is a few microseconds of host time: the current stream as a number, without an object for it
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
 class _Plan:
     """A call of the library marshalled once for fixed tensors. The tensors are kept alive; run() enqueues
     the call on `stream` (default: the current stream of the plan's device)."""
@@ -127,12 +132,13 @@ class _Plan:
         self._name, self._fn, self._args, self._keep, self._device = fn, getattr(lib(), fn), args, keep, device
 
     def run(self, stream=None):
-        s = torch.cuda.current_stream(self._device) if stream is None else stream
-        if torch.cuda.current_device() != self._device.index:
-            with torch.cuda.device(self._device):
-                rc = self._fn(*self._args, s.cuda_stream)
+        index = self._device.index
+        s = _current_raw_stream(index) if stream is None else stream.cuda_stream
+        if _current_device() == index:
+            rc = self._fn(*self._args, s)
         else:
-            rc = self._fn(*self._args, s.cuda_stream)
+            with torch.cuda.device(self._device):
+                rc = self._fn(*self._args, s)
         if rc != 0:
             _check(self._name, rc)
 

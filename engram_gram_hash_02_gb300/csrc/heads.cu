@@ -9,9 +9,10 @@
 // scale is the smallest 2^e with max|x| / 2^e <= 448, e >= -126, and a code is x / 2^e rounded to the
 // nearest e4m3 value, ties to even (the convention of the FP8 tables; an all-zero block has byte 127).
 //
-// Bound by HBM: a row is read once and written once. A row is held by 8, 16 or 32 lanes, 8 values
-// each (16-byte loads of bf16), so a norm is a few shuffles; a group of lanes takes several heads of one
-// token when there are enough rows to fill the GPU, so the token's angles are read once for all of them.
+// Bound by HBM: a row is read once and written once. A row is held by 8, 16 or 32 lanes, 8 values each, so a
+// norm is a few shuffles. Measured on a GB300 (share of the 6.78 TB/s of a plain copy): 32768 tokens of 32 + 8
+// heads of 128 normed and turned in 111 us, 6.15 TB/s (0.91; issue slots 76 % busy); 8 + 8 heads written as FP8
+// in 36 us (0.84), as bf16 in 41 us (0.96); read back in 34 us (0.88) and 41 us (0.96).
 #include "attn.cuh"
 
 namespace engram {
@@ -19,30 +20,10 @@ namespace {
 
 constexpr int kThreads = 128;
 
-template <bool kF32>
-struct Raw;
-template <>
-struct Raw<false> {
-  uint4 a;
-  __device__ void load(const void* p) { a = *static_cast<const uint4*>(p); }   // not ld.nc: the output may be the input
-  __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
-  __device__ void get(float (&x)[8]) const {
-    x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
-    x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
-  }
-};
-template <>
-struct Raw<true> {
-  float4 a, b;
-  __device__ void load(const void* p) {
-    a = *static_cast<const float4*>(p);
-    b = *(static_cast<const float4*>(p) + 1);
-  }
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-};
+__device__ __forceinline__ void unpack8(uint4 a, float (&x)[8]) {
+  x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
+  x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
+}
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -53,15 +34,17 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-__device__ __forceinline__ void store8(const HeadRows& o, int64_t t, int h, int d0, const float (&x)[8]) {
-  const int64_t i = t * o.ts + h * o.hs + d0;
-  if (o.f32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.data) + i);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+// 8 values at p, as fp32 or bf16
+__device__ __forceinline__ void store8(void* p, bool f32, const float (&x)[8]) {
+  if (f32) {
+    static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.data) + i) = pack8(x);
+    *static_cast<uint4*>(p) = pack8(x);
   }
+}
+__device__ __forceinline__ uint8_t* row_of(const HeadRows& o, int64_t t, int h, int d0) {
+  return static_cast<uint8_t*>(o.data) + (t * o.ts + h * o.hs + d0) * (o.f32 ? 4 : 2);
 }
 
 // byte offsets of slot's row of head h: false if the slot is out of range
@@ -83,146 +66,199 @@ __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// 2^e for e in [-149, 127], exactly (a subnormal below -126)
-__device__ __forceinline__ float pow2(int e) {
-  return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (149 + e));
+// The scale byte of a block: amax = 1.m * 2^(field - 127) is at most 448 * 2^e = 1.75 * 2^(8 + e) from
+// e = field - 135 on, one more when 1.m > 1.75 (the sum below carries into the field then); byte 127 + e, at
+// least 1, and 127 for an all-zero block. An infinity gets 2^127: 448 * 2^127 reads back as infinite.
+__device__ __forceinline__ int scale_byte(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int byte = max((int)((bits + 0x1FFFFFu) >> 23) - 8, 1);
+  return bits == 0 ? 127 : bits == 0x7F800000u ? 254 : byte;
+}
+// 2^-e of a scale byte 127 + e in [1, 254]: exact (a subnormal at the end)
+__device__ __forceinline__ float inverse_scale(int byte) {
+  return __uint_as_float(byte == 254 ? 0x00400000u : (uint32_t)(254 - byte) << 23);
 }
 
-// The exponent of a block's scale: amax = 1.m * 2^(field - 127) is at most 448 * 2^e = 1.75 * 2^(8 + e) from
-// e = field - 135 on, one more when 1.m > 1.75. An infinity gets 2^127: 448 * 2^127 reads back as infinite.
-__device__ __forceinline__ int block_exponent(float amax) {
-  const uint32_t bits = __float_as_uint(amax);
-  const int field = (int)(bits >> 23);
-  const int e = max(field - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
-  return amax == 0.f ? 0 : field == 255 ? 127 : e;
+// until at most n of a thread's copies are in flight (n < kRows, known when the loop is unrolled)
+template <int kRows>
+__device__ __forceinline__ void wait_rows(int n) {
+  switch (n) {
+    case 0: cp_async_wait<0>(); break;
+    case 1: cp_async_wait<1>(); break;
+    case 2: cp_async_wait<2>(); break;
+    case 3: cp_async_wait<3>(); break;
+    case 4: cp_async_wait<4>(); break;
+    case 5: cp_async_wait<5>(); break;
+    case 6: cp_async_wait<6>(); break;
+    default: cp_async_wait<7>(); break;
+  }
+  static_assert(kRows <= 8, "");
 }
 
 // kLanes lanes hold one row (8 values each); a group of lanes takes kRows heads of one token. A block's rows
 // are all queries, all keys or all values, so what is done to them is uniform and every shuffle has the whole
 // warp; rows past the end are computed on zeros and not stored.
+//
+// All rows of a thread are requested at once by cp.async into places of its own in shared memory, so their
+// bytes in flight do not depend on registers, and the angles are fetched behind them. Norm and turn are
+//   out_i = r * (x_i * A_i + y_i * B_i),  r = 1 / sqrt(mean(x^2) + eps),  y_i the other value of x_i's pair,
+// with A_i = w_i cos, B_i = -+ w_y sin formed once per token; y comes from the partner lane's place.
 template <int kLanes, bool kF32, int kRows>
 __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvParams p) {
+  constexpr unsigned kWarp = 0xFFFFFFFFu;
+  constexpr int kBytes = kF32 ? 4 : 2;
+  constexpr int kParts = kF32 ? 2 : 1;                // 16-byte chunks per lane
+  __shared__ uint4 place_of[kRows][kThreads * kParts];
   pdl_wait();
   pdl_trigger();
-  constexpr unsigned kWarp = 0xFFFFFFFFu;
   const bool is_q = blockIdx.x < p.first_k, is_v = blockIdx.x >= p.first_v;
   const HeadRows in = is_q ? p.q : is_v ? p.v : p.k;
   const HeadRows out = is_q ? p.q_out : is_v ? HeadRows{} : p.k_out;
   const uint16_t* wp = is_q ? p.nr.qw : is_v ? nullptr : p.nr.kw;
   const bool turn = !is_v && p.nr.R > 0;
   const bool to_cache = !is_q && p.cache.k != nullptr;
-  const int sub = threadIdx.x & (kLanes - 1);
+  const int tid = threadIdx.x, sub = tid & (kLanes - 1);
   const uint32_t block = blockIdx.x - (is_q ? 0u : is_v ? p.first_v : p.first_k);
-  const int64_t item = (int64_t)block * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const int64_t item = (int64_t)block * (kThreads / kLanes) + tid / kLanes;
   const int groups = (in.heads + kRows - 1) / kRows;
-  const FastDiv div = is_q ? p.div_q : p.div_kv;
-  int64_t t = item < ((int64_t)1 << 31) ? fast_div((uint32_t)item, div) : item / groups;
+  int64_t t = item < ((int64_t)1 << 31) ? fast_div((uint32_t)item, is_q ? p.div_q : p.div_kv) : item / groups;
   const int h0 = (int)(item - t * groups) * kRows;
   const bool there = t < p.T;
   if (!there) t = 0;
   const int d0 = sub * 8;
   const bool live = there && d0 < p.D;
+  const int rows = live ? min(in.heads - h0, kRows) : 0;
 
-  Raw<kF32> raw[kRows];
-  const uint8_t* src = static_cast<const uint8_t*>(in.data) + (kF32 ? 4 : 2) * (t * in.ts + h0 * in.hs + d0);
+  // a group's lanes copy consecutive chunks; chunk c of a row lies at c ^ (c / 8 & 1), so that reads of two
+  // chunks per lane (fp32) meet no bank twice
+  auto chunk_at = [&](int c) { return (tid - sub) * kParts + (kF32 ? c ^ ((c >> 3) & 1) : c); };
+  const uint8_t* src = static_cast<const uint8_t*>(in.data) + kBytes * (t * in.ts + h0 * in.hs);
+  const int64_t step = kBytes * in.hs;
+  const int there_rows = there ? in.heads - h0 : 0;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    if (live && h0 + r < in.heads)
-      raw[r].load(src + (kF32 ? 4 : 2) * (r * in.hs));
-    else
-      raw[r].zero();
+#pragma unroll
+    for (int z = 0; z < kParts; ++z) {
+      const int c = sub + z * kLanes;
+      if (r < there_rows && c * 16 < p.D * kBytes)
+        cp_async16((uint32_t)__cvta_generic_to_shared(&place_of[r][chunk_at(c)]), src + 16 * c);
+      else
+        place_of[r][chunk_at(c)] = make_uint4(0, 0, 0, 0);
+    }
+    cp_async_commit();
+    src += step;
   }
 
-  // the token's angles for this thread's 8 values; values outside the turned part get angle 0. A value of a
-  // second half takes + sin times its partner, one of a first half - sin.
+  // A and B of this thread's 8 values. A value of a second half takes + sin times its partner, one of a first
+  // half - sin.
   const int half = p.nr.R >> 1;
   const int r0 = d0 - p.nr.start;
-  const bool turned = turn && r0 >= 0 && r0 < p.nr.R;
+  const bool turned = turn && live && r0 >= 0 && r0 < p.nr.R;
   const bool pairs = p.nr.interleaved;
   int other = sub;
-  float cs[8], sn[8];
-  if (turn) {
+  float A[8], B[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
-    if (turned) {
-      int64_t pos = __ldg(p.positions + t);
-      if (pos < 0 || pos >= p.nr.rows) {
-        if (there && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_POSITION);
-        pos = pos < 0 ? 0 : p.nr.rows - 1;
-      }
-      const float* row = p.nr.table + pos * p.nr.R;
-      if (pairs) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(row + (r0 >> 1)));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + (r0 >> 1)));
-        cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
-        sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
-      } else {
-        const bool second = r0 >= half;
-        const int i = second ? r0 - half : r0;
-        load8(row + i, cs);
-        load8(row + half + i, sn);
-        other = second ? sub - (half >> 3) : sub + (half >> 3);
-        if (!second) {
+  for (int i = 0; i < 8; ++i) { A[i] = 1.f; B[i] = 0.f; }
+  if (turned) {
+    int64_t pos = __ldg(p.positions + t);
+    if (pos < 0 || pos >= p.nr.rows) {
+      if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_POSITION);
+      pos = pos < 0 ? 0 : p.nr.rows - 1;
+    }
+    const float* row = p.nr.table + pos * p.nr.R;
+    if (pairs) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(row + (r0 >> 1)));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + (r0 >> 1)));
+      A[0] = A[1] = c.x; A[2] = A[3] = c.y; A[4] = A[5] = c.z; A[6] = A[7] = c.w;
+      B[0] = -s.x; B[1] = s.x; B[2] = -s.y; B[3] = s.y; B[4] = -s.z; B[5] = s.z; B[6] = -s.w; B[7] = s.w;
+    } else {
+      const bool second = r0 >= half;
+      const int i = second ? r0 - half : r0;
+      load8(row + i, A);
+      load8(row + half + i, B);
+      other = second ? sub - (half >> 3) : sub + (half >> 3);
+      if (!second) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sn[k] = -sn[k];
-        }
+        for (int k = 0; k < 8; ++k) B[k] = -B[k];
       }
     }
   }
-  float w[8];
-  if (wp != nullptr) {
-    Raw<false> rw;
-    rw.zero();
-    if (d0 < p.D) rw.load(wp + d0);
-    rw.get(w);
+  if (wp != nullptr && live) {
+    float w[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(wp + d0)), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) A[i] *= w[i];
+    if (turned) {
+      if (!pairs) unpack8(__ldg(reinterpret_cast<const uint4*>(wp + 8 * other)), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) B[i] *= w[pairs ? i ^ 1 : i];
+    }
   }
-  uint8_t *rows = nullptr, *scales = nullptr;         // the token's place in the cache
+  uint8_t *dst = nullptr, *scales = nullptr;          // this thread's place in the token's first row of the cache
+  bool stored = false;
   if (to_cache) {
     const int64_t slot = __ldg(p.slots + t);
     int64_t page, at;
-    if (place(p.cache, slot, &page, &at) && there) {
-      rows = (is_v ? p.cache.v : p.cache.k) + page * p.cache.page_b + at * p.cache.tok_b;
-      scales = (is_v ? p.cache.vs : p.cache.ks) + page * p.cache.spage_b + at * p.cache.stok_b;
+    stored = place(p.cache, slot, &page, &at);
+    if (stored) {
+      dst = (is_v ? p.cache.v : p.cache.k) + page * p.cache.page_b + at * p.cache.tok_b + h0 * p.cache.head_b + (p.cache.fp8 ? d0 : 2 * d0);
+      scales = (is_v ? p.cache.vs : p.cache.ks) + page * p.cache.spage_b + at * p.cache.stok_b + h0 * p.cache.shead_b + (d0 >> 5);
     }
-    if (there && slot >= p.cache.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
+    if (live && slot >= p.cache.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
   }
+  uint8_t* to = row_of(out, t, h0, d0);
+  const int64_t to_step = out.hs * (out.f32 ? 4 : 2);
 
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    const int h = h0 + r;
-    const bool mine = live && h < in.heads;
+    wait_rows<kRows>(kRows - 1 - r);
+    __syncwarp();                                     // what the warp's other lanes copied is there too
+    auto values = [&](int s, float (&v)[8]) {         // lane s's of the group
+      if (kF32) {
+        const uint4 a = place_of[r][chunk_at(2 * s)], b = place_of[r][chunk_at(2 * s + 1)];
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+      } else {
+        unpack8(place_of[r][chunk_at(s)], v);
+      }
+    };
     float x[8];
-    raw[r].get(x);
+    values(sub, x);
+    float inv = 1.f;
     if (wp != nullptr) {
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kWarp, ss, o);
-      const float inv = rsqrtf(ss * p.inv_d + p.nr.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+      inv = rsqrtf(ss * p.inv_d + p.nr.eps);
     }
-    if (turn) {
+    if (turn || wp != nullptr) {
+      float y[8];
       if (pairs) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * cs[i] - b * sn[i];
-          x[2 * i + 1] = b * cs[i] + a * sn[i];
-        }
-      } else {
-        float y[8];
+        for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+      } else if (turn) {
+        values(other, y);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kWarp, x[i], other, kLanes);
+      for (int i = 0; i < 8; ++i) x[i] *= A[i];
+      if (turned) {                                   // (a value that is not turned takes nothing from another)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + y[i] * sn[i];
+        for (int i = 0; i < 8; ++i) x[i] += y[i] * B[i];
+      }
+      if (wp != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= inv;
       }
     }
-    if (out.data != nullptr && mine) store8(out, t, h, d0, x);
+    if (out.data != nullptr) {
+      if (r < rows) store8(to, out.f32, x);
+      to += to_step;
+    }
     if (to_cache) {
       if (!p.cache.fp8) {
-        if (mine && rows != nullptr) *reinterpret_cast<uint4*>(rows + h * p.cache.head_b + 2 * d0) = pack8(x);
+        if (r < rows && stored) *reinterpret_cast<uint4*>(dst) = pack8(x);
       } else {
         // the four lanes of a block of 32 values share its scale
         float amax = 0.f;
@@ -230,26 +266,27 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
         amax = fmaxf(amax, __shfl_xor_sync(kWarp, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kWarp, amax, 2));
-        const int e = block_exponent(amax);
-        const float inv = pow2(-e);            // e <= 127: 2^-127 is a subnormal, exact
-        if (mine && rows != nullptr) {
+        const int byte = scale_byte(amax);
+        const float down = inverse_scale(byte);
+        if (r < rows && stored) {
           uint2 codes;
-          codes.x = code4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-          codes.y = code4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-          *reinterpret_cast<uint2*>(rows + h * p.cache.head_b + d0) = codes;
-          if ((d0 & 31) == 0) scales[h * p.cache.shead_b + (d0 >> 5)] = (uint8_t)(127 + e);
+          codes.x = code4(x[0] * down, x[1] * down, x[2] * down, x[3] * down);
+          codes.y = code4(x[4] * down, x[5] * down, x[6] * down, x[7] * down);
+          *reinterpret_cast<uint2*>(dst) = codes;
+          if ((sub & 3) == 0) *scales = (uint8_t)byte;
         }
+        scales += p.cache.shead_b;
       }
+      dst += p.cache.head_b;
     }
   }
 }
 
 // Rows of the cache by slot, rounded once to the output's type; a slot below 0 or past the cache reads as
-// zeros. A thread takes 16 bytes of kRows heads of a token (16 codes or 8 bf16): with the slot known, that
-// is kRows loads in flight.
+// zeros. A thread takes 8 values of kRows heads of a token: with the slot known, that is kRows loads in
+// flight, and every store of the warp is a run of full sectors.
 template <int kLanes, bool kFp8, int kRows>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvReadParams p) {
-  constexpr int kVals = kFp8 ? 16 : 8;
   const int sub = threadIdx.x & (kLanes - 1);
   const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
   const int groups = (p.heads + kRows - 1) / kRows;
@@ -258,14 +295,14 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   const int group = (int)(item - t * 2 * groups);
   const bool is_v = group >= groups;
   const int h0 = (group - (is_v ? groups : 0)) * kRows;
-  const int d0 = sub * kVals;
+  const int d0 = sub * 8;
   if (d0 >= p.D) return;
   const CacheRef& c = p.cache;
   const int64_t slot = __ldg(p.slots + t);
   int64_t page = 0, at = 0;
   const bool ok = place(c, slot, &page, &at);
   if (slot >= c.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
-  const uint8_t* row = (is_v ? c.v : c.k) + page * c.page_b + at * c.tok_b + h0 * c.head_b + sub * 16;
+  const uint8_t* row = (is_v ? c.v : c.k) + page * c.page_b + at * c.tok_b + h0 * c.head_b + (kFp8 ? d0 : 2 * d0);
   const uint8_t* scale = (is_v ? c.vs : c.ks) + page * c.spage_b + at * c.stok_b + h0 * c.shead_b + (d0 >> 5);
   uint4 raw[kRows];
   uint32_t byte[kRows];
@@ -274,37 +311,62 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     raw[r] = make_uint4(0, 0, 0, 0);
     byte[r] = 0;
     if (ok && h0 + r < p.heads) {
-      raw[r] = __ldg(reinterpret_cast<const uint4*>(row + r * c.head_b));
-      if (kFp8) byte[r] = __ldg(scale + r * c.shead_b);
+      if (kFp8) {
+        const uint2 codes = __ldg(reinterpret_cast<const uint2*>(row + r * c.head_b));
+        raw[r].x = codes.x;
+        raw[r].y = codes.y;
+        byte[r] = __ldg(scale + r * c.shead_b);
+      } else {
+        raw[r] = __ldg(reinterpret_cast<const uint4*>(row + r * c.head_b));
+      }
     }
   }
+  const HeadRows& out = is_v ? p.v_out : p.k_out;
+  const bool f32 = out.f32;
+  uint8_t* to = row_of(out, t, h0, d0);
+  const int64_t step = out.hs * (f32 ? 4 : 2);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (h0 + r >= p.heads) break;
     float x[8];
     if (kFp8) {
       const float f = __uint_as_float(byte[r] << 23);
-      const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+      uint32_t hh[4];
+      e4m3x4_to_f16x2(raw[r].x, hh[0], hh[1]);
+      e4m3x4_to_f16x2(raw[r].y, hh[2], hh[3]);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hh[4];
-        e4m3x4_to_f16x2(w[2 * half], hh[0], hh[1]);
-        e4m3x4_to_f16x2(w[2 * half + 1], hh[2], hh[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hh[i]));
-          x[2 * i] = v.x * f;
-          x[2 * i + 1] = v.y * f;
-        }
-        store8(is_v ? p.v_out : p.k_out, t, h0 + r, d0 + 8 * half, x);
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hh[i]));
+        x[2 * i] = v.x * f;
+        x[2 * i + 1] = v.y * f;
       }
     } else {
-      Raw<false> b;
-      b.a = raw[r];
-      b.get(x);
-      store8(is_v ? p.v_out : p.k_out, t, h0 + r, d0, x);
+      unpack8(raw[r], x);
+    }
+    store8(to, f32, x);
+    to += step;
+  }
+}
+
+// Heads of one token that a group of lanes takes. More of them share the token's angles and slot and are in
+// flight together: 32768 tokens of 32 + 8 heads of 128 are normed and turned in 312, 195, 133 and 111 us with 1,
+// 2, 4 and 8. But few rows want lanes of their own: 256 tokens of 8 + 8 heads are written in 2.3 us with 1 and
+// 3.7 us with 8 (half of the GPU's lanes or less), 1024 tokens in 4.1, 3.2, 3.2 and 4.0 us. Within those limits
+// the choice wastes least: a group costs what its rows do, a part-filled one as much as a full one, and
+// about three rows more.
+int rows_per_group(int64_t T, const int (&heads)[3], int lanes) {
+  const double fill = (double)T * (heads[0] + heads[1] + heads[2]) * lanes / (num_sms() * 2048.0);
+  const int most = fill < 0.5 ? 1 : fill < 2.0 ? 4 : 8;
+  int best = 1, least = 0;
+  for (int r = 1; r <= most; r *= 2) {
+    int cost = 0;
+    for (int h : heads) cost += (h + r - 1) / r * (r + 3);
+    if (r == 1 || cost < least) {
+      best = r;
+      least = cost;
     }
   }
+  return best;
 }
 
 template <int kLanes, bool kF32, int kRows>
@@ -326,10 +388,13 @@ cudaError_t go(QkvParams p, cudaStream_t stream) {
 
 template <int kLanes, bool kF32>
 cudaError_t go_rows(const QkvParams& p, cudaStream_t stream) {
-  // four heads per group of lanes share the token's angles and keep four loads in flight; with fewer rows
-  // than four per resident group of lanes every row gets its own lanes
-  const int64_t rows = p.T * (p.q.heads + p.k.heads + p.v.heads);
-  return rows * kLanes > (int64_t)num_sms() * 2048 * 4 ? go<kLanes, kF32, 4>(p, stream) : go<kLanes, kF32, 1>(p, stream);
+  const int heads[3] = {p.q.heads, p.k.heads, p.v.heads};
+  switch (rows_per_group(p.T, heads, kLanes)) {
+    case 8: return go<kLanes, kF32, 8>(p, stream);
+    case 4: return go<kLanes, kF32, 4>(p, stream);
+    case 2: return go<kLanes, kF32, 2>(p, stream);
+    default: return go<kLanes, kF32, 1>(p, stream);
+  }
 }
 
 template <bool kF32>
@@ -348,11 +413,19 @@ cudaError_t go_read(KvReadParams p, cudaStream_t stream) {
 
 template <bool kFp8, int kRows>
 cudaError_t go_read_lanes(const KvReadParams& p, cudaStream_t stream) {
-  const int bytes = kFp8 ? p.D : 2 * p.D;              // 16 per lane
-  return bytes <= 64    ? go_read<4, kFp8, kRows>(p, stream)
-         : bytes <= 128 ? go_read<8, kFp8, kRows>(p, stream)
-         : bytes <= 256 ? go_read<16, kFp8, kRows>(p, stream)
-                        : go_read<32, kFp8, kRows>(p, stream);
+  return p.D <= 64    ? go_read<8, kFp8, kRows>(p, stream)
+         : p.D <= 128 ? go_read<16, kFp8, kRows>(p, stream)
+                      : go_read<32, kFp8, kRows>(p, stream);
+}
+template <bool kFp8>
+cudaError_t go_read_rows(const KvReadParams& p, cudaStream_t stream) {
+  const int heads[3] = {0, p.heads, p.heads};
+  switch (rows_per_group(p.T, heads, p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32)) {
+    case 8: return go_read_lanes<kFp8, 8>(p, stream);
+    case 4: return go_read_lanes<kFp8, 4>(p, stream);
+    case 2: return go_read_lanes<kFp8, 2>(p, stream);
+    default: return go_read_lanes<kFp8, 1>(p, stream);
+  }
 }
 
 }  // namespace
@@ -363,10 +436,7 @@ cudaError_t launch_qkv(const QkvParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {
-  // as above: four rows per thread once every resident thread has that many
-  const bool many = p.T * p.heads * p.D / 8 > (int64_t)num_sms() * 2048 * 4;
-  if (p.cache.fp8) return many ? go_read_lanes<true, 4>(p, stream) : go_read_lanes<true, 1>(p, stream);
-  return many ? go_read_lanes<false, 4>(p, stream) : go_read_lanes<false, 1>(p, stream);
+  return p.cache.fp8 ? go_read_rows<true>(p, stream) : go_read_rows<false>(p, stream);
 }
 
 }  // namespace engram
