@@ -42,6 +42,24 @@ namespace attn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                            // parts of a cut run that one CTA joins
+#ifndef ATTN_RUN
+#define ATTN_RUN 2
+#endif
+#ifndef C64
+#define C64 3
+#define S64 4
+#endif
+#ifndef C128
+#define C128 2
+#define S128 3
+#endif
+#ifndef ATTN_MIN
+#define ATTN_MIN 1
+#endif
+#ifndef ATTN_BATCH
+#define ATTN_BATCH 16
+#endif
+constexpr int kRunCost = ATTN_RUN, kMinPlaces = ATTN_MIN;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -74,6 +92,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// releases what the CTA wrote before its last barrier, and acquires what other arrivals released
+__device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -93,8 +117,8 @@ struct Cfg {
   static constexpr int kRowB = kFp8 ? DP : 2 * DP;
   static constexpr int kWords = (DP + 127) / 128;     // scale words per row
   static constexpr int kStageB = 2 * kStep * kRowB + (kFp8 ? 2 * kStep * kWords * 4 : 0);
-  static constexpr int kCtas = DP == 64 ? 3 : DP == 128 ? 2 : 1;
-  static constexpr int kStages = DP == 64 ? 4 : 3;
+  static constexpr int kCtas = DP == 64 ? C64 : DP == 128 ? C128 : 1;
+  static constexpr int kStages = DP == 64 ? S64 : DP == 128 ? S128 : 3;
   static constexpr int kRingB = kWarps * kStages * kStageB;
   static constexpr int kQPitch = DP + 8;              // 16-bit values
   static constexpr int kQB = NQ * 8 * kQPitch * 2;    // per part (high, low)
@@ -118,7 +142,7 @@ __host__ __device__ constexpr uint32_t swz(int r) {
 struct Meta {
   uint32_t mask;               // keys of the step that are attended
   uint32_t ends;               // bit 0: first tile of its run, bit 1: last
-  int32_t seq, hc, tile, tiles;// sequence, head * chunks + chunk, tile of the run and tiles it has
+  int32_t seq, hc, run0, tiles;// sequence, head * chunks + chunk, place of the run's first tile and its tiles
   int32_t pad[2];
 };
 
@@ -142,14 +166,18 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   int* sm_i = reinterpret_cast<int*>(small + 160);   // scan and broadcast words
   const int heads = p.Hk * p.chunks;
 
-  // ---- this CTA's run of tiles ---------------------------------------------------------------
+  // ---- this CTA's share --------------------------------------------------------------------
+  // A run (a sequence's tiles for one key head and group of query heads) takes kRunCost + tiles places in a
+  // row of all runs; CTA i takes the tiles at places [i * per_cta, (i + 1) * per_cta).
+  auto tiles_of = [&](int raw) { return (attended(clamp_len(raw, p.cap), p.window) + C::kTile - 1) / C::kTile; };
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = tid * per, b1 = min(p.B, b0 + per);
   int mine = 0;
   for (int b = b0; b < b1; ++b) {
     const int raw = __ldg(p.lens + b);
     if (blockIdx.x == 0 && (raw < 0 || raw > p.cap) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
-    mine += (attended(clamp_len(raw, p.cap), p.window) + C::kTile - 1) / C::kTile * heads;
+    const int tiles = tiles_of(raw);
+    mine += tiles > 0 ? (tiles + kRunCost) * heads : 0;
   }
   int scan = mine;
 #pragma unroll
@@ -165,26 +193,29 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     if (w < warp) before += sm_i[w];
     total += sm_i[w];
   }
-  const int per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
-  const int t0 = min(total, (int)blockIdx.x * per_cta), t1 = min(total, t0 + per_cta);
-  if (t0 < t1 && t0 >= before && t0 < before + mine) {
+  const int per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinPlaces);
+  const int place0 = min(total, (int)blockIdx.x * per_cta), place1 = min(total, place0 + per_cta);
+  if (place0 < place1 && place0 >= before && place0 < before + mine) {
     int at = before;
     for (int b = b0; b < b1; ++b) {
-      const int tiles = (attended(clamp_len(__ldg(p.lens + b), p.cap), p.window) + C::kTile - 1) / C::kTile;
-      if (t0 < at + tiles * heads) {
+      const int tiles = tiles_of(__ldg(p.lens + b));
+      const int places = tiles > 0 ? (tiles + kRunCost) * heads : 0;
+      if (place0 < at + places) {
+        const int run = (place0 - at) / (tiles + kRunCost);
         sm_i[8] = b;
-        sm_i[9] = (t0 - at) / tiles;
-        sm_i[10] = (t0 - at) % tiles;
+        sm_i[9] = run;
+        sm_i[10] = max((place0 - at) - run * (tiles + kRunCost) - kRunCost, 0);
+        sm_i[11] = at + run * (tiles + kRunCost) + kRunCost;   // the run's first tile
         break;
       }
-      at += tiles * heads;
+      at += places;
     }
   }
   __syncthreads();
   pdl_wait();
 
-  // ---- the producer's place: step i is tile t0 + i ----------------------------------------------
-  int seq = sm_i[8], hc = sm_i[9], tile = sm_i[10], first = 0, end = 0, tiles = 0;
+  // ---- the producer: one tile after another ------------------------------------------------------
+  int seq = sm_i[8], hc = sm_i[9], tile = sm_i[10], run0 = sm_i[11], first = 0, end = 0, tiles = 0;
   int64_t head_off = 0, shead_off = 0;
   auto enter_head = [&] {
     const int head = p.chunks == 1 ? hc : hc / p.chunks;
@@ -200,16 +231,18 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   };
   auto advance = [&] {
     if (++tile < tiles) return;
+    run0 += tiles + kRunCost;                         // the next run's first tile
     tile = 0;
     if (++hc == heads) {
       hc = 0;
       do {
-        if (++seq >= p.B) return;                     // past the last tile: never fetched
+        if (++seq >= p.B) return;                     // past the last place: never fetched
         enter();
       } while (tiles == 0);
     }
     enter_head();
   };
+  auto more = [&] { return run0 + tile < place1; };
   // the page of this lane's row, requested one step before its copies
   int page = -1, at = 0;
   bool inside = false;
@@ -237,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     if (lane == 0) {
       Meta m;
       m.mask = mask; m.ends = (tile == 0 ? 1u : 0u) | (tile + 1 == tiles ? 2u : 0u);
-      m.seq = seq; m.hc = hc; m.tile = tile; m.tiles = tiles;
+      m.seq = seq; m.hc = hc; m.run0 = run0; m.tiles = tiles;
       meta[stage] = m;
     }
     if (mask == 0) return;                            // no keys for this warp: the stage is not read
@@ -297,22 +330,22 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   const bool padded = p.D < DP;
   const uint32_t scale_bytes = p.D % 128 == 0 ? 0xFFFFFFFFu : (1u << (8 * (p.D % 128 / 32))) - 1u;   // of the last word
 
-  const int n = t1 - t0;
   int ahead = 0;                                      // steps requested so far
-  if (n > 0) {
+  if (place0 < place1) {
     if (padded) {
       for (int s = 0; s < kStages; ++s) clear_pad(s);
       __syncwarp();
     }
     enter();
     enter_head();
-    request();
+    if (more()) request();
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
-      if (ahead < n) {
+      if (more()) {
         issue(s);
+        ++ahead;
         advance();
-        if (++ahead < n) request();
+        if (more()) request();
       }
       cp_async_commit();
     }
@@ -344,31 +377,60 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     }
   };
 
+  // A run's query rows: two (NQ = 1) or four per warp, DP / 32 consecutive values per lane. They are requested
+  // while the run before is still computed.
+  constexpr int kQRows = 8 * NQ / kWarps, kQVals = DP / 32;
+  constexpr int kQWords = C::kSplit ? kQVals : (kQVals + 1) / 2;
+  uint32_t q_raw[kQRows][kQWords];
+  auto chunk_of = [&](int hc) { return p.chunks == 1 ? 0 : hc % p.chunks; };
+  auto first_head = [&](int hc) { return (p.chunks == 1 ? hc : hc / p.chunks) * p.G + chunk_of(hc) * 8 * NQ; };
+  auto heads_of = [&](int hc) { return min(8 * NQ, p.G - chunk_of(hc) * 8 * NQ); };
+  auto request_q = [&](int seq, int hc) {
+    const int h0 = first_head(hc), have = heads_of(hc);
+#pragma unroll
+    for (int k = 0; k < kQRows; ++k) {
+      const int r = warp + k * kWarps;
+#pragma unroll
+      for (int e = 0; e < kQWords; ++e) q_raw[k][e] = 0;
+      if (r < have && lane * kQVals < p.D) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q.data) +
+            ((int64_t)seq * p.q.ts + (int64_t)(h0 + r) * p.q.hs + lane * kQVals) * (C::kSplit ? 4 : 2));
+#pragma unroll
+        for (int e = 0; e < kQWords; e += 4) {
+          if (kQWords >= 4) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + e);
+            q_raw[k][e] = y.x; q_raw[k][kQWords > 1 ? e + 1 : e] = y.y;
+            q_raw[k][kQWords > 2 ? e + 2 : e] = y.z; q_raw[k][kQWords > 3 ? e + 3 : e] = y.w;
+          } else if (kQWords == 2) {
+            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            q_raw[k][0] = y.x; q_raw[k][kQWords > 1 ? 1 : 0] = y.y;
+          } else {
+            q_raw[k][0] = *src;
+          }
+        }
+      }
+    }
+  };
+
   int stage = 0;
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < ahead; ++i) {
     cp_async_wait<kStages - 2>();
     __syncwarp();
     const uint32_t mask = meta[stage].mask, ends = meta[stage].ends;
 
     if (i == 0 || (ends & 1u)) {
       // a new run: its query rows to shared memory (16-bit, zero rows and columns as padding)
-      const Meta me = meta[stage];
-      const int chunk = p.chunks == 1 ? 0 : me.hc % p.chunks;
-      const int head = p.chunks == 1 ? me.hc : me.hc / p.chunks;
-      rows = min(8 * NQ, p.G - chunk * 8 * NQ);
-      const int h0 = head * p.G + chunk * 8 * NQ;
-      for (int r = warp; r < 8 * NQ; r += kWarps) {
-        float x[DP / 32];
+      if (i == 0) request_q(meta[stage].seq, meta[stage].hc);
+      rows = heads_of(meta[stage].hc);
+#pragma unroll
+      for (int k = 0; k < kQRows; ++k) {
+        const int r = warp + k * kWarps;
+        float x[kQVals];
         float amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < DP / 32; ++e) {
-          const int d = lane + 32 * e;
-          x[e] = 0.f;
-          if (r < rows && d < p.D) {
-            const int64_t at_q = (int64_t)me.seq * p.q.ts + (int64_t)(h0 + r) * p.q.hs + d;
-            x[e] = C::kSplit ? static_cast<const float*>(p.q.data)[at_q]
-                             : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.q.data)[at_q] << 16);
-          }
+        for (int e = 0; e < kQVals; ++e) {
+          const uint32_t w = q_raw[k][C::kSplit ? e : e / 2];
+          x[e] = C::kSplit ? __uint_as_float(w) : (e & 1) ? bf16_hi(w) : bf16_lo(w);
           amax = fmaxf(amax, fabsf(x[e]));
         }
         int up = 0;                                   // x * 2^up in f16
@@ -379,25 +441,19 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
           if (amax > 0.f && field < 255) up = 140 - max(field, 1);   // amax * 2^up in [2^13, 2^14)
           if (lane == 0) sm_c[r] = ldexpf(p.scale_log2, -up);
         }
-        uint16_t* dst = reinterpret_cast<uint16_t*>(qs) + r * C::kQPitch + lane;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(qs + (r * C::kQPitch + lane * kQVals) * 2);
 #pragma unroll
-        for (int e = 0; e < DP / 32; ++e) {
-          if (C::kFp8) {
-            const float y = ldexpf(x[e], up);
-            const __half hi = __float2half_rn(y);
-            dst[32 * e] = __half_as_ushort(hi);
-            if (C::kSplit) {
-              const float lo = y - __half2float(hi);                 // inf - inf: the high part says it all
-              dst[32 * e + C::kQB / 2] = __half_as_ushort(__float2half_rn(lo == lo ? lo : 0.f));
-            }
-          } else {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(x[e]);
-            dst[32 * e] = __bfloat16_as_ushort(hi);
-            if (C::kSplit) {
-              const float lo = x[e] - __bfloat162float(hi);
-              dst[32 * e + C::kQB / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(lo == lo ? lo : 0.f));
-            }
+        for (int e = 0; e < kQVals; e += 2) {
+          float hi[2], lo[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float y = C::kFp8 ? ldexpf(x[e + z], up) : x[e + z];
+            hi[z] = C::kFp8 ? __half2float(__float2half_rn(y)) : __bfloat162float(__float2bfloat16_rn(y));
+            lo[z] = y - hi[z];
+            if (lo[z] != lo[z]) lo[z] = 0.f;          // inf - inf: the high part says it all
           }
+          dst[e / 2] = C::kFp8 ? pack_f16(hi[0], hi[1]) : pack_bf16(hi[0], hi[1]);
+          if (C::kSplit) dst[e / 2 + C::kQB / 4] = C::kFp8 ? pack_f16(lo[0], lo[1]) : pack_bf16(lo[0], lo[1]);
         }
       }
       __syncthreads();
@@ -424,12 +480,18 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     }
 
     // the stage consumed in the last step is refilled while this one is computed
-    if (ahead < n) {
+    if (more()) {
       issue(stage == 0 ? kStages - 1 : stage - 1);
+      ++ahead;
       advance();
-      if (++ahead < n) request();
+      if (more()) request();
     }
     cp_async_commit();
+    if ((ends & 2u) && i + 1 < ahead) {
+      __syncwarp();                                   // lane 0 may have just written the next step's
+      const Meta* next = meta + (stage + 1 == kStages ? 0 : stage + 1);
+      request_q(next->seq, next->hc);
+    }
 
     if (mask != 0) {
       // this lane's row and chunk of every ldmatrix: rows 0..7 and 8..15, chunks 2x and 2x + 1
@@ -685,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       }
     }
 
-    if ((ends & 2u) || i + 1 == n) {
+    if ((ends & 2u) || i + 1 == ahead) {
       // ---- the run ends here, or this CTA's part of it: join the four warps -----------------------
       const Meta me = meta[stage];
       __syncwarp();                                   // the stage is read: it takes this warp's o
@@ -731,15 +793,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       }
       __syncthreads();
 
-      const int run0 = t0 + i - me.tile;              // the run's first tile
-      const int c_first = run0 / per_cta, c_last = (run0 + me.tiles - 1) / per_cta;
+      const int c_first = me.run0 / per_cta, c_last = (me.run0 + me.tiles - 1) / per_cta;
       const bool whole = c_first == c_last;
-      const int chunk = p.chunks == 1 ? 0 : me.hc % p.chunks;
-      const int h0 = (p.chunks == 1 ? me.hc : me.hc / p.chunks) * p.G + chunk * 8 * NQ;
+      const int h0 = first_head(me.hc);
       const int q_heads = p.Hk * p.G;
       constexpr int kSlot = 8 * NQ * (DP + 2);        // floats of a part: o, then (maximum, sum) per head
-      // a CTA has at most two parts of cut runs: slot 0 for the one it starts in, slot 1 for the one it ends in
-      auto slot_of = [&](int cta) { return p.part + (int64_t)(2 * cta + (cta == c_first && run0 != cta * per_cta ? 1 : 0)) * kSlot; };
+      // a CTA has at most two parts of cut runs: slot 1 for the one that starts in its share, slot 0 for the one before
+      auto slot_of = [&](int cta) { return p.part + (int64_t)(2 * cta + (cta == c_first ? 1 : 0)) * kSlot; };
       auto emit = [&](int q, int d, const float (&x)[4], float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint2 w;
@@ -779,16 +839,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         // through one SM. A counter belongs to its group by the group's first CTA; a run's first group may
         // share that CTA with the end of another run, so it has an array of its own.
         auto arrive_last = [&](uint32_t* counter, int parties) {
-          __threadfence();
-          __syncthreads();
+          __syncthreads();                            // every thread's part is written
           if (tid == 0) {
-            const int last = atomicAdd(counter, 1u) == (uint32_t)(parties - 1);
+            const int last = atom_add_acq_rel(counter, 1u) == (uint32_t)(parties - 1);
             if (last) *counter = 0;                   // the next call finds it zero
-            __threadfence();
-            sm_i[11] = last;
+            sm_i[12] = last;
           }
           __syncthreads();
-          return sm_i[11] != 0;
+          return sm_i[12] != 0;
         };
         auto join = [&](int from, int step, int parts, bool final) {
           for (int e0 = 0; e0 < rows * (DP / 4); e0 += kThreads) {
@@ -797,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             const bool mine = e < rows * (DP / 4) && d < p.D;
             float m = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
             if (mine) {
-              constexpr int kBatch = 8;               // parts in flight per thread
+              constexpr int kBatch = ATTN_BATCH;               // parts in flight per thread
               for (int k0 = 0; k0 < parts; k0 += kBatch) {
                 float2 ml[kBatch];
                 float4 y[kBatch];
@@ -872,10 +930,13 @@ template <typename C>
 cudaError_t launch(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
   static PerContextOnce once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemB);
+    const cudaError_t e = cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemB);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  const int64_t grid = max_tiles < plan.grid_max ? max_tiles : plan.grid_max;
+  const int64_t places = max_tiles * (1 + kRunCost);
+  const int64_t grid = places < plan.grid_max ? places : plan.grid_max;
   return launch_k(attention_kernel<C>, dim3((unsigned)grid), dim3(kThreads), C::kSmemB, stream, pdl, p);
 }
 
