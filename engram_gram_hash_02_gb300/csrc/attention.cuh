@@ -23,10 +23,11 @@
 //
 // FP8 rows (codes, one power-of-two scale per 32 values) are converted to f16 in registers (exact). A key
 // block's scale multiplies that block's fp32 partial product. The value scales join the weights before those
-// are rounded: with 2^e_j the largest scale of value row j, a second running maximum M (of s_j + e_j) gives
-// weights 2^(s_j + e_j - M + 15) that fill f16's range, and a block's own scale enters as 2^(scale - e_j), a
-// half that is exact down to 2^-24. So no spread of the rows' sizes overflows, and a weight loses bits only
-// 2^-29 below its head's largest contribution.
+// are rounded: with 2^e_j the largest scale of value row j, the running maximum is that of s_j + e_j, the
+// weights 2^(s_j + e_j - maximum + 15) fill f16's range, and a block's own scale enters as 2^(scale - e_j), a
+// half that is exact down to 2^-24; the sum takes the weights times 2^-e_j. So no spread of the rows' sizes
+// overflows, and a weight loses bits only 2^-29 below its head's largest contribution (value blocks whose scale
+// is 2^-24 below their row's largest, or below 2^-88, count as zero).
 //
 // Roundings below 32 bits: with bf16 rows P is fed as the sum of two bf16 (hi + lo, 16 bits: 2^-17); with
 // FP8 rows as f16 (2^-12, an eighth of the output's own rounding). bf16 queries enter as they are; fp32
@@ -354,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   // ---- the consumer ----------------------------------------------------------------------------
   float o[DP / 16][NQ][4];
   float m_run[NQ][2], l_run[NQ][2];
-  float u_run[NQ][2];                                 // FP8: running maximum of s + e, the units of o
   uint32_t qf[C::kQRegs ? NQ : 1][C::kQRegs ? DP / 16 : 1][C::kSplit ? 4 : 2];
   int rows = 0;                                       // query heads of this run
 
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) { m_run[nq][e] = u_run[nq][e] = -INFINITY; l_run[nq][e] = 0.f; }
+        for (int e = 0; e < 2; ++e) { m_run[nq][e] = -INFINITY; l_run[nq][e] = 0.f; }
 #pragma unroll
         for (int mt = 0; mt < DP / 16; ++mt)
 #pragma unroll
@@ -578,20 +578,18 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         }
       }
 
-      // this lane's key: e = its largest value scale, and its blocks' scales relative to that as halves, which
-      // take the place of the step's scale words ([key][2 * kWords] words). A block that holds an infinity
-      // (bytes 254 and 255) has an infinite factor and no part in e: it spoils its own 32 values only.
-      float e_own = 0.f;
+      // FP8: this lane's key has e = its largest value scale; its blocks' scales relative to that, as halves, take
+      // the place of the step's scale words ([key][2 * kWords] words). A block that holds an infinity (bytes 254
+      // and 255) has an infinite factor and no part in e: it spoils its own 32 values only.
+      int top = 63;                                   // e + 127, at least -64 + 127: the sum takes 2^-e
       if (C::kFp8) {
         uint32_t w[C::kWords], f[2 * C::kWords];
-        int top = 0;
 #pragma unroll
         for (int b = 0; b < DP / 32; ++b) {
           if ((b & 3) == 0) w[b / 4] = vw[lane * C::kWords + b / 4] & (b / 4 + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
           const int by = (int)((w[b / 4] >> (8 * (b & 3))) & 0xFFu);
           if (by < 254) top = max(top, by);
         }
-        e_own = (float)(top - 127);
 #pragma unroll
         for (int x = 0; x < 2 * C::kWords; ++x) {
           float y[2];
@@ -613,62 +611,52 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       float alpha[NQ][2];                             // what o is multiplied by
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
-        float mx[2] = {-INFINITY, -INFINITY}, ux[2] = {-INFINITY, -INFINITY};
-        float u[KT][4];
+        float mx[2] = {-INFINITY, -INFINITY};
+        float un[KT][2];                              // FP8: 2^-e of keys g and g + 8
         const float c0 = C::kFp8 ? sm_c[nq * 8 + 2 * j] : p.scale_log2;
         const float c1 = C::kFp8 ? sm_c[nq * 8 + 2 * j + 1] : p.scale_log2;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
           float(&x)[4] = t[kt][nq];
-          x[0] *= c0; x[1] *= c1; x[2] *= c0; x[3] *= c1;
+          if (C::kFp8) {
+            const int t0 = __shfl_sync(0xFFFFFFFFu, top, kt * 16 + g), t1 = __shfl_sync(0xFFFFFFFFu, top, kt * 16 + g + 8);
+            un[kt][0] = __uint_as_float((uint32_t)(254 - t0) << 23);
+            un[kt][1] = __uint_as_float((uint32_t)(254 - t1) << 23);
+            // e as a float: the integer behind 2^23
+            const float e0 = __uint_as_float(0x4B000000u + t0) - 8388735.f, e1 = __uint_as_float(0x4B000000u + t1) - 8388735.f;
+            x[0] = x[0] * c0 + e0; x[1] = x[1] * c1 + e0; x[2] = x[2] * c0 + e1; x[3] = x[3] * c1 + e1;
+          } else {
+            x[0] *= c0; x[1] *= c1; x[2] *= c0; x[3] *= c1;
+          }
           if (mask != (kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
             if (!((mask >> (kt * 16 + g)) & 1u)) x[0] = x[1] = -INFINITY;
             if (!((mask >> (kt * 16 + g + 8)) & 1u)) x[2] = x[3] = -INFINITY;
           }
           mx[0] = fmaxf(mx[0], fmaxf(x[0], x[2]));
           mx[1] = fmaxf(mx[1], fmaxf(x[1], x[3]));
-          if (C::kFp8) {
-            const float e0 = __shfl_sync(0xFFFFFFFFu, e_own, kt * 16 + g), e1 = __shfl_sync(0xFFFFFFFFu, e_own, kt * 16 + g + 8);
-            u[kt][0] = x[0] + e0; u[kt][1] = x[1] + e0; u[kt][2] = x[2] + e1; u[kt][3] = x[3] + e1;
-            ux[0] = fmaxf(ux[0], fmaxf(u[kt][0], u[kt][2]));
-            ux[1] = fmaxf(ux[1], fmaxf(u[kt][1], u[kt][3]));
-          }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int s = 4; s < 32; s <<= 1) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], s));
-            if (C::kFp8) ux[e] = fmaxf(ux[e], __shfl_xor_sync(0xFFFFFFFFu, ux[e], s));
-          }
-          const float m = fmaxf(m_run[nq][e], mx[e]);
-          const float fade = ex2_rel(m_run[nq][e], m);
-          if (!C::kFp8) {
-            alpha[nq][e] = fade;
-            moved |= m != m_run[nq][e];
-          }
+          for (int s = 4; s < 32; s <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], s));
+          // (FP8: weights up to 2^15, so the units of o and the sum are 2^(maximum - 15))
+          const float m = fmaxf(m_run[nq][e], C::kFp8 ? mx[e] - 15.f : mx[e]);
+          alpha[nq][e] = ex2_rel(m_run[nq][e], m);
+          moved |= m != m_run[nq][e];
           m_run[nq][e] = m;
           const float base = m == -INFINITY ? 0.f : m;
           float sum = 0.f;
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
-            t[kt][nq][e] = ex2(t[kt][nq][e] - base);
-            t[kt][nq][e + 2] = ex2(t[kt][nq][e + 2] - base);
-            sum += t[kt][nq][e] + t[kt][nq][e + 2];
+            float(&x)[4] = t[kt][nq];
+            x[e] = ex2(x[e] - base);
+            x[e + 2] = ex2(x[e + 2] - base);
+            if (C::kFp8)
+              sum += x[e] * un[kt][0] + x[e + 2] * un[kt][1];
+            else
+              sum += x[e] + x[e + 2];
           }
-          l_run[nq][e] = l_run[nq][e] * fade + sum;
-          if (C::kFp8) {
-            const float um = fmaxf(u_run[nq][e], ux[e]);
-            alpha[nq][e] = ex2_rel(u_run[nq][e], um);
-            moved |= um != u_run[nq][e];
-            u_run[nq][e] = um;
-            const float ubase = um == -INFINITY ? 0.f : um - 15.f;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-              t[kt][nq][e] = ex2(u[kt][e] - ubase);
-              t[kt][nq][e + 2] = ex2(u[kt][e + 2] - ubase);
-            }
-          }
+          l_run[nq][e] = l_run[nq][e] * alpha[nq][e] + sum;
         }
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
@@ -752,20 +740,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       const Meta me = meta[stage];
       __syncwarp();                                   // the stage is read: it takes this warp's o
       float* mine_o = reinterpret_cast<float*>(ring + stage * C::kStageB);
-      // FP8: o from units of 2^(u_run - 15) to those of the weights, 2^m_run
-      float frac[NQ][2];
-      int units[NQ][2];
-      if (C::kFp8) {
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float d = u_run[nq][e] == -INFINITY ? 0.f : u_run[nq][e] - m_run[nq][e];
-            const float whole = floorf(d);
-            frac[nq][e] = ex2(d - whole);
-            units[nq][e] = (int)whole - 15;
-          }
-      }
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
@@ -785,9 +759,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             const int q = nq * 8 + 2 * j + (e & 1);
             // rows of a fragment: values g and g + 8 (bf16), 2g and 2g + 1 (FP8)
             const int d = mt * 16 + (C::kFp8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
-            float x = o[mt][nq][e];
-            if (C::kFp8) x = ldexpf(x * frac[nq][e & 1], units[nq][e & 1]);
-            mine_o[q * DP + (d ^ (((q >> 1) & 3) << 3))] = x;
+            mine_o[q * DP + (d ^ (((q >> 1) & 3) << 3))] = o[mt][nq][e];
           }
         }
       }
