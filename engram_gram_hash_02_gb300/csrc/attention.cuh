@@ -43,24 +43,7 @@ namespace attn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                            // parts of a cut run that one CTA joins
-#ifndef ATTN_RUN
-#define ATTN_RUN 2
-#endif
-#ifndef C64
-#define C64 3
-#define S64 4
-#endif
-#ifndef C128
-#define C128 2
-#define S128 3
-#endif
-#ifndef ATTN_MIN
-#define ATTN_MIN 1
-#endif
-#ifndef ATTN_BATCH
-#define ATTN_BATCH 16
-#endif
-constexpr int kRunCost = ATTN_RUN, kMinPlaces = ATTN_MIN;
+constexpr int kRunCost = 2;                           // a run's fixed cost, in tiles
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -77,6 +60,12 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// two 16 x 16 matrices of bytes (row addresses from lanes 0..15 and 16..31), transposed: registers 0 and 1 hold
+// columns lane / 4 and lane / 4 + 8 of the first, rows 4 (lane % 4) .. + 3; registers 2 and 3 of the second
+__device__ __forceinline__ void ldsm8t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -107,6 +96,10 @@ __device__ __forceinline__ float ex2(float x) {
 // exp2(x - m) for m = max(x, ...): a maximum of -inf (nothing attended yet) gives 0
 __device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
 
+// CTAs per SM: what registers allow without spilling in the loop over the steps (168 with three CTAs are enough
+// only for heads of 64 in one tile of eight), and shared memory at three stages or more
+constexpr int resident_ctas(int dp, int nq) { return dp == 64 && nq == 1 ? 3 : dp <= 128 ? 2 : 1; }
+
 template <int DP_, bool kFp8_, int NQ_, bool kSplit_>
 struct Cfg {
   static constexpr int DP = DP_;                      // head_dim rounded up to 64, 128 or 256
@@ -118,15 +111,17 @@ struct Cfg {
   static constexpr int kRowB = kFp8 ? DP : 2 * DP;
   static constexpr int kWords = (DP + 127) / 128;     // scale words per row
   static constexpr int kStageB = 2 * kStep * kRowB + (kFp8 ? 2 * kStep * kWords * 4 : 0);
-  static constexpr int kCtas = DP == 64 ? C64 : DP == 128 ? C128 : 1;
-  static constexpr int kStages = DP == 64 ? S64 : DP == 128 ? S128 : 3;
+  static constexpr int kCtas = resident_ctas(DP, NQ);
+  static constexpr int kStages = DP == 64 ? 4 : 3;
   static constexpr int kRingB = kWarps * kStages * kStageB;
   static constexpr int kQPitch = DP + 8;              // 16-bit values
   static constexpr int kQB = NQ * 8 * kQPitch * 2;    // per part (high, low)
   static constexpr int kMetaB = kWarps * kStages * 32;
   static constexpr int kSmall = 1024;                 // maxima, sums, query scales, scan words
+  static constexpr int kScaleRow = 4 * kWords + 2;    // FP8, per key of a step: key block scales, e and 2^-e
+  static constexpr int kScalesB = kFp8 ? kWarps * kStep * kScaleRow * 4 : 0;
   static constexpr int kAlign = 512;                  // a row's XORed bits are zero in its stage's address
-  static constexpr int kSmemB = kAlign + kRingB + kQB * (kSplit ? 2 : 1) + kMetaB + kSmall;
+  static constexpr int kSmemB = kAlign + kRingB + kQB * (kSplit ? 2 : 1) + kMetaB + kSmall + kScalesB;
   static constexpr bool kQRegs = DP / 16 * 2 * NQ * (kSplit ? 2 : 1) <= 32;
   static_assert(NQ * 8 * DP * 4 <= kStageB, "a warp's result is joined in its own last stage");
   static_assert(kStageB % (kRowB < kAlign ? kRowB : kAlign) == 0, "stages keep the rows' alignment");
@@ -165,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   float* sm_l = small + 64;                          // [warp][16] sums
   float* sm_c = small + 128;                         // [16] softmax scale of each query row, log2 units
   int* sm_i = reinterpret_cast<int*>(small + 160);   // scan and broadcast words
+  float* key_scales = small + C::kSmall / 4 + warp * kStep * C::kScaleRow;   // (FP8) [key][4 * kWords], then [key][2]
+  float* value_scales = key_scales + kStep * 4 * C::kWords;
   const int heads = p.Hk * p.chunks;
 
   // ---- this CTA's share --------------------------------------------------------------------
@@ -194,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     if (w < warp) before += sm_i[w];
     total += sm_i[w];
   }
-  const int per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinPlaces);
+  const int per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
   const int place0 = min(total, (int)blockIdx.x * per_cta), place1 = min(total, place0 + per_cta);
   if (place0 < place1 && place0 >= before && place0 < before + mine) {
     int at = before;
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     if (mask == 0) return;                            // no keys for this warp: the stage is not read
     const uint32_t dst = ring_u + stage * C::kStageB;
     const uint32_t to = dst + lane_dst;
-    const int64_t off = live ? page * p.cache.page_b + at * p.cache.tok_b + head_off : 0;
+    const int64_t off = live ? ((int64_t)((uint64_t)(uint32_t)page * p.cache.page_u + (uint64_t)(uint32_t)at * p.cache.tok_u) << 4) + head_off : 0;
     // all rows attended and in one page: equal steps from the first one
     const int at0 = __shfl_sync(0xFFFFFFFFu, at, 0);
     if (mask == kAll && at0 + kStep <= p.cache.page_size) {
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       }
     }
     if (C::kFp8 && lane < kStep) {
-      const int64_t so = live ? page * p.cache.spage_b + at * p.cache.stok_b + shead_off : 0;
+      const int64_t so = live ? ((int64_t)((uint64_t)(uint32_t)page * p.cache.spage_u + (uint64_t)(uint32_t)at * p.cache.stok_u) << 2) + shead_off : 0;
       const uint32_t sd = dst + 2 * kStep * kRowB + lane * C::kWords * 4;
 #pragma unroll
       for (int w = 0; w < C::kWords; ++w) {
@@ -494,25 +491,70 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     }
 
     if (mask != 0) {
-      // this lane's row and chunk of every ldmatrix: rows 0..7 and 8..15, chunks 2x and 2x + 1
+      // This lane's row and chunk of every ldmatrix. bf16, keys and values: rows 0..7 and 8..15, chunks 2x and
+      // 2x + 1. FP8 keys: the key of row r of the product is kr(r), such that the transposed weights have the
+      // keys in the order in which a register of the transposed value codes holds them.
+      auto kr = [](int r) { return C::kFp8 ? ((r & 6) << 1) | (r & 1) | ((r >> 3) << 1) : r; };
       constexpr int kHi = C::kFp8 ? 4 : 3, kRow8 = C::kFp8 ? 3 : 4;
-      const int lrow = ((lane >> kRow8) & 1) * 8 + (lane & 7);
+      const int lrow = kr(((lane >> kRow8) & 1) * 8 + (lane & 7));
       const uint32_t tiles_u = (ring_u + stage * C::kStageB + lrow * kRowB) + ((((lane >> kHi) & 1) << 4) ^ swz<kRowB>(lrow));
+      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + lane) * kRowB + swz<kRowB>(lane);   // FP8 values
+      const int k0 = kr(g), k8 = kr(g + 8);           // keys of this lane's fragment rows
       constexpr int KT = kStep / 16;
       uint32_t pb[KT][NQ][C::kFp8 ? 2 : 4];            // P as the second product's operand (bf16: high, low)
       float t[KT][NQ][4];
       uint32_t* kw = reinterpret_cast<uint32_t*>(ring + stage * C::kStageB + 2 * kStep * kRowB);
       const uint32_t* vw = kw + kStep * C::kWords;
 
+      // FP8: the scales of this lane's key for all lanes. Key blocks' scales as floats; e = the largest value scale
+      // and 2^-e; value blocks' scales relative to e as halves, in the place of the step's scale words ([key][2 *
+      // kWords] words). A block that holds an infinity (bytes 254 and 255) has an infinite factor and no part in
+      // e: it spoils its own 32 values only.
+      if (C::kFp8) {
+        int top = 63;                                 // e + 127, at least -64 + 127: the sum takes 2^-e
+        uint32_t kb[C::kWords], vb[C::kWords], f[2 * C::kWords];
+#pragma unroll
+        for (int w = 0; w < C::kWords; ++w) {
+          const uint32_t used = w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu;
+          kb[w] = kw[lane * C::kWords + w] & used;
+          vb[w] = vw[lane * C::kWords + w] & used;
+          float y[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            y[z] = __uint_as_float(((kb[w] >> (8 * z)) & 0xFFu) << 23);
+            const int by = (int)((vb[w] >> (8 * z)) & 0xFFu);
+            if (by < 254) top = max(top, by);
+          }
+          *reinterpret_cast<float4*>(key_scales + (lane * C::kWords + w) * 4) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+        // e as a float: the integer behind 2^23
+        *reinterpret_cast<float2*>(value_scales + 2 * lane) =
+            make_float2(__uint_as_float(0x4B000000u + top) - 8388735.f, __uint_as_float((uint32_t)(254 - top) << 23));
+#pragma unroll
+        for (int x = 0; x < 2 * C::kWords; ++x) {
+          float y[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int by = (int)((vb[x / 2] >> (16 * (x & 1) + 8 * z)) & 0xFFu);
+            y[z] = __uint_as_float(by >= 254 ? 0x7F800000u : (uint32_t)max(127 + by - top, 0) << 23);
+          }
+          f[x] = pack_f16(y[0], y[1]);
+        }
+        __syncwarp();                                 // every lane has read the scale words
+#pragma unroll
+        for (int x = 0; x < 2 * C::kWords; ++x) kw[lane * 2 * C::kWords + x] = f[x];
+        __syncwarp();
+      }
+
       // S^T = K Q^T
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         if (C::kFp8) {
-          uint32_t w0[C::kWords], w1[C::kWords];
+          float s0[4 * C::kWords], s1[4 * C::kWords];
 #pragma unroll
           for (int w = 0; w < C::kWords; ++w) {
-            w0[w] = kw[(kt * 16 + g) * C::kWords + w] & (w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
-            w1[w] = kw[(kt * 16 + g + 8) * C::kWords + w] & (w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
+            *reinterpret_cast<float4*>(s0 + 4 * w) = *reinterpret_cast<const float4*>(key_scales + ((kt * 16 + k0) * C::kWords + w) * 4);
+            *reinterpret_cast<float4*>(s1 + 4 * w) = *reinterpret_cast<const float4*>(key_scales + ((kt * 16 + k8) * C::kWords + w) * 4);
           }
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
@@ -520,10 +562,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             for (int e = 0; e < 4; ++e) t[kt][nq][e] = 0.f;
 #pragma unroll
           for (int b = 0; b < DP / 32; ++b) {
-            uint32_t a[4];                             // codes: keys g, g + 8 (values 0..15), g, g + 8 (16..31)
+            uint32_t a[4];                             // codes: keys of rows g, g + 8 (values 0..15), the same (16..31)
             ldsm4(a, (tiles_u ^ (b << 5)) + kt * 16 * kRowB);
-            const float s0 = __uint_as_float(((w0[b / 4] >> (8 * (b & 3))) & 0xFFu) << 23);
-            const float s1 = __uint_as_float(((w1[b / 4] >> (8 * (b & 3))) & 0xFFu) << 23);
             uint32_t f[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2(a[e], f[2 * e], f[2 * e + 1]);
@@ -542,10 +582,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
                 mma<true>(acc, f[4 * e], f[4 * e + 2], f[4 * e + 1], f[4 * e + 3], q4[0], q4[1]);
                 if (C::kSplit) mma<true>(acc, f[4 * e], f[4 * e + 2], f[4 * e + 1], f[4 * e + 3], q4[2], q4[3]);
               }
-              t[kt][nq][0] += acc[0] * s0;
-              t[kt][nq][1] += acc[1] * s0;
-              t[kt][nq][2] += acc[2] * s1;
-              t[kt][nq][3] += acc[3] * s1;
+              t[kt][nq][0] += acc[0] * s0[b];
+              t[kt][nq][1] += acc[1] * s0[b];
+              t[kt][nq][2] += acc[2] * s1[b];
+              t[kt][nq][3] += acc[3] * s1[b];
             }
           }
         } else {
@@ -578,59 +618,31 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         }
       }
 
-      // FP8: this lane's key has e = its largest value scale; its blocks' scales relative to that, as halves, take
-      // the place of the step's scale words ([key][2 * kWords] words). A block that holds an infinity (bytes 254
-      // and 255) has an infinite factor and no part in e: it spoils its own 32 values only.
-      int top = 63;                                   // e + 127, at least -64 + 127: the sum takes 2^-e
-      if (C::kFp8) {
-        uint32_t w[C::kWords], f[2 * C::kWords];
-#pragma unroll
-        for (int b = 0; b < DP / 32; ++b) {
-          if ((b & 3) == 0) w[b / 4] = vw[lane * C::kWords + b / 4] & (b / 4 + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu);
-          const int by = (int)((w[b / 4] >> (8 * (b & 3))) & 0xFFu);
-          if (by < 254) top = max(top, by);
-        }
-#pragma unroll
-        for (int x = 0; x < 2 * C::kWords; ++x) {
-          float y[2];
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int by = (int)((w[x / 2] >> (16 * (x & 1) + 8 * z)) & 0xFFu);
-            y[z] = __uint_as_float(by >= 254 ? 0x7F800000u : (uint32_t)max(127 + by - top, 0) << 23);
-          }
-          f[x] = pack_f16(y[0], y[1]);
-        }
-        __syncwarp();                                 // every lane has read the scale words
-#pragma unroll
-        for (int x = 0; x < 2 * C::kWords; ++x) kw[lane * 2 * C::kWords + x] = f[x];
-        __syncwarp();
-      }
-
       // softmax over the step's keys, for each of this lane's two heads per tile
       bool moved = false;
       float alpha[NQ][2];                             // what o is multiplied by
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
         float mx[2] = {-INFINITY, -INFINITY};
-        float un[KT][2];                              // FP8: 2^-e of keys g and g + 8
+        float un[KT][2];                              // FP8: 2^-e of this lane's two keys
         const float c0 = C::kFp8 ? sm_c[nq * 8 + 2 * j] : p.scale_log2;
         const float c1 = C::kFp8 ? sm_c[nq * 8 + 2 * j + 1] : p.scale_log2;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
           float(&x)[4] = t[kt][nq];
           if (C::kFp8) {
-            const int t0 = __shfl_sync(0xFFFFFFFFu, top, kt * 16 + g), t1 = __shfl_sync(0xFFFFFFFFu, top, kt * 16 + g + 8);
-            un[kt][0] = __uint_as_float((uint32_t)(254 - t0) << 23);
-            un[kt][1] = __uint_as_float((uint32_t)(254 - t1) << 23);
-            // e as a float: the integer behind 2^23
-            const float e0 = __uint_as_float(0x4B000000u + t0) - 8388735.f, e1 = __uint_as_float(0x4B000000u + t1) - 8388735.f;
+            const float2 v0 = *reinterpret_cast<const float2*>(value_scales + 2 * (kt * 16 + k0));
+            const float2 v1 = *reinterpret_cast<const float2*>(value_scales + 2 * (kt * 16 + k8));
+            const float e0 = v0.x, e1 = v1.x;
+            un[kt][0] = v0.y;
+            un[kt][1] = v1.y;
             x[0] = x[0] * c0 + e0; x[1] = x[1] * c1 + e0; x[2] = x[2] * c0 + e1; x[3] = x[3] * c1 + e1;
           } else {
             x[0] *= c0; x[1] *= c1; x[2] *= c0; x[3] *= c1;
           }
           if (mask != (kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
-            if (!((mask >> (kt * 16 + g)) & 1u)) x[0] = x[1] = -INFINITY;
-            if (!((mask >> (kt * 16 + g + 8)) & 1u)) x[2] = x[3] = -INFINITY;
+            if (!((mask >> (kt * 16 + k0)) & 1u)) x[0] = x[1] = -INFINITY;
+            if (!((mask >> (kt * 16 + k8)) & 1u)) x[2] = x[3] = -INFINITY;
           }
           mx[0] = fmaxf(mx[0], fmaxf(x[0], x[2]));
           mx[1] = fmaxf(mx[1], fmaxf(x[1], x[3]));
@@ -688,48 +700,52 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       }
 
       // O^T += V^T P^T
+      if (C::kFp8) {
+        uint32_t sc[KT][4][2 * C::kWords];            // block scales of keys 4j .. 4j + 3
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        if (C::kFp8) {
-          uint32_t s0[2][2 * C::kWords], s1[2][2 * C::kWords];   // block scales of keys 2j, 2j + 1 (+ 0 and + 8)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-          for (int x = 0; x < 2 * C::kWords; ++x) {
-            s0[0][x] = kw[(kt * 16 + 2 * j) * 2 * C::kWords + x];
-            s0[1][x] = kw[(kt * 16 + 2 * j + 1) * 2 * C::kWords + x];
-            s1[0][x] = kw[(kt * 16 + 2 * j + 8) * 2 * C::kWords + x];
-            s1[1][x] = kw[(kt * 16 + 2 * j + 9) * 2 * C::kWords + x];
-          }
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int b = 0; b < DP / 32; ++b) {
-            uint32_t a[4];                             // pairs of values: keys 0..7, 8..15 (values 0..15), the same of 16..31
-            ldsm4t(a, (tiles_u ^ (b << 5)) + (kStep + kt * 16) * kRowB);
-            const uint32_t y0 = __byte_perm(s0[0][b / 2], s0[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
-            const uint32_t y1 = __byte_perm(s1[0][b / 2], s1[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
-            uint32_t f[8];
+            for (int x = 0; x < 2 * C::kWords; ++x) sc[kt][k][x] = kw[(kt * 16 + 4 * j + k) * 2 * C::kWords + x];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // (value 2g of both keys, value 2g + 1 of both)
-              e4m3x4_to_f16x2(__byte_perm(a[e], 0u, 0x3120), f[2 * e], f[2 * e + 1]);
-            }
+        for (int b = 0; b < DP / 32; ++b) {
+          uint32_t ps[KT][NQ][2];                     // the weights times the block's scales
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            const uint32_t y0 = __byte_perm(sc[kt][0][b / 2], sc[kt][1][b / 2], (b & 1) ? 0x7632 : 0x5410);
+            const uint32_t y1 = __byte_perm(sc[kt][2][b / 2], sc[kt][3][b / 2], (b & 1) ? 0x7632 : 0x5410);
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
               const __half2 p0 = __hmul2(*reinterpret_cast<const __half2*>(&pb[kt][nq][0]), *reinterpret_cast<const __half2*>(&y0));
               const __half2 p1 = __hmul2(*reinterpret_cast<const __half2*>(&pb[kt][nq][1]), *reinterpret_cast<const __half2*>(&y1));
-              const uint32_t b0w = *reinterpret_cast<const uint32_t*>(&p0), b1w = *reinterpret_cast<const uint32_t*>(&p1);
-              mma<true>(o[2 * b][nq], f[0], f[1], f[2], f[3], b0w, b1w);
-              mma<true>(o[2 * b + 1][nq], f[4], f[5], f[6], f[7], b0w, b1w);
+              ps[kt][nq][0] = *reinterpret_cast<const uint32_t*>(&p0);
+              ps[kt][nq][1] = *reinterpret_cast<const uint32_t*>(&p1);
             }
           }
-        } else {
 #pragma unroll
-          for (int mt = 0; mt < DP / 16; ++mt) {
-            uint32_t a[4];                             // values 0..7, 8..15 (keys 0..7), the same of keys 8..15
-            ldsm4t(a, (tiles_u ^ (mt << 5)) + kStep * kRowB);
+          for (int mt = 2 * b; mt < 2 * b + 2; ++mt) {
+            uint32_t a[4];                            // codes of values g, g + 8: keys 4j .. 4j + 3 of 0..15, of 16..31
+            ldsm8t(a, codes_u ^ (mt << 4));
 #pragma unroll
-            for (int nq = 0; nq < NQ; ++nq) {
-              mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[kt][nq][0], pb[kt][nq][1]);
-              mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[kt][nq][C::kFp8 ? 0 : 2], pb[kt][nq][C::kFp8 ? 1 : 3]);
+            for (int kt = 0; kt < KT; ++kt) {
+              uint32_t f[4];
+              e4m3x4_to_f16x2(a[2 * kt], f[0], f[2]);
+              e4m3x4_to_f16x2(a[(2 * kt + 1) & 3], f[1], f[3]);
+#pragma unroll
+              for (int nq = 0; nq < NQ; ++nq) mma<true>(o[mt][nq], f[0], f[1], f[2], f[3], ps[kt][nq][0], ps[kt][nq][1]);
             }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt) {
+          uint32_t a[4];                               // values 0..7, 8..15 (keys 0..7), the same of keys 8..15
+          ldsm4t(a, (tiles_u ^ (mt << 5)) + kStep * kRowB);
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq) {
+            mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[0][nq][0], pb[0][nq][1]);
+            mma<false>(o[mt][nq], a[0], a[1], a[2], a[3], pb[0][nq][C::kFp8 ? 0 : 2], pb[0][nq][C::kFp8 ? 1 : 3]);
           }
         }
       }
@@ -757,8 +773,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int q = nq * 8 + 2 * j + (e & 1);
-            // rows of a fragment: values g and g + 8 (bf16), 2g and 2g + 1 (FP8)
-            const int d = mt * 16 + (C::kFp8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
+            const int d = mt * 16 + g + 8 * (e >> 1);
             mine_o[q * DP + (d ^ (((q >> 1) & 3) << 3))] = o[mt][nq][e];
           }
         }
@@ -827,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             const bool mine = e < rows * (DP / 4) && d < p.D;
             float m = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
             if (mine) {
-              constexpr int kBatch = ATTN_BATCH;               // parts in flight per thread
+              constexpr int kBatch = 16;               // parts in flight per thread
               for (int k0 = 0; k0 < parts; k0 += kBatch) {
                 float2 ml[kBatch];
                 float4 y[kBatch];

@@ -22,6 +22,8 @@ struct CacheRef {
   uint8_t *ks, *vs;            // scale words (FP8 only)
   int64_t page_b, head_b, tok_b;
   int64_t spage_b, shead_b, stok_b;
+  uint32_t page_u, tok_u;      // page_b and tok_b in units of 16 bytes
+  uint32_t spage_u, stok_u;    // spage_b and stok_b in units of 4 bytes
   int64_t slots;               // num_pages * page_size
   int64_t num_pages;
   int32_t page_size, fp8;

@@ -93,6 +93,11 @@ int check_cache(const char* fn, const EngramKVCache* c, CacheRef* to) {
   to->page_b = c->page_stride * bytes;
   to->head_b = c->head_stride * bytes;
   to->tok_b = c->token_stride * bytes;
+  ENGRAM_CHECK_ARG(to->page_b / 16 < (int64_t)1 << 32 && to->tok_b / 16 < (int64_t)1 << 32,
+                   "%s: the cache's page and token strides must be below 2^36 bytes", fn);
+  to->page_u = (uint32_t)(to->page_b / 16);
+  to->tok_u = (uint32_t)(to->tok_b / 16);
+  to->spage_u = to->stok_u = 0;
   to->ks = to->vs = nullptr;
   to->spage_b = to->shead_b = to->stok_b = 0;
   if (fp8) {
@@ -106,6 +111,10 @@ int check_cache(const char* fn, const EngramKVCache* c, CacheRef* to) {
     to->spage_b = c->scale_page_stride;
     to->shead_b = c->scale_head_stride;
     to->stok_b = c->scale_token_stride;
+    ENGRAM_CHECK_ARG(to->spage_b / 4 < (int64_t)1 << 32 && to->stok_b / 4 < (int64_t)1 << 32,
+                     "%s: the scale page and token strides must be below 2^34 bytes", fn);
+    to->spage_u = (uint32_t)(to->spage_b / 4);
+    to->stok_u = (uint32_t)(to->stok_b / 4);
   }
   to->num_pages = c->num_pages;
   to->page_size = c->page_size;

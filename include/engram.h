@@ -475,7 +475,8 @@ typedef struct EngramHeads {
  * (page, head, place) is at k (or v) + page*page_stride + head*head_stride + place*token_stride, strides
  * in values (bf16 or codes), the same for k and v; its scale words likewise with the scale strides in
  * bytes. Any order of the axes, any padding: k, v and the strides are multiples of 16 bytes, scales and
- * their strides multiples of 4. Offsets are 64-bit.
+ * their strides multiples of 4. Offsets are 64-bit; page and token strides are below 2^36 bytes (2^34 for
+ * scales).
  */
 typedef struct EngramKVCache {
   int32_t format;            /* EngramCacheFmt */
