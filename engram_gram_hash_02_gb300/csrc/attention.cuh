@@ -164,56 +164,90 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   float* value_scales = key_scales + kStep * 4 * C::kWords;
   const int heads = p.Hk * p.chunks;
 
+  if (!p.lens_ready) pdl_wait();
+
   // ---- this CTA's share --------------------------------------------------------------------
   // A run (a sequence's tiles for one key head and group of query heads) takes kRunCost + tiles places in a
   // row of all runs; CTA i takes the tiles at places [i * per_cta, (i + 1) * per_cta).
   auto tiles_of = [&](int raw) { return (attended(clamp_len(raw, p.cap), p.window) + C::kTile - 1) / C::kTile; };
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = tid * per, b1 = min(p.B, b0 + per);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
+  int total, place0, place1, per_cta;
+  int seq = 0, hc = 0, tile = 0, run0 = 0;            // the first tile of the share, and its run's first place
+  auto divide = [&] {
+    per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+    place0 = min(total, (int)blockIdx.x * per_cta);
+    place1 = min(total, place0 + per_cta);
+  };
+  auto locate = [&](int b, int at, int tiles) {       // place0 lies in sequence b, whose places start at `at`
+    const int run = (place0 - at) / (tiles + kRunCost);
+    seq = b;
+    hc = run;
+    run0 = at + run * (tiles + kRunCost) + kRunCost;
+    tile = max(place0 - run0, 0);
+  };
+  auto places_of = [&](int tiles) { return tiles > 0 ? (tiles + kRunCost) * heads : 0; };
+  auto read_len = [&](int b) {
     const int raw = __ldg(p.lens + b);
     if (blockIdx.x == 0 && (raw < 0 || raw > p.cap) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
-    const int tiles = tiles_of(raw);
-    mine += tiles > 0 ? (tiles + kRunCost) * heads : 0;
-  }
-  int scan = mine;
+    return raw;
+  };
+  if (p.B <= 32) {                                    // every warp for itself: no barrier before the first copy
+    const int tiles = lane < p.B ? tiles_of(read_len(lane)) : 0;
+    int scan = places_of(tiles);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if (lane >= o) scan += y;
-  }
-  if (lane == 31) sm_i[warp] = scan;
-  __syncthreads();
-  int total = 0, before = scan - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm_i[w];
-    total += sm_i[w];
-  }
-  const int per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
-  const int place0 = min(total, (int)blockIdx.x * per_cta), place1 = min(total, place0 + per_cta);
-  if (place0 < place1 && place0 >= before && place0 < before + mine) {
-    int at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int tiles = tiles_of(__ldg(p.lens + b));
-      const int places = tiles > 0 ? (tiles + kRunCost) * heads : 0;
-      if (place0 < at + places) {
-        const int run = (place0 - at) / (tiles + kRunCost);
-        sm_i[8] = b;
-        sm_i[9] = run;
-        sm_i[10] = max((place0 - at) - run * (tiles + kRunCost) - kRunCost, 0);
-        sm_i[11] = at + run * (tiles + kRunCost) + kRunCost;   // the run's first tile
-        break;
-      }
-      at += places;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+      if (lane >= o) scan += y;
     }
+    total = __shfl_sync(0xFFFFFFFFu, scan, 31);
+    divide();
+    const int b = __ffs(__ballot_sync(0xFFFFFFFFu, scan > place0)) - 1;   // none past the end
+    if (b >= 0) locate(b, __shfl_sync(0xFFFFFFFFu, scan - places_of(tiles), b), __shfl_sync(0xFFFFFFFFu, tiles, b));
+  } else {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = tid * per, b1 = min(p.B, b0 + per);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += places_of(tiles_of(read_len(b)));
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    if (lane == 31) sm_i[warp] = scan;
+    __syncthreads();
+    total = 0;
+    int before = scan - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm_i[w];
+      total += sm_i[w];
+    }
+    divide();
+    if (place0 < place1 && place0 >= before && place0 < before + mine) {
+      int at = before;
+      for (int b = b0; b < b1; ++b) {
+        const int tiles = tiles_of(__ldg(p.lens + b));
+        if (place0 < at + places_of(tiles)) {
+          locate(b, at, tiles);
+          sm_i[8] = seq;
+          sm_i[9] = hc;
+          sm_i[10] = tile;
+          sm_i[11] = run0;
+          break;
+        }
+        at += places_of(tiles);
+      }
+    }
+    __syncthreads();
+    seq = sm_i[8];
+    hc = sm_i[9];
+    tile = sm_i[10];
+    run0 = sm_i[11];
   }
-  __syncthreads();
-  pdl_wait();
+  if (p.lens_ready) pdl_wait();
 
   // ---- the producer: one tile after another ------------------------------------------------------
-  int seq = sm_i[8], hc = sm_i[9], tile = sm_i[10], run0 = sm_i[11], first = 0, end = 0, tiles = 0;
+  int first = 0, end = 0, tiles = 0;
   int64_t head_off = 0, shead_off = 0;
   auto enter_head = [&] {
     const int head = p.chunks == 1 ? hc : hc / p.chunks;

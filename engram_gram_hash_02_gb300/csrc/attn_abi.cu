@@ -314,7 +314,7 @@ int engram_paged_attention(const EngramKVCache* cache, const EngramPagedSeqs* se
   if (rc) return rc;
   if (seqs->batch == 0) return ENGRAM_OK;
   a.p.err = err_flag;
-  return run_attention(fn, a, static_cast<cudaStream_t>(stream), false);
+  return run_attention(fn, a, static_cast<cudaStream_t>(stream), true);
 }
 
 int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q,
@@ -356,6 +356,7 @@ int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, 
   const cudaError_t e = launch_qkv(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, fn);
   a.p.q = p.q_out;
+  a.p.lens_ready = 1;
   a.p.err = err_flag;
   return run_attention(fn, a, static_cast<cudaStream_t>(stream), true);
 }

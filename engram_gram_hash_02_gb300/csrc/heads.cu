@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
 // flight, and every store of the warp is a run of full sectors.
 template <int kLanes, bool kFp8, int kRows>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvReadParams p) {
+  pdl_wait();
   const int sub = threadIdx.x & (kLanes - 1);
   const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
   const int groups = (p.heads + kRows - 1) / kRows;
@@ -383,7 +384,7 @@ cudaError_t go(QkvParams p, cudaStream_t stream) {
   p.div_q = make_fastdiv((uint32_t)max((p.q.heads + kRows - 1) / kRows, 1));
   p.div_kv = make_fastdiv((uint32_t)max((p.k.heads + kRows - 1) / kRows, 1));   // v has k's heads
   p.inv_d = 1.f / (float)p.D;
-  return launch_k(qkv_kernel<kLanes, kF32, kRows>, dim3((unsigned)(nq + nk + nv)), dim3(kThreads), 0, stream, false, p);
+  return launch_k(qkv_kernel<kLanes, kF32, kRows>, dim3((unsigned)(nq + nk + nv)), dim3(kThreads), 0, stream, true, p);
 }
 
 template <int kLanes, bool kF32>
@@ -408,7 +409,7 @@ cudaError_t go_read(KvReadParams p, cudaStream_t stream) {
   p.div_token = make_fastdiv((uint32_t)(2 * groups));
   const int64_t blocks = (p.T * 2 * groups * kLanes + kThreads - 1) / kThreads;
   if (blocks >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-  return launch_k(kv_read_kernel<kLanes, kFp8, kRows>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, false, p);
+  return launch_k(kv_read_kernel<kLanes, kFp8, kRows>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, true, p);
 }
 
 template <bool kFp8, int kRows>
