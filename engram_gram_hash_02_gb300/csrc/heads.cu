@@ -11,8 +11,8 @@
 //
 // Bound by HBM: a row is read once and written once. A row is held by 8, 16 or 32 lanes, 8 values each, so a
 // norm is a few shuffles. Measured on a GB300 (share of the 6.78 TB/s of a plain copy): 32768 tokens of 32 + 8
-// heads of 128 normed and turned in 111 us, 6.15 TB/s (0.91; issue slots 76 % busy); 8 + 8 heads written as FP8
-// in 36 us (0.84), as bf16 in 41 us (0.96); read back in 34 us (0.88) and 41 us (0.96).
+// heads of 128 normed and turned in 110 us, 6.2 TB/s (0.92; issue slots 76 % busy); 8 + 8 heads written as FP8
+// in 35 us (0.85), as bf16 in 41 us (0.96); read back in 34 us (0.88) and 41 us (0.96).
 #include "attn.cuh"
 
 namespace engram {
@@ -102,9 +102,10 @@ __device__ __forceinline__ void wait_rows(int n) {
 // All rows of a thread are requested at once by cp.async into places of its own in shared memory, so their
 // bytes in flight do not depend on registers, and the angles are fetched behind them. Norm and turn are
 //   out_i = r * (x_i * A_i + y_i * B_i),  r = 1 / sqrt(mean(x^2) + eps),  y_i the other value of x_i's pair,
-// with A_i = w_i cos, B_i = -+ w_y sin formed once per token; y comes from the partner lane's place.
+// with A_i = w_i cos, B_i = -+ w_y sin formed once per token; y comes from the partner lane's place. Nine CTAs
+// per SM (56 registers): with eight 118 us instead of 110 for 32768 tokens of 32 + 8 heads, with ten spills, 133.
 template <int kLanes, bool kF32, int kRows>
-__global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvParams p) {
+__global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant__ QkvParams p) {
   constexpr unsigned kWarp = 0xFFFFFFFFu;
   constexpr int kBytes = kF32 ? 4 : 2;
   constexpr int kParts = kF32 ? 2 : 1;                // 16-byte chunks per lane
@@ -129,6 +130,10 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
   const bool live = there && d0 < p.D;
   const int rows = live ? min(in.heads - h0, kRows) : 0;
 
+  const int half = p.nr.R >> 1;
+  const int r0 = d0 - p.nr.start;
+  const bool turned = turn && live && r0 >= 0 && r0 < p.nr.R;
+  int64_t pos = turned ? __ldg(p.positions + t) : 0;  // (its angles are two loads away)
   // a group's lanes copy consecutive chunks; chunk c of a row lies at c ^ (c / 8 & 1), so that reads of two
   // chunks per lane (fp32) meet no bank twice
   auto chunk_at = [&](int c) { return (tid - sub) * kParts + (kF32 ? c ^ ((c >> 3) & 1) : c); };
@@ -151,16 +156,12 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
 
   // A and B of this thread's 8 values. A value of a second half takes + sin times its partner, one of a first
   // half - sin.
-  const int half = p.nr.R >> 1;
-  const int r0 = d0 - p.nr.start;
-  const bool turned = turn && live && r0 >= 0 && r0 < p.nr.R;
   const bool pairs = p.nr.interleaved;
   int other = sub;
   float A[8], B[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) { A[i] = 1.f; B[i] = 0.f; }
   if (turned) {
-    int64_t pos = __ldg(p.positions + t);
     if (pos < 0 || pos >= p.nr.rows) {
       if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_POSITION);
       pos = pos < 0 ? 0 : p.nr.rows - 1;
