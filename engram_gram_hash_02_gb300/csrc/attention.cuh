@@ -40,8 +40,7 @@
 namespace engram {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kRings = 4;                             // of a CTA: its tile is a step of each
 constexpr int kGroup = 16;                            // parts of a cut run that one CTA joins
 constexpr int kRunCost = 2;                           // a run's fixed cost, in tiles
 
@@ -67,6 +66,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void ldsm8t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// the first of the two only
+__device__ __forceinline__ void ldsm8t_one(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+  r[2] = r[3] = 0;
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -96,34 +100,48 @@ __device__ __forceinline__ float ex2(float x) {
 // exp2(x - m) for m = max(x, ...): a maximum of -inf (nothing attended yet) gives 0
 __device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
 
-// CTAs per SM: what registers allow without spilling in the loop over the steps (168 with three CTAs are enough
-// only for heads of 64 in one tile of eight), and shared memory at three stages or more
-constexpr int resident_ctas(int dp, int nq) { return dp == 64 && nq == 1 ? 3 : dp <= 128 ? 2 : 1; }
+// How a kernel for heads of up to dp (64, 128 or 256) and `tiles` tiles of 8 query heads runs. Registers bound it:
+// a warp needs some 230 for its o, queries and the fragments in flight (spilled values come back from L2, shared
+// memory leaves no L1), so 8 warps per SM (12 for heads of 64 in one tile). Two tiles of heads of 256 do not fit
+// one warp: two warps then share a ring, a tile each.
+constexpr int team_warps(int dp, int tiles) { return dp == 256 && tiles == 2 ? 2 : 1; }
+// FP8 steps of 32 keys (the fixed part of a step is a third of its instructions), 16 where a ring of 32 would leave
+// room for four warps only: 64 sequences of up to 4096 tokens, 8 heads of 256 per key head, 36.5 us (40.6 with 32)
+constexpr int step_keys(bool fp8, int dp, int tiles) { return fp8 && !(dp == 256 && tiles == 1) ? 32 : 16; }
+constexpr int resident_ctas(bool fp8, int dp, int tiles) {
+  return dp == 64 && tiles == 1 ? 3 : dp <= 128 || (fp8 && tiles == 1) ? 2 : 1;
+}
 
-template <int DP_, bool kFp8_, int NQ_, bool kSplit_>
+template <int DP_, bool kFp8_, int kTiles_, bool kSplit_>
 struct Cfg {
   static constexpr int DP = DP_;                      // head_dim rounded up to 64, 128 or 256
   static constexpr bool kFp8 = kFp8_;
-  static constexpr int NQ = NQ_;                      // tiles of 8 query heads
+  static constexpr int kTiles = kTiles_;              // tiles of 8 query heads per CTA
+  static constexpr int kTeam = team_warps(DP, kTiles);// warps that share a ring
+  static constexpr int NQ = kTiles / kTeam;           // tiles per warp
+  static constexpr int kHeads = 8 * kTiles;
+  static constexpr int kWarps = kRings * kTeam;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr bool kSplit = kSplit_;             // fp32 queries: high and low parts
-  static constexpr int kStep = kFp8 ? 32 : 16;        // keys per warp and step
-  static constexpr int kTile = kWarps * kStep;
+  static constexpr int kStep = step_keys(kFp8, DP, kTiles);   // keys per ring and step
+  static constexpr int kTile = kRings * kStep;
   static constexpr int kRowB = kFp8 ? DP : 2 * DP;
   static constexpr int kWords = (DP + 127) / 128;     // scale words per row
   static constexpr int kStageB = 2 * kStep * kRowB + (kFp8 ? 2 * kStep * kWords * 4 : 0);
-  static constexpr int kCtas = resident_ctas(DP, NQ);
+  static constexpr int kCtas = resident_ctas(kFp8, DP, kTiles);   // per SM
   static constexpr int kStages = DP == 64 ? 4 : 3;
-  static constexpr int kRingB = kWarps * kStages * kStageB;
+  static constexpr int kRingB = kRings * kStages * kStageB;
   static constexpr int kQPitch = DP + 8;              // 16-bit values
-  static constexpr int kQB = NQ * 8 * kQPitch * 2;    // per part (high, low)
-  static constexpr int kMetaB = kWarps * kStages * 32;
+  static constexpr int kQB = kHeads * kQPitch * 2;    // per part (high, low)
+  static constexpr int kMetaB = kRings * kStages * 32;
   static constexpr int kSmall = 1024;                 // maxima, sums, query scales, scan words
-  static constexpr int kScaleRow = 4 * kWords + 2;    // FP8, per key of a step: key block scales, e and 2^-e
-  static constexpr int kScalesB = kFp8 ? kWarps * kStep * kScaleRow * 4 : 0;
+  // FP8, per ring and key of a step: key block scales, e and 2^-e, and (two warps per ring) value block scales
+  static constexpr int kScaleRow = 4 * kWords + 2 + (kTeam == 2 ? 2 * kWords : 0);
+  static constexpr int kScalesB = kFp8 ? kRings * kStep * kScaleRow * 4 : 0;
   static constexpr int kAlign = 512;                  // a row's XORed bits are zero in its stage's address
   static constexpr int kSmemB = kAlign + kRingB + kQB * (kSplit ? 2 : 1) + kMetaB + kSmall + kScalesB;
   static constexpr bool kQRegs = DP / 16 * 2 * NQ * (kSplit ? 2 : 1) <= 32;
-  static_assert(NQ * 8 * DP * 4 <= kStageB, "a warp's result is joined in its own last stage");
+  static_assert(kHeads * DP * 4 <= kStageB, "a ring's result is joined in its own last stage");
   static_assert(kStageB % (kRowB < kAlign ? kRowB : kAlign) == 0, "stages keep the rows' alignment");
 };
 
@@ -146,22 +164,32 @@ __device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 
 __device__ __forceinline__ int attended(int len, int window) { return window > 0 && len > window ? window : len; }
 
 template <typename C>
-__global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const AttnParams p) {
   constexpr int DP = C::DP, NQ = C::NQ, kStages = C::kStages, kStep = C::kStep, kRowB = C::kRowB;
+  constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kTeam = C::kTeam, kHeads = C::kHeads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & (C::kAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, j = lane & 3;             // fragment row and column pair
-  uint8_t* ring = smem + warp * kStages * C::kStageB;
+  const int my_ring = warp / kTeam, rank = warp % kTeam;
+  uint8_t* ring = smem + my_ring * kStages * C::kStageB;
   uint8_t* qs = smem + C::kRingB;
-  Meta* meta = reinterpret_cast<Meta*>(qs + C::kQB * (C::kSplit ? 2 : 1)) + warp * kStages;
+  Meta* meta = reinterpret_cast<Meta*>(qs + C::kQB * (C::kSplit ? 2 : 1)) + my_ring * kStages;
   float* small = reinterpret_cast<float*>(qs + C::kQB * (C::kSplit ? 2 : 1) + C::kMetaB);
-  float* sm_m = small;                               // [warp][16] maxima (log2 units)
-  float* sm_l = small + 64;                          // [warp][16] sums
+  float* sm_m = small;                               // [ring][16] maxima (log2 units)
+  float* sm_l = small + 64;                          // [ring][16] sums
   float* sm_c = small + 128;                         // [16] softmax scale of each query row, log2 units
   int* sm_i = reinterpret_cast<int*>(small + 160);   // scan and broadcast words
-  float* key_scales = small + C::kSmall / 4 + warp * kStep * C::kScaleRow;   // (FP8) [key][4 * kWords], then [key][2]
+  float* key_scales = small + C::kSmall / 4 + my_ring * kStep * C::kScaleRow;   // (FP8) [key][4 * kWords], then [key][2]
   float* value_scales = key_scales + kStep * 4 * C::kWords;
+  uint32_t* own_factors = reinterpret_cast<uint32_t*>(value_scales + kStep * 2);   // (two warps per ring)
+  // the warps of a ring: what each has copied, read or written so far is done
+  auto sync_ring = [&] {
+    if (kTeam == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + my_ring), "n"(32 * kTeam) : "memory");
+  };
   const int heads = p.Hk * p.chunks;
 
   if (!p.lens_ready) pdl_wait();
@@ -279,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   int page = -1, at = 0;
   bool inside = false;
   auto request = [&] {
-    const int pos = first + tile * C::kTile + warp * kStep + (lane & (kStep - 1));
+    const int pos = first + tile * C::kTile + my_ring * kStep + (lane & (kStep - 1));
     inside = pos < end;
     page = -1;
     if (inside) {
@@ -288,18 +316,19 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       page = __ldg(p.table + (int64_t)seq * p.table_stride + n);
     }
   };
-  // a lane copies chunk c of rows sub, sub + kRows, ...
+  // a lane copies chunk c of rows sub, sub + kRows, ... (the warps of a ring take turns at these passes)
   constexpr int kChunks = kRowB / 16, kRows = 32 / kChunks;
   const int c = lane & (kChunks - 1), sub = lane / kChunks;
   const bool in_row = c * 16 < (C::kFp8 ? p.D : 2 * p.D);
   const uint32_t lane_dst = (uint32_t)(sub * kRowB) + ((uint32_t)(c << 4) ^ swz<kRowB>(sub));
   const uint32_t ring_u = smem_u32(ring);
+  auto my_pass = [&](int r0) { return kTeam == 1 || (r0 / kRows) % kTeam == rank; };
   auto issue = [&](int stage) {
     const bool live = inside && page >= 0 && page < p.cache.num_pages;
     if (inside && !live && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
     constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu;
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live) & kAll;
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       Meta m;
       m.mask = mask; m.ends = (tile == 0 ? 1u : 0u) | (tile + 1 == tiles ? 2u : 0u);
       m.seq = seq; m.hc = hc; m.run0 = run0; m.tiles = tiles;
@@ -318,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         if (p.cache.tok_b == kRowB) {                 // the steps are immediates
 #pragma unroll
           for (int r0 = 0; r0 < kStep; r0 += kRows) {
+            if (!my_pass(r0)) continue;
             cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp + r0 * kRowB);
             cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp + r0 * kRowB);
           }
@@ -325,8 +355,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
           const int64_t step = kRows * p.cache.tok_b;
 #pragma unroll
           for (int r0 = 0; r0 < kStep; r0 += kRows) {
-            cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp);
-            cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp);
+            if (my_pass(r0)) {
+              cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp);
+              cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp);
+            }
             kp += step;
             vp += step;
           }
@@ -338,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
         const int r = r0 + sub;
         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + c * 16;
         const bool row_live = (mask >> r) & 1u;
-        if (in_row) {
+        if (in_row && my_pass(r0)) {
           cp_async16_or_zero((to ^ swz<kRowB>(r0)) + r0 * kRowB, p.cache.k + o, row_live);
           cp_async16_or_zero((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, p.cache.v + o, row_live);
         }
@@ -349,14 +381,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       const uint32_t sd = dst + 2 * kStep * kRowB + lane * C::kWords * 4;
 #pragma unroll
       for (int w = 0; w < C::kWords; ++w) {
-        cp_async4_or_zero(sd + 4 * w, p.cache.ks + so + 4 * w, live);
-        cp_async4_or_zero(sd + kStep * C::kWords * 4 + 4 * w, p.cache.vs + so + 4 * w, live);
+        if (rank == 0) cp_async4_or_zero(sd + 4 * w, p.cache.ks + so + 4 * w, live);
+        if (rank == kTeam - 1) cp_async4_or_zero(sd + kStep * C::kWords * 4 + 4 * w, p.cache.vs + so + 4 * w, live);
       }
     }
   };
   // rows narrower than DP: the products run over their pad, which is zero in every stage
   auto clear_pad = [&](int stage) {
-    for (int r = sub; r < 2 * kStep; r += kRows)
+    for (int r = sub + rank * kRows; r < 2 * kStep; r += kTeam * kRows)
       if (!in_row) *reinterpret_cast<uint4*>(ring + stage * C::kStageB + r * kRowB + ((uint32_t)(c << 4) ^ swz<kRowB>(r))) = make_uint4(0, 0, 0, 0);
   };
   const bool padded = p.D < DP;
@@ -390,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   int rows = 0;                                       // query heads of this run
 
   auto q_frag = [&](int nq, int ks, uint32_t (&b)[4]) {
-    const uint8_t* row = qs + ((nq * 8 + g) * C::kQPitch + ks * 16) * 2;
+    const uint8_t* row = qs + (((rank * NQ + nq) * 8 + g) * C::kQPitch + ks * 16) * 2;
     if (C::kFp8) {                                    // the pairs of values a lane's four codes hold
       const uint2 hi = *reinterpret_cast<const uint2*>(row + 8 * j);
       b[0] = hi.x; b[1] = hi.y;
@@ -408,14 +440,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     }
   };
 
-  // A run's query rows: two (NQ = 1) or four per warp, DP / 32 consecutive values per lane. They are requested
+  // A run's query rows: two or four per warp, DP / 32 consecutive values per lane. They are requested
   // while the run before is still computed.
-  constexpr int kQRows = 8 * NQ / kWarps, kQVals = DP / 32;
+  constexpr int kQRows = kHeads / kWarps, kQVals = DP / 32;
   constexpr int kQWords = C::kSplit ? kQVals : (kQVals + 1) / 2;
   uint32_t q_raw[kQRows][kQWords];
   auto chunk_of = [&](int hc) { return p.chunks == 1 ? 0 : hc % p.chunks; };
-  auto first_head = [&](int hc) { return (p.chunks == 1 ? hc : hc / p.chunks) * p.G + chunk_of(hc) * 8 * NQ; };
-  auto heads_of = [&](int hc) { return min(8 * NQ, p.G - chunk_of(hc) * 8 * NQ); };
+  auto first_head = [&](int hc) { return (p.chunks == 1 ? hc : hc / p.chunks) * p.G + chunk_of(hc) * kHeads; };
+  auto heads_of = [&](int hc) { return min(kHeads, p.G - chunk_of(hc) * kHeads); };
   auto request_q = [&](int seq, int hc) {
     const int h0 = first_head(hc), have = heads_of(hc);
 #pragma unroll
@@ -446,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
   int stage = 0;
   for (int i = 0; i < ahead; ++i) {
     cp_async_wait<kStages - 2>();
-    __syncwarp();
+    sync_ring();
     const uint32_t mask = meta[stage].mask, ends = meta[stage].ends;
 
     if (i == 0 || (ends & 1u)) {
@@ -532,26 +564,29 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       constexpr int kHi = C::kFp8 ? 4 : 3, kRow8 = C::kFp8 ? 3 : 4;
       const int lrow = kr(((lane >> kRow8) & 1) * 8 + (lane & 7));
       const uint32_t tiles_u = (ring_u + stage * C::kStageB + lrow * kRowB) + ((((lane >> kHi) & 1) << 4) ^ swz<kRowB>(lrow));
-      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + lane) * kRowB + swz<kRowB>(lane);   // FP8 values
+      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + (lane & (kStep - 1))) * kRowB + swz<kRowB>(lane & (kStep - 1));   // FP8 values
       const int k0 = kr(g), k8 = kr(g + 8);           // keys of this lane's fragment rows
       constexpr int KT = kStep / 16;
       uint32_t pb[KT][NQ][C::kFp8 ? 2 : 4];            // P as the second product's operand (bf16: high, low)
       float t[KT][NQ][4];
       uint32_t* kw = reinterpret_cast<uint32_t*>(ring + stage * C::kStageB + 2 * kStep * kRowB);
       const uint32_t* vw = kw + kStep * C::kWords;
+      uint32_t* factors = kTeam == 1 ? kw : own_factors;
 
       // FP8: the scales of this lane's key for all lanes. Key blocks' scales as floats; e = the largest value scale
-      // and 2^-e; value blocks' scales relative to e as halves, in the place of the step's scale words ([key][2 *
-      // kWords] words). A block that holds an infinity (bytes 254 and 255) has an infinite factor and no part in
+      // and 2^-e; value blocks' scales relative to e as halves ([key][2 * kWords] words: in the place of the step's
+      // scale words, which no other warp reads, or apart from them). A block that holds an infinity (bytes 254 and 255) has an infinite factor and no part in
       // e: it spoils its own 32 values only.
       if (C::kFp8) {
+        const int own = lane & (kStep - 1);
+        const bool writes = kTeam == 1 || own / (kStep / kTeam) == rank;   // two warps spread half of the keys each
         int top = 63;                                 // e + 127, at least -64 + 127: the sum takes 2^-e
         uint32_t kb[C::kWords], vb[C::kWords], f[2 * C::kWords];
 #pragma unroll
         for (int w = 0; w < C::kWords; ++w) {
           const uint32_t used = w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu;
-          kb[w] = kw[lane * C::kWords + w] & used;
-          vb[w] = vw[lane * C::kWords + w] & used;
+          kb[w] = kw[own * C::kWords + w] & used;
+          vb[w] = vw[own * C::kWords + w] & used;
           float y[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
@@ -559,11 +594,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
             const int by = (int)((vb[w] >> (8 * z)) & 0xFFu);
             if (by < 254) top = max(top, by);
           }
-          *reinterpret_cast<float4*>(key_scales + (lane * C::kWords + w) * 4) = make_float4(y[0], y[1], y[2], y[3]);
+          if (writes) *reinterpret_cast<float4*>(key_scales + (own * C::kWords + w) * 4) = make_float4(y[0], y[1], y[2], y[3]);
         }
         // e as a float: the integer behind 2^23
-        *reinterpret_cast<float2*>(value_scales + 2 * lane) =
-            make_float2(__uint_as_float(0x4B000000u + top) - 8388735.f, __uint_as_float((uint32_t)(254 - top) << 23));
+        if (writes)
+          *reinterpret_cast<float2*>(value_scales + 2 * own) = make_float2(
+              __uint_as_float(0x4B000000u + top) - 8388735.f, __uint_as_float((uint32_t)(254 - top) << 23));
 #pragma unroll
         for (int x = 0; x < 2 * C::kWords; ++x) {
           float y[2];
@@ -574,10 +610,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
           }
           f[x] = pack_f16(y[0], y[1]);
         }
-        __syncwarp();                                 // every lane has read the scale words
+        if (kTeam == 1) __syncwarp();                 // every lane has read the scale words
 #pragma unroll
-        for (int x = 0; x < 2 * C::kWords; ++x) kw[lane * 2 * C::kWords + x] = f[x];
-        __syncwarp();
+        for (int x = 0; x < 2 * C::kWords; ++x)
+          if (writes) factors[own * 2 * C::kWords + x] = f[x];
+        sync_ring();
       }
 
       // S^T = K Q^T
@@ -659,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       for (int nq = 0; nq < NQ; ++nq) {
         float mx[2] = {-INFINITY, -INFINITY};
         float un[KT][2];                              // FP8: 2^-e of this lane's two keys
-        const float c0 = C::kFp8 ? sm_c[nq * 8 + 2 * j] : p.scale_log2;
-        const float c1 = C::kFp8 ? sm_c[nq * 8 + 2 * j + 1] : p.scale_log2;
+        const float c0 = C::kFp8 ? sm_c[(rank * NQ + nq) * 8 + 2 * j] : p.scale_log2;
+        const float c1 = C::kFp8 ? sm_c[(rank * NQ + nq) * 8 + 2 * j + 1] : p.scale_log2;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
           float(&x)[4] = t[kt][nq];
@@ -741,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int x = 0; x < 2 * C::kWords; ++x) sc[kt][k][x] = kw[(kt * 16 + 4 * j + k) * 2 * C::kWords + x];
+            for (int x = 0; x < 2 * C::kWords; ++x) sc[kt][k][x] = factors[(kt * 16 + 4 * j + k) * 2 * C::kWords + x];
 #pragma unroll
         for (int b = 0; b < DP / 32; ++b) {
           uint32_t ps[KT][NQ][2];                     // the weights times the block's scales
@@ -760,7 +797,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 #pragma unroll
           for (int mt = 2 * b; mt < 2 * b + 2; ++mt) {
             uint32_t a[4];                            // codes of values g, g + 8: keys 4j .. 4j + 3 of 0..15, of 16..31
-            ldsm8t(a, codes_u ^ (mt << 4));
+            if (KT == 2) ldsm8t(a, codes_u ^ (mt << 4));
+            else ldsm8t_one(a, codes_u ^ (mt << 4));
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
               uint32_t f[4];
@@ -786,10 +824,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
     }
 
     if ((ends & 2u) || i + 1 == ahead) {
-      // ---- the run ends here, or this CTA's part of it: join the four warps -----------------------
+      // ---- the run ends here, or this CTA's part of it: join the rings -----------------------
       const Meta me = meta[stage];
-      __syncwarp();                                   // the stage is read: it takes this warp's o
-      float* mine_o = reinterpret_cast<float*>(ring + stage * C::kStageB);
+      sync_ring();                                   // the stage is read: it takes its warps' o
+      float* mine_o = reinterpret_cast<float*>(ring + stage * C::kStageB) + rank * NQ * 8 * DP;
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
@@ -798,8 +836,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
 #pragma unroll
           for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
           if (g == 0) {
-            sm_m[warp * 16 + nq * 8 + 2 * j + e] = m_run[nq][e];
-            sm_l[warp * 16 + nq * 8 + 2 * j + e] = l;
+            sm_m[my_ring * 16 + (rank * NQ + nq) * 8 + 2 * j + e] = m_run[nq][e];
+            sm_l[my_ring * 16 + (rank * NQ + nq) * 8 + 2 * j + e] = l;
           }
         }
 #pragma unroll
@@ -818,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       const bool whole = c_first == c_last;
       const int h0 = first_head(me.hc);
       const int q_heads = p.Hk * p.G;
-      constexpr int kSlot = 8 * NQ * (DP + 2);        // floats of a part: o, then (maximum, sum) per head
+      constexpr int kSlot = kHeads * (DP + 2);        // floats of a part: o, then (maximum, sum) per head
       // a CTA has at most two parts of cut runs: slot 1 for the one that starts in its share, slot 0 for the one before
       auto slot_of = [&](int cta) { return p.part + (int64_t)(2 * cta + (cta == c_first ? 1 : 0)) * kSlot; };
       auto emit = [&](int q, int d, const float (&x)[4], float m, float l) {
@@ -832,17 +870,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
       };
       auto put = [&](float* part, int q, int d, const float (&x)[4], float m, float l) {
         __stcg(reinterpret_cast<float4*>(part + q * DP + d), make_float4(x[0], x[1], x[2], x[3]));
-        if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NQ * DP + 2 * q), make_float2(m, l));
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + kHeads * DP + 2 * q), make_float2(m, l));
       };
       for (int e = tid; e < rows * (DP / 4); e += kThreads) {
         const int q = e / (DP / 4), d = (e % (DP / 4)) * 4;
         if (d >= p.D) continue;
         float m = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w * 16 + q]);
+        for (int w = 0; w < kRings; ++w) m = fmaxf(m, sm_m[w * 16 + q]);
         float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kRings; ++w) {
           const float f = ex2_rel(sm_m[w * 16 + q], m);
           l += sm_l[w * 16 + q] * f;
           const float4 y = *reinterpret_cast<const float4*>(
@@ -886,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) attention_kernel(const Att
                   y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                   if (k0 + k < parts) {
                     const float* s = slot_of(from + (k0 + k) * step);
-                    ml[k] = __ldcg(reinterpret_cast<const float2*>(s + 8 * NQ * DP + 2 * q));
+                    ml[k] = __ldcg(reinterpret_cast<const float2*>(s + kHeads * DP + 2 * q));
                     y[k] = __ldcg(reinterpret_cast<const float4*>(s + q * DP + d));
                   }
                 }
@@ -958,7 +996,7 @@ cudaError_t launch(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles,
   if (e != cudaSuccess) return e;
   const int64_t places = max_tiles * (1 + kRunCost);
   const int64_t grid = places < plan.grid_max ? places : plan.grid_max;
-  return launch_k(attention_kernel<C>, dim3((unsigned)grid), dim3(kThreads), C::kSmemB, stream, pdl, p);
+  return launch_k(attention_kernel<C>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmemB, stream, pdl, p);
 }
 
 template <int DP, bool kFp8>

@@ -5,11 +5,11 @@ namespace engram {
 
 AttnPlan attn_plan(int32_t G, int32_t D, bool fp8, int sms) {
   AttnPlan a;
-  (void)fp8;
   a.nq = G <= 8 ? 1 : 2;                              // 9 and more heads: 16 per CTA share a row's read
   a.chunks = (G + 8 * a.nq - 1) / (8 * a.nq);
   const int dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-  const int ctas = sms * attn::resident_ctas(dp, a.nq);
+  const int ctas = sms * attn::resident_ctas(fp8, dp, a.nq);
+  a.tile = attn::kRings * attn::step_keys(fp8, dp, a.nq);
   a.grid_max = ctas < kMaxAttnCtas ? ctas : kMaxAttnCtas;
   a.slot_floats = 8 * a.nq * (dp + 2);
   return a;

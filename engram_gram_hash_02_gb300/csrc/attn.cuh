@@ -88,15 +88,14 @@ struct AttnParams {
 constexpr int kMaxAttnCtas = 1024;
 constexpr size_t kAttnZeroBytes = ENGRAM_ATTENTION_ZERO_BYTES;
 static_assert(3 * kMaxAttnCtas * sizeof(uint32_t) <= kAttnZeroBytes, "the counters lie in the zeroed part");
-// how a shape runs: its kernel's query tiles per CTA, CTAs and partial floats per slot
+// how a shape runs: its kernel's query tiles per CTA, CTAs, partial floats per slot, keys per tile
 struct AttnPlan {
-  int32_t nq, chunks, grid_max, slot_floats;
+  int32_t nq, chunks, grid_max, slot_floats, tile;
 };
 AttnPlan attn_plan(int32_t G, int32_t D, bool fp8, int sms);
 size_t attn_workspace_bytes(int32_t G, int32_t D, bool fp8, int sms);
 cudaError_t launch_attention_bf16(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl);
 cudaError_t launch_attention_fp8(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl);
-constexpr int attn_tile_keys(bool fp8) { return fp8 ? 128 : 64; }
 
 // ---- asynchronous copies of 16 bytes to shared memory --------------------------------------
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

@@ -191,7 +191,7 @@ int check_attention(const char* fn, const EngramKVCache* cache, const EngramPage
   p.counters = static_cast<uint32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnZeroBytes);
   const int64_t longest = window > 0 && window < p.cap ? window : p.cap;
-  const int64_t tile = attn_tile_keys(p.cache.fp8);
+  const int64_t tile = a->plan.tile;
   const __int128 tiles = (__int128)p.B * p.Hk * p.chunks * ((longest + tile - 1) / tile);
   ENGRAM_CHECK_ARG(tiles < (__int128)1 << 28, "%s: batch * kv_heads * page table capacity is too large", fn);
   a->max_tiles = tiles < 1 ? 1 : (int64_t)tiles;
