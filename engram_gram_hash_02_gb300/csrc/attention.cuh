@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
   };
   auto places_of = [&](int tiles) { return tiles > 0 ? (tiles + kRunCost) * heads : 0; };
   auto read_len = [&](int b) {
-    const int raw = __ldg(p.lens + b);
+    const int raw = __ldcg(p.lens + b);
     if (blockIdx.x == 0 && (raw < 0 || raw > p.cap) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
     return raw;
   };
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     if (place0 < place1 && place0 >= before && place0 < before + mine) {
       int at = before;
       for (int b = b0; b < b1; ++b) {
-        const int tiles = tiles_of(__ldg(p.lens + b));
+        const int tiles = tiles_of(__ldcg(p.lens + b));
         if (place0 < at + places_of(tiles)) {
           locate(b, at, tiles);
           sm_i[8] = seq;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     if (C::kFp8) shead_off = head * p.cache.shead_b;
   };
   auto enter = [&] {                                  // seq is new
-    const int len = clamp_len(__ldg(p.lens + seq), p.cap);
+    const int len = clamp_len(__ldcg(p.lens + seq), p.cap);
     const int n = attended(len, p.window);
     first = len - n;
     end = len;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     if (inside) {
       const int n = (int)fast_div((uint32_t)pos, p.cache.div_page);
       at = pos - n * p.cache.page_size;
-      page = __ldg(p.table + (int64_t)seq * p.table_stride + n);
+      page = p.table[(int64_t)seq * p.table_stride + n];
     }
   };
   // a lane copies chunk c of rows sub, sub + kRows, ... (the warps of a ring take turns at these passes)
@@ -976,7 +976,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
   // ---- sequences with nothing to attend to -----------------------------------------------------
   const int q_heads = p.Hk * p.G;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (clamp_len(__ldg(p.lens + b), p.cap) > 0) continue;
+    if (clamp_len(__ldcg(p.lens + b), p.cap) > 0) continue;
     for (int e = tid; e < q_heads * (p.D / 4); e += kThreads) {
       const int h = e / (p.D / 4), d = (e % (p.D / 4)) * 4;
       *reinterpret_cast<uint2*>(p.out + (int64_t)b * p.out_ts + (int64_t)h * p.out_hs + d) = make_uint2(0, 0);

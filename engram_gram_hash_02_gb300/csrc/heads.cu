@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
   const int half = p.nr.R >> 1;
   const int r0 = d0 - p.nr.start;
   const bool turned = turn && live && r0 >= 0 && r0 < p.nr.R;
-  int64_t pos = turned ? __ldg(p.positions + t) : 0;  // (its angles are two loads away)
+  int64_t pos = turned ? p.positions[t] : 0;  // (its angles are two loads away)
   // a group's lanes copy consecutive chunks; chunk c of a row lies at c ^ (c / 8 & 1), so that reads of two
   // chunks per lane (fp32) meet no bank twice
   auto chunk_at = [&](int c) { return (tid - sub) * kParts + (kF32 ? c ^ ((c >> 3) & 1) : c); };
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
   uint8_t *dst = nullptr, *scales = nullptr;          // this thread's place in the token's first row of the cache
   bool stored = false;
   if (to_cache) {
-    const int64_t slot = __ldg(p.slots + t);
+    const int64_t slot = p.slots[t];
     int64_t page, at;
     stored = place(p.cache, slot, &page, &at);
     if (stored) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   const int d0 = sub * 8;
   if (d0 >= p.D) return;
   const CacheRef& c = p.cache;
-  const int64_t slot = __ldg(p.slots + t);
+  const int64_t slot = p.slots[t];
   int64_t page = 0, at = 0;
   const bool ok = place(c, slot, &page, &at);
   if (slot >= c.slots && sub == 0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SLOT);
@@ -314,12 +314,12 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     byte[r] = 0;
     if (ok && h0 + r < p.heads) {
       if (kFp8) {
-        const uint2 codes = __ldg(reinterpret_cast<const uint2*>(row + r * c.head_b));
+        const uint2 codes = *reinterpret_cast<const uint2*>(row + r * c.head_b);
         raw[r].x = codes.x;
         raw[r].y = codes.y;
-        byte[r] = __ldg(scale + r * c.shead_b);
+        byte[r] = scale[r * c.shead_b];
       } else {
-        raw[r] = __ldg(reinterpret_cast<const uint4*>(row + r * c.head_b));
+        raw[r] = *reinterpret_cast<const uint4*>(row + r * c.head_b);
       }
     }
   }
