@@ -448,6 +448,10 @@ int engram_forward_noalloc(const EngramDims* dims, const EngramHashTables* table
  * the formulas are stated at each call): per-head norms of queries and keys with the position
  * rotation, rows written to a paged cache (bf16, or the FP8 tables' own format) and read back, and
  * attention of one new token per sequence over that cache. Inference only.
+ *
+ * Every kernel is launched with programmatic stream serialization: it may start while its predecessor on
+ * the stream finishes, and waits for it before it reads or writes anything of the caller's. All calls can be
+ * captured in CUDA graphs (after one call outside of capture on the device, which sets kernel attributes).
  */
 
 /* Value types of rows of heads. */
