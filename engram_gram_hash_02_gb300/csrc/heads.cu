@@ -11,7 +11,7 @@
 //
 // Bound by HBM: a row is read once and written once. A row is held by 8, 16 or 32 lanes, 8 values each, so a
 // norm is a few shuffles. Measured on a GB300 (share of the 6.78 TB/s of a plain copy): 32768 tokens of 32 + 8
-// heads of 128 normed and turned in 110 us, 6.2 TB/s (0.92; issue slots 76 % busy); 8 + 8 heads written as FP8
+// heads of 128 normed and turned in 103 us, 6.7 TB/s (0.98); 8 + 8 heads written as FP8
 // in 35 us (0.85), as bf16 in 41 us (0.96); read back in 34 us (0.88) and 41 us (0.96).
 #include "attn.cuh"
 
@@ -104,7 +104,9 @@ __device__ __forceinline__ void wait_rows(int n) {
 //   out_i = r * (x_i * A_i + y_i * B_i),  r = 1 / sqrt(mean(x^2) + eps),  y_i the other value of x_i's pair,
 // with A_i = w_i cos, B_i = -+ w_y sin formed once per token; y comes from the partner lane's place. Nine CTAs
 // per SM (56 registers): with eight 118 us instead of 110 for 32768 tokens of 32 + 8 heads, with ten spills, 133.
-template <int kLanes, bool kF32, int kRows>
+// kPairs: values 2i and 2i + 1 are turned, else i and i + R/2 (one kernel for both has a quarter more instructions:
+// 110 us instead of 103 for the 32768 tokens above).
+template <int kLanes, bool kF32, bool kPairs, int kRows>
 __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant__ QkvParams p) {
   constexpr unsigned kWarp = 0xFFFFFFFFu;
   constexpr int kBytes = kF32 ? 4 : 2;
@@ -156,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
 
   // A and B of this thread's 8 values. A value of a second half takes + sin times its partner, one of a first
   // half - sin.
-  const bool pairs = p.nr.interleaved;
   int other = sub;
   float A[8], B[8];
 #pragma unroll
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
       pos = pos < 0 ? 0 : p.nr.rows - 1;
     }
     const float* row = p.nr.table + pos * p.nr.R;
-    if (pairs) {
+    if (kPairs) {
       const float4 c = __ldg(reinterpret_cast<const float4*>(row + (r0 >> 1)));
       const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + (r0 >> 1)));
       A[0] = A[1] = c.x; A[2] = A[3] = c.y; A[4] = A[5] = c.z; A[6] = A[7] = c.w;
@@ -190,9 +191,9 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < 8; ++i) A[i] *= w[i];
     if (turned) {
-      if (!pairs) unpack8(__ldg(reinterpret_cast<const uint4*>(wp + 8 * other)), w);
+      if (!kPairs) unpack8(__ldg(reinterpret_cast<const uint4*>(wp + 8 * other)), w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) B[i] *= w[pairs ? i ^ 1 : i];
+      for (int i = 0; i < 8; ++i) B[i] *= w[kPairs ? i ^ 1 : i];
     }
   }
   uint8_t *dst = nullptr, *scales = nullptr;          // this thread's place in the token's first row of the cache
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
     }
     if (turn || wp != nullptr) {
       float y[8];
-      if (pairs) {
+      if (kPairs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
       } else if (turn) {
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 }
 
 // Heads of one token that a group of lanes takes. More of them share the token's angles and slot and are in
-// flight together: 32768 tokens of 32 + 8 heads of 128 are normed and turned in 312, 195, 133 and 111 us with 1,
+// flight together: 32768 tokens of 32 + 8 heads of 128 are normed and turned in 312, 195, 133 and 110 us with 1,
 // 2, 4 and 8. But few rows want lanes of their own: 256 tokens of 8 + 8 heads are written in 2.3 us with 1 and
 // 3.7 us with 8 (half of the GPU's lanes or less), 1024 tokens in 4.1, 3.2, 3.2 and 4.0 us. Within those limits
 // the choice wastes least: a group costs what its rows do, a part-filled one as much as a full one, and
@@ -371,7 +372,7 @@ int rows_per_group(int64_t T, const int (&heads)[3], int lanes) {
   return best;
 }
 
-template <int kLanes, bool kF32, int kRows>
+template <int kLanes, bool kF32, bool kPairs, int kRows>
 cudaError_t go(QkvParams p, cudaStream_t stream) {
   const int64_t per_block = kThreads / kLanes;
   auto blocks = [&](const HeadRows& r) {
@@ -385,23 +386,25 @@ cudaError_t go(QkvParams p, cudaStream_t stream) {
   p.div_q = make_fastdiv((uint32_t)max((p.q.heads + kRows - 1) / kRows, 1));
   p.div_kv = make_fastdiv((uint32_t)max((p.k.heads + kRows - 1) / kRows, 1));   // v has k's heads
   p.inv_d = 1.f / (float)p.D;
-  return launch_k(qkv_kernel<kLanes, kF32, kRows>, dim3((unsigned)(nq + nk + nv)), dim3(kThreads), 0, stream, true, p);
+  return launch_k(qkv_kernel<kLanes, kF32, kPairs, kRows>, dim3((unsigned)(nq + nk + nv)), dim3(kThreads), 0, stream, true, p);
 }
 
-template <int kLanes, bool kF32>
+template <int kLanes, bool kF32, bool kPairs>
 cudaError_t go_rows(const QkvParams& p, cudaStream_t stream) {
   const int heads[3] = {p.q.heads, p.k.heads, p.v.heads};
   switch (rows_per_group(p.T, heads, kLanes)) {
-    case 8: return go<kLanes, kF32, 8>(p, stream);
-    case 4: return go<kLanes, kF32, 4>(p, stream);
-    case 2: return go<kLanes, kF32, 2>(p, stream);
-    default: return go<kLanes, kF32, 1>(p, stream);
+    case 8: return go<kLanes, kF32, kPairs, 8>(p, stream);
+    case 4: return go<kLanes, kF32, kPairs, 4>(p, stream);
+    case 2: return go<kLanes, kF32, kPairs, 2>(p, stream);
+    default: return go<kLanes, kF32, kPairs, 1>(p, stream);
   }
 }
 
-template <bool kF32>
+template <bool kF32, bool kPairs>
 cudaError_t go_lanes(const QkvParams& p, cudaStream_t stream) {
-  return p.D <= 64 ? go_rows<8, kF32>(p, stream) : p.D <= 128 ? go_rows<16, kF32>(p, stream) : go_rows<32, kF32>(p, stream);
+  return p.D <= 64    ? go_rows<8, kF32, kPairs>(p, stream)
+         : p.D <= 128 ? go_rows<16, kF32, kPairs>(p, stream)
+                      : go_rows<32, kF32, kPairs>(p, stream);
 }
 
 template <int kLanes, bool kFp8, int kRows>
@@ -434,7 +437,9 @@ cudaError_t go_read_rows(const KvReadParams& p, cudaStream_t stream) {
 
 cudaError_t launch_qkv(const QkvParams& p, cudaStream_t stream) {
   const bool f32 = p.q.data != nullptr ? p.q.f32 : p.k.f32;
-  return f32 ? go_lanes<true>(p, stream) : go_lanes<false>(p, stream);
+  const bool pairs = p.nr.R > 0 && p.nr.interleaved;
+  if (f32) return pairs ? go_lanes<true, true>(p, stream) : go_lanes<true, false>(p, stream);
+  return pairs ? go_lanes<false, true>(p, stream) : go_lanes<false, false>(p, stream);
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {
