@@ -565,7 +565,9 @@ size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_he
  * h / (q_heads / kv_heads). Over the tokens j in [max(0, len - window), len) (window 0: [0, len)):
  *     s_j = scale * <q_h, k_j>,  out_h = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse_h = log sum_j exp(s_j)
  * A sequence with no tokens, or whose scores are all -inf, gives zeros and lse -inf. What lies in the
- * cache outside the attended tokens is not read into the result, whatever it holds.
+ * cache outside the attended tokens is not read into the result, whatever it holds. An attended infinity
+ * may come out as NaN (operands enter as sums of two parts); in an FP8 cache a value block whose scale is
+ * 2^-24 below its row's largest, or below 2^-88, counts as zero.
  *   q          rows [B, q_heads, head_dim], bf16 or fp32; q_heads a multiple of kv_heads
  *   seqs       lengths outside [0, table_width * page_size] are clamped (ENGRAM_ERR_SEQ_LEN); a page
  *              number outside the cache hides its tokens (ENGRAM_ERR_PAGE)
@@ -589,6 +591,8 @@ int engram_paged_attention(const EngramKVCache* cache, const EngramPagedSeqs* se
  * engram_paged_attention one after another, bit for bit.
  *   q          rows [B, q_heads, head_dim]; k, v rows [B, kv_heads, head_dim]; one type for all three
  *   positions  device int32 [B]       slots  device int64 [B]
+ * Every entry's key and value are written before any is attended, so several new tokens of one sequence
+ * may be entries of one batch (equal rows of the page table, lengths that grow by one).
  */
 int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs,
                           const EngramHeads* q, const EngramHeads* k, const EngramHeads* v,

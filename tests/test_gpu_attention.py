@@ -505,3 +505,55 @@ def test_two_streams_at_once_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for cache, table, lens, q, plan, _ in made:
         H.check_attention(cache, table, lens, q, plan.out, plan.lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_several_new_tokens_of_one_sequence_as_entries_of_the_batch(fmt):
+    # entries 0 .. 2 are one sequence's next three tokens, each attending the ones before; entry 3 is another
+    Hk, G, D, page = 2, 4, 128, 16
+    rng = np.random.default_rng(8)
+    owners, pages = H.tables([33, 70], page, rng)
+    cache = H.empty_cache(pages, page, Hk, D, fmt)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    old = np.concatenate([H.slots_of(owners, 0, 0, 30, page), H.slots_of(owners, 1, 0, 69, page)])
+    E().engram_kv_write(cache, *(randn(g, (len(old), Hk, D)) for _ in range(2)), torch.from_numpy(old).to(DEV))
+    table = owners[[0, 0, 0, 1]]
+    lens = [31, 32, 33, 70]
+    q, k, v = (randn(g, (4, h, D), torch.bfloat16) for h in (Hk * G, Hk, Hk))
+    slots = torch.tensor([int(H.slots_of(table, b, n - 1, n, page)[0]) for b, n in enumerate(lens)], device=DEV)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    nr = E().NormRope(None, None, 0.0, torch.from_numpy(A.rope_angles(80, D)).to(DEV))
+    out, lse = E().engram_attention_step(nr, cache, q, k, v, sl - 1, slots, torch.from_numpy(table).to(DEV), sl, lse=True)
+    q32 = torch.empty(q.shape, dtype=torch.float32, device=DEV)
+    E().engram_qk_norm_rope(nr, q, None, sl - 1, q32)
+    H.check_attention(cache, table, lens, q32, out, lse, D ** -0.5)
+
+
+def test_a_table_without_columns_leaves_every_sequence_empty():
+    cache = E().KVCache.allocate(1, 16, 1, 64)
+    q = torch.ones((3, 2, 64), dtype=torch.bfloat16, device=DEV)
+    err = word()
+    out, lse = E().engram_paged_attention(cache, q, torch.zeros((3, 0), dtype=torch.int32, device=DEV),
+                                          torch.tensor([0, 5, 0], dtype=torch.int32, device=DEV), lse=True, err=err)
+    assert not out.any() and bool(torch.isinf(lse).all()) and int(err) == E().ERR_SEQ_LEN
+
+
+def test_calls_from_plain_c(tmp_path):
+    """tests/c/attention_c_abi.c, built with the host C compiler against include/engram.h."""
+    import os
+    import shutil
+    import subprocess
+    from engram_gram_hash_02_gb300 import binding, build
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    binding.lib()
+    libdir = os.path.dirname(os.path.abspath(binding.LIB_PATH))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc())))
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c", "attention_c_abi.c")
+    exe = str(tmp_path / "attention_c_abi")
+    subprocess.run([cc, "-std=c99", "-O2", "-Wall", "-Werror", "-I", build.INCLUDE, "-I", os.path.join(cuda, "include"), src, "-L", libdir,
+                    "-lengram", "-L", os.path.join(cuda, "lib64"), "-lcudart", "-lm", f"-Wl,-rpath,{libdir}",
+                    f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}", "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout + out.stderr
