@@ -10,7 +10,8 @@
 //   S^T[keys, heads] = K Q^T      and      O^T[values, heads] += V^T P^T
 // With one token per sequence the heads of a group are the only rows there are; the tensor pipe stays
 // mostly idle, and operands in registers (no tensor memory to set up, drain and rescale through) keep a
-// warp's chain from a landed copy to the next one short.
+// warp's chain from a landed copy to the next one short. (ncu: 11 to 16 % of that pipe's cycles in all of the shapes
+// below, tcgen05 or not: it has nothing to win here.)
 //
 // Work is cut at keys, not at sequences: the tiles (64 keys of bf16, 128 of FP8) of all sequences and key
 // heads form one row, sequence by sequence, and each CTA takes an equal run of it, so a batch of any mix of
@@ -575,7 +576,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       constexpr int kHi = C::kFp8 ? 4 : 3, kRow8 = C::kFp8 ? 3 : 4;
       const int lrow = kr(((lane >> kRow8) & 1) * 8 + (lane & 7));
       const uint32_t tiles_u = (ring_u + stage * C::kStageB + lrow * kRowB) + ((((lane >> kHi) & 1) << 4) ^ swz<kRowB>(lrow));
-      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + (lane & (kStep - 1))) * kRowB + swz<kRowB>(lane & (kStep - 1));   // FP8 values
+      const int own_row = lane & (kStep - 1);         // FP8 values: the row this lane addresses
+      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + own_row) * kRowB + swz<kRowB>(own_row);
       const int k0 = kr(g), k8 = kr(g + 8);           // keys of this lane's fragment rows
       constexpr int KT = kStep / 16;
       uint32_t pb[KT][NQ][C::kFp8 ? 2 : 4];            // P as the second product's operand (bf16: high, low)
@@ -586,8 +588,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
 
       // FP8: the scales of this lane's key for all lanes. Key blocks' scales as floats; e = the largest value scale
       // and 2^-e; value blocks' scales relative to e as halves ([key][2 * kWords] words: in the place of the step's
-      // scale words, which no other warp reads, or apart from them). A block that holds an infinity (bytes 254 and 255) has an infinite factor and no part in
-      // e: it spoils its own 32 values only.
+      // scale words where no other warp reads them, else apart from them). A block that holds an infinity (bytes
+      // 254 and 255) has an infinite factor and no part in e: it spoils its own 32 values only.
       if (C::kFp8) {
         const int own = lane & (kStep - 1);
         const bool writes = kTeam == 1 || own / (kStep / kTeam) == rank;   // two warps spread half of the keys each
@@ -808,8 +810,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
 #pragma unroll
           for (int mt = 2 * b; mt < 2 * b + 2; ++mt) {
             uint32_t a[4];                            // codes of values g, g + 8: keys 4j .. 4j + 3 of 0..15, of 16..31
-            if (KT == 2) ldsm8t(a, codes_u ^ (mt << 4));
-            else ldsm8t_one(a, codes_u ^ (mt << 4));
+            if (KT == 2)
+              ldsm8t(a, codes_u ^ (mt << 4));
+            else
+              ldsm8t_one(a, codes_u ^ (mt << 4));
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
               uint32_t f[4];
