@@ -10,7 +10,7 @@
 //   S^T[keys, heads] = K Q^T      and      O^T[values, heads] += V^T P^T
 // With one token per sequence the heads of a group are the only rows there are; the tensor pipe stays
 // mostly idle, and operands in registers (no tensor memory to set up, drain and rescale through) keep a
-// warp's chain from a landed copy to the next one short. (ncu: 11 to 16 % of that pipe's cycles in all of the shapes
+// warp's chain from a landed copy to the next one short. (ncu: 11 to 17 % of that pipe's cycles in all of the shapes
 // below, tcgen05 or not: it has nothing to win here.)
 //
 // Work is cut at keys, not at sequences: the tiles (64 keys of bf16, 128 of FP8) of all sequences and key
@@ -33,8 +33,8 @@
 // Measured on one GB300 (share of the 6.78 TB/s of a plain copy), heads of 128, 8 query heads per key head unless
 // said: one sequence of 131072 tokens, 4 key heads, bf16, 49 us, 5.5 TB/s (0.81): 3 us until the first rows are
 // there, then 7.3 TB/s, 5 us for the slowest SM and the join. 64 sequences of up to 8192 tokens, 2 key heads of 256,
-// bf16, 88 us, 6.1 TB/s (0.90). 256 sequences of up to 4096 tokens, 8 key heads with 4 query heads each, FP8, 183 us,
-// 6.1 TB/s (0.90): 690 instructions per 32 keys of 8448 bytes and eight warps per SM to issue them. 48 windows of
+// bf16, 88 us, 6.1 TB/s (0.90). 256 sequences of up to 4096 tokens, 8 key heads with 4 query heads each, FP8, 173 us,
+// 6.4 TB/s (0.95): 690 instructions per 32 keys of 8448 bytes and twelve warps per SM to issue them. 48 windows of
 // 1024 tokens, 16 heads of 64, bf16, 38 us, 5.1 TB/s (0.75): 1.7 runs per CTA. One sequence of 777 tokens 6.1 us:
 // 1.2 us for lengths and page, 1 us for the rows, 0.5 us of computing, 2 us to join 13 parts.
 //
@@ -43,6 +43,8 @@
 // queries as two bf16 or two f16; for f16 each query row is first scaled by a power of two (its largest
 // value below 2^14). Scores, maxima, sums and o are fp32.
 #pragma once
+
+#include <atomic>
 
 #include "attn.cuh"
 
@@ -112,17 +114,20 @@ __device__ __forceinline__ float ex2(float x) {
 // exp2(x - m) for m = max(x, ...): a maximum of -inf (nothing attended yet) gives 0
 __device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
 
-// How a kernel for heads of up to dp (64, 128 or 256) and `tiles` tiles of 8 query heads runs. Registers bound it:
-// a warp needs some 230 for its o, queries and the fragments in flight (spilled values come back from L2, shared
-// memory leaves no L1), so 8 warps per SM (12 for heads of 64 in one tile). Two tiles of heads of 256 do not fit
-// one warp: two warps then share a ring, a tile each.
+// How a kernel for heads of up to dp (64, 128 or 256) and `tiles` tiles of 8 query heads runs.
+// Two tiles of heads of 256 do not fit a warp's registers: two warps then share a ring, a tile each.
 constexpr int team_warps(int dp, int tiles) { return dp == 256 && tiles == 2 ? 2 : 1; }
 // FP8 steps of 32 keys (the fixed part of a step is a third of its instructions), 16 where a ring of 32 would leave
-// room for four warps only: 64 sequences of up to 4096 tokens, 8 heads of 256 per key head, 36.5 us (40.6 with 32)
+// room for four warps only: 64 sequences of up to 4096 tokens, 8 heads of 256 per key head, 36.5 us (40.6 with 32).
 constexpr int step_keys(bool fp8, int dp, int tiles) { return fp8 && !(dp == 256 && tiles == 1) ? 32 : 16; }
+// CTAs per SM and stages per ring: as many warps as registers and shared memory allow, where instructions count
+// (FP8 in one tile: 256 sequences of heads of 128 take 173 us with three CTAs of two stages, 183 with two of three;
+// 64 of heads of 64 take 35.6 us with four of two, 37.2 with three of four), else three stages, which keep more
+// bytes in flight (bf16: one sequence of 131072 takes 49.3 us, 51.1 with three CTAs of two stages).
 constexpr int resident_ctas(bool fp8, int dp, int tiles) {
-  return dp == 64 && tiles == 1 ? 3 : dp <= 128 || (fp8 && tiles == 1) ? 2 : 1;
+  return tiles == 2 ? (dp == 256 ? 1 : 2) : (dp == 64 ? 3 : dp == 128 ? 2 : 1) + (fp8 ? 1 : 0);
 }
+constexpr int ring_stages(bool fp8, int dp, int tiles) { return fp8 && tiles == 1 && dp <= 128 ? 2 : 3; }
 
 template <int DP_, bool kFp8_, int kTiles_, bool kSplit_>
 struct Cfg {
@@ -141,7 +146,7 @@ struct Cfg {
   static constexpr int kWords = (DP + 127) / 128;     // scale words per row
   static constexpr int kStageB = 2 * kStep * kRowB + (kFp8 ? 2 * kStep * kWords * 4 : 0);
   static constexpr int kCtas = resident_ctas(kFp8, DP, kTiles);   // per SM
-  static constexpr int kStages = DP == 64 ? 4 : 3;
+  static constexpr int kStages = ring_stages(kFp8, DP, kTiles);
   static constexpr int kRingB = kRings * kStages * kStageB;
   static constexpr int kQPitch = DP + 8;              // 16-bit values
   static constexpr int kQB = kHeads * kQPitch * 2;    // per part (high, low)
@@ -576,8 +581,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       constexpr int kHi = C::kFp8 ? 4 : 3, kRow8 = C::kFp8 ? 3 : 4;
       const int lrow = kr(((lane >> kRow8) & 1) * 8 + (lane & 7));
       const uint32_t tiles_u = (ring_u + stage * C::kStageB + lrow * kRowB) + ((((lane >> kHi) & 1) << 4) ^ swz<kRowB>(lrow));
-      const int own_row = lane & (kStep - 1);         // FP8 values: the row this lane addresses
-      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + own_row) * kRowB + swz<kRowB>(own_row);
+      constexpr int kRowMask = kStep - 1;             // FP8 values: a lane addresses row lane & kRowMask
+      const uint32_t codes_u = ring_u + stage * C::kStageB + (kStep + (lane & kRowMask)) * kRowB + swz<kRowB>(lane & kRowMask);
       const int k0 = kr(g), k8 = kr(g + 8);           // keys of this lane's fragment rows
       constexpr int KT = kStep / 16;
       uint32_t pb[KT][NQ][C::kFp8 ? 2 : 4];            // P as the second product's operand (bf16: high, low)
@@ -929,7 +934,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
             const bool mine = e < rows * (DP / 4) && d < p.D;
             float m = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
             if (mine) {
-              constexpr int kBatch = 8;                // parts in flight per thread
+              constexpr int kBatch = C::kTiles == 2 ? 16 : 8;   // parts in flight per thread (registers are free here)
               for (int k0 = 0; k0 < parts; k0 += kBatch) {
                 float2 ml[kBatch];
                 float4 y[kBatch];
@@ -1003,14 +1008,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
 template <typename C>
 cudaError_t launch(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
   static PerContextOnce once;
+  static std::atomic<int> resident{C::kCtas};          // what fits an SM: the work is divided over one wave of CTAs
   const cudaError_t e = once.run([] {
-    const cudaError_t e = cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemB);
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemB);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    e = cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<C>, C::kThreads, C::kSmemB);
+    if (e == cudaSuccess) resident = n < 1 ? 1 : n < C::kCtas ? n : C::kCtas;
+    return e;
   });
   if (e != cudaSuccess) return e;
-  const int64_t places = max_tiles * (1 + kRunCost);
-  const int64_t grid = places < plan.grid_max ? places : plan.grid_max;
+  int64_t grid = max_tiles * (1 + kRunCost);
+  if (grid > plan.grid_max) grid = plan.grid_max;
+  if (grid > (int64_t)num_sms() * resident) grid = (int64_t)num_sms() * resident;
   return launch_k(attention_kernel<C>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmemB, stream, pdl, p);
 }
 
