@@ -885,8 +885,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
         w.x = pack_bf16(x[0] * inv, x[1] * inv);
         w.y = pack_bf16(x[2] * inv, x[3] * inv);
         *reinterpret_cast<uint2*>(p.out + (int64_t)me.seq * p.out_ts + (int64_t)(h0 + q) * p.out_hs + d) = w;
-        if (d == 0 && p.lse != nullptr)
-          p.lse[(int64_t)me.seq * q_heads + h0 + q] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+        if (d == 0 && p.lse != nullptr) {
+          // m + log2(l) with l's exponent added to m first: the two may be large and of opposite sign (FP8)
+          const uint32_t b = __float_as_uint(l);
+          const float log2_sum = (m + (float)((int)(b >> 23) - 127)) + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u));
+          p.lse[(int64_t)me.seq * q_heads + h0 + q] = l == 0.f ? -INFINITY : l - l == 0.f ? 0.6931471805599453f * log2_sum : l;
+        }
       };
       auto put = [&](float* part, int q, int d, const float (&x)[4], float m, float l) {
         __stcg(reinterpret_cast<float4*>(part + q * DP + d), make_float4(x[0], x[1], x[2], x[3]));
