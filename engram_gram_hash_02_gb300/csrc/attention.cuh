@@ -235,7 +235,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     if (blockIdx.x == 0 && (raw < 0 || raw > p.cap) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
     return raw;
   };
-  if (p.B <= 32) {                                    // every warp for itself: no barrier before the first copy
+  // Few sequences: every warp for itself, no barrier before its first copy (one sequence of 777 tokens:
+  // 6.05 us, 6.29 by the CTA's sum below, which takes any batch).
+  if (p.B <= 32) {
     const int tiles = lane < p.B ? tiles_of(read_len(lane)) : 0;
     int scan = places_of(tiles);
 #pragma unroll
@@ -355,30 +357,22 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     const uint32_t dst = ring_u + stage * C::kStageB;
     const uint32_t to = dst + lane_dst;
     const int64_t off = live ? ((int64_t)((uint64_t)(uint32_t)page * p.cache.page_u + (uint64_t)(uint32_t)at * p.cache.tok_u) << 4) + head_off : 0;
-    // all rows attended and in one page: equal steps from the first one
+    // All rows attended and in one page: equal steps from the first one, without a shuffle for each row (one
+    // sequence of 131072 tokens: 48.4 us, 50.1 without this; 256 FP8 sequences: 170.9, 173.1).
     const int at0 = __shfl_sync(0xFFFFFFFFu, at, 0);
     if (mask == kAll && at0 + kStep <= p.cache.page_size) {
       const uint8_t* kp = p.cache.k + (__shfl_sync(0xFFFFFFFFu, off, 0) + sub * p.cache.tok_b + c * 16);
       const uint8_t* vp = kp + (p.cache.v - p.cache.k);
       if (in_row) {
-        if (p.cache.tok_b == kRowB) {                 // the steps are immediates
+        const int64_t step = kRows * p.cache.tok_b;
 #pragma unroll
-          for (int r0 = 0; r0 < kStep; r0 += kRows) {
-            if (!my_pass(r0)) continue;
-            cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp + r0 * kRowB);
-            cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp + r0 * kRowB);
+        for (int r0 = 0; r0 < kStep; r0 += kRows) {
+          if (my_pass(r0)) {
+            cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp);
+            cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp);
           }
-        } else {
-          const int64_t step = kRows * p.cache.tok_b;
-#pragma unroll
-          for (int r0 = 0; r0 < kStep; r0 += kRows) {
-            if (my_pass(r0)) {
-              cp_async16((to ^ swz<kRowB>(r0)) + r0 * kRowB, kp);
-              cp_async16((to ^ swz<kRowB>(r0)) + (kStep + r0) * kRowB, vp);
-            }
-            kp += step;
-            vp += step;
-          }
+          kp += step;
+          vp += step;
         }
       }
     } else {
@@ -919,7 +913,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       if (!whole) {
         // The last CTA to arrive of each group of kGroup joins the group's parts into the group's first slot,
         // the last group to be joined joins the groups: 2 * sqrt(parts) reads in a row instead of all of them
-        // through one SM. A counter belongs to its group by the group's first CTA; a run's first group may
+        // through one SM (one sequence of 131072 tokens: 48.4 us, 55.3 in one level). A counter belongs to its group by the group's first CTA; a run's first group may
         // share that CTA with the end of another run, so it has an array of its own.
         auto arrive_last = [&](uint32_t* counter, int parties) {
           __syncthreads();                            // every thread's part is written
