@@ -913,8 +913,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       if (!whole) {
         // The last CTA to arrive of each group of kGroup joins the group's parts into the group's first slot,
         // the last group to be joined joins the groups: 2 * sqrt(parts) reads in a row instead of all of them
-        // through one SM (one sequence of 131072 tokens: 48.4 us, 55.3 in one level). A counter belongs to its group by the group's first CTA; a run's first group may
-        // share that CTA with the end of another run, so it has an array of its own.
+        // through one SM (one sequence of 131072 tokens: 48.4 us, 55.3 in one level). A counter belongs to its
+        // group by the group's first CTA; a run's first group may share that CTA with the end of another run,
+        // so it has an array of its own.
         auto arrive_last = [&](uint32_t* counter, int parties) {
           __syncthreads();                            // every thread's part is written
           if (tid == 0) {

@@ -11,8 +11,9 @@
 //
 // Bound by HBM: a row is read once and written once. A row is held by 8, 16 or 32 lanes, 8 values each, so a
 // norm is a few shuffles. Measured on a GB300 (share of the 6.78 TB/s of a plain copy): 32768 tokens of 32 + 8
-// heads of 128 normed and turned in 103 us, 6.7 TB/s (0.98); 8 + 8 heads written as FP8
-// in 35 us (0.85), as bf16 in 41 us (0.96); read back in 34 us (0.88) and 41 us (0.96).
+// heads of 128 normed and turned in 103 us, 6.7 TB/s (0.98), 106 to 108 us (0.95) where three sets of rows take
+// turns; 8 + 8 heads written as FP8 in 35 us (0.85), as bf16 in 41 us (0.96); read back in 34 us (0.88) and 41 us
+// (0.96).
 #include "attn.cuh"
 
 namespace engram {
