@@ -24,11 +24,14 @@
 //
 // FP8 rows (codes, one power-of-two scale per 32 values) are converted to f16 in registers (exact). A key
 // block's scale multiplies that block's fp32 partial product. The value scales join the weights before those
-// are rounded: with 2^e_j the largest scale of value row j, the running maximum is that of s_j + e_j, the
-// weights 2^(s_j + e_j - maximum + 15) fill f16's range, and a block's own scale enters as 2^(scale - e_j), a
-// half that is exact down to 2^-24; the sum takes the weights times 2^-e_j. So no spread of the rows' sizes
-// overflows, and a weight loses bits only 2^-29 below its head's largest contribution (value blocks whose scale
-// is 2^-24 below their row's largest, or below 2^-88, count as zero).
+// are rounded: with 2^e_j the largest scale of value row j's blocks that are not zero (2^-64 at least), the
+// running maximum is that of s_j + e_j, the weights w_j = 2^(s_j + e_j - maximum + 15) fill f16's range, and a
+// block's own scale enters as f = 2^(scale - e_j), a half that is exact down to 2^-24; the sum takes the weights
+// times 2^-e_j. So no spread of the rows' sizes overflows, and what is lost is, per block: f16(f16(w_j) f) is off by
+// 2^-11 of itself or, below 2^-14, by 2^-24; that is 2^-39 max_i(p_i 2^e_i) per unit of a code (p the normalised
+// weights; the largest is taken over all blocks, so a block that is small in every row has less of its own). Blocks
+// whose scale is 2^-24 below their row's largest, or below 2^-88, count as zero, and so do weights 2^-141 below the
+// largest s_j + e_j in the sum (fp32; rows' scales that far apart).
 //
 // Measured on one GB300 (share of the 6.78 TB/s of a plain copy), heads of 128, 8 query heads per key head unless
 // said: one sequence of 131072 tokens, 4 key heads, bf16, 49 us, 5.5 TB/s (0.81): 3 us until the first rows are
@@ -588,12 +591,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       // FP8: the scales of this lane's key for all lanes. Key blocks' scales as floats; e = the largest value scale
       // and 2^-e; value blocks' scales relative to e as halves ([key][2 * kWords] words: in the place of the step's
       // scale words where no other warp reads them, else apart from them). A block that holds an infinity (bytes
-      // 254 and 255) has an infinite factor and no part in e: it spoils its own 32 values only.
+      // 254 and 255) has an infinite factor and no part in e: it spoils its own 32 values only. A block of zeros (byte
+      // 127, however small the values around it) has no part in e either: with one, the other blocks' weights and
+      // factors would be in units of a contribution that is not there. Byte 127 is rare else (values up to 224 to
+      // 448), so codes are looked at only in steps that have one.
       if (C::kFp8) {
         const int own = lane & (kStep - 1);
         const bool writes = kTeam == 1 || own / (kStep / kTeam) == rank;   // two warps spread half of the keys each
         int top = 63;                                 // e + 127, at least -64 + 127: the sum takes 2^-e
-        uint32_t kb[C::kWords], vb[C::kWords], f[2 * C::kWords];
+        uint32_t kb[C::kWords], vb[C::kWords], f[2 * C::kWords], ones = 0;
 #pragma unroll
         for (int w = 0; w < C::kWords; ++w) {
           const uint32_t used = w + 1 == C::kWords ? scale_bytes : 0xFFFFFFFFu;
@@ -601,12 +607,27 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
           vb[w] = vw[own * C::kWords + w] & used;
           float y[4];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            y[z] = __uint_as_float(((kb[w] >> (8 * z)) & 0xFFu) << 23);
-            const int by = (int)((vb[w] >> (8 * z)) & 0xFFu);
-            if (by < 254) top = max(top, by);
-          }
+          for (int z = 0; z < 4; ++z) y[z] = __uint_as_float(((kb[w] >> (8 * z)) & 0xFFu) << 23);
           if (writes) *reinterpret_cast<float4*>(key_scales + (own * C::kWords + w) * 4) = make_float4(y[0], y[1], y[2], y[3]);
+          const uint32_t x = vb[w] ^ 0x7F7F7F7Fu;     // (a zero byte here: a byte 127 there)
+          ones |= (x - 0x01010101u) & ~x & 0x80808080u;
+        }
+        if (__any_sync(0xFFFFFFFFu, ones != 0)) {
+          const uint8_t* codes = ring + stage * C::kStageB + (kStep + own) * kRowB;
+#pragma unroll
+          for (int b = 0; b < DP / 32; ++b) {
+            const uint32_t byte = 0xFFu << (8 * (b & 3));
+            if ((vb[b / 4] & byte) == (0x7F7F7F7Fu & byte)) {
+              const uint4 x = *reinterpret_cast<const uint4*>(codes + ((uint32_t)(b << 5) ^ swz<kRowB>(own)));
+              const uint4 y = *reinterpret_cast<const uint4*>(codes + ((uint32_t)(b << 5 | 16) ^ swz<kRowB>(own)));
+              if (((x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu) == 0) vb[b / 4] &= ~byte;
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 4 * C::kWords; ++b) {
+          const int by = (int)((vb[b / 4] >> (8 * (b & 3))) & 0xFFu);
+          if (by < 254) top = max(top, by);
         }
         // e as a float: the integer behind 2^23
         if (writes)

@@ -566,8 +566,12 @@ size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_he
  *     s_j = scale * <q_h, k_j>,  out_h = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse_h = log sum_j exp(s_j)
  * A sequence with no tokens, or whose scores are all -inf, gives zeros and lse -inf. What lies in the
  * cache outside the attended tokens is not read into the result, whatever it holds. An attended infinity
- * may come out as NaN (operands enter as sums of two parts); in an FP8 cache a value block whose scale is
- * 2^-24 below its row's largest, or below 2^-88, counts as zero.
+ * may come out as NaN (operands enter as sums of two parts).
+ * Weights enter a bf16 cache's products with a relative error of 2^-16. Over an FP8 cache they enter each
+ * block as an f16: with p_j = exp(s_j - lse), c the codes' values, 2^e_j the largest scale of row j's value
+ * blocks that hold a value other than zero (2^-64 at least; a block of zeros has byte 127), value d is off by
+ *     2^-11 sum_j p_j |v_jd| + 2^-39 max_j(p_j 2^e_j) sum_j |c_jd|
+ * at most, and a value block whose scale is 2^-24 below its row's 2^e_j, or below 2^-88, counts as zero.
  *   q          rows [B, q_heads, head_dim], bf16 or fp32; q_heads a multiple of kv_heads
  *   seqs       lengths outside [0, table_width * page_size] are clamped (ENGRAM_ERR_SEQ_LEN); a page
  *              number outside the cache hides its tokens (ENGRAM_ERR_PAGE)
