@@ -124,16 +124,40 @@ _current_raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
 
 
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Plan:
     """A call of the library marshalled once for fixed tensors. The tensors are kept alive; run() enqueues
-    the call on `stream` (default: the current stream of the plan's device)."""
+    the call on `stream` (default: the current stream of the plan's device).
 
-    def __init__(self, fn: str, device, keep, *args):
+    What the plan made itself (`made`: outputs, a workspace and its zeros) belongs to the stream it was made
+    on: `home`. The first run on any other stream waits for what has been enqueued there, and the memory goes
+    back only when that stream is done with it, too. Nothing of this enters a graph: a run that is captured on
+    a stream of its own is the caller's to order after the plan's making (torch.cuda.graph synchronises)."""
+
+    def __init__(self, fn: str, device, keep, *args, made=(), home=None):
         self._name, self._fn, self._args, self._keep, self._device = fn, getattr(lib(), fn), args, keep, device
+        self._made = tuple(t for t in made if t is not None)
+        if self._made:
+            self._home = torch.cuda.current_stream(device) if home is None else home
+            self._ordered = {self._home.cuda_stream}
+
+    def _order(self, stream):
+        if _capturing(stream) or _capturing(self._home):
+            return
+        stream.wait_stream(self._home)
+        for t in self._made:
+            t.record_stream(stream)
+        self._ordered.add(stream.cuda_stream)
 
     def run(self, stream=None):
         index = self._device.index
         s = _current_raw_stream(index) if stream is None else stream.cuda_stream
+        if self._made and s not in self._ordered:
+            self._order(torch.cuda.current_stream(self._device) if stream is None else stream)
         if _current_device() == index:
             rc = self._fn(*self._args, s)
         else:
@@ -251,7 +275,7 @@ def attention_workspace_bytes(cache: KVCache, q_heads: int, batch: int) -> int:
 def attention_workspace(cache: KVCache, q_heads: int, batch: int) -> torch.Tensor:
     """A workspace of the attention calls on this cache for up to `batch` sequences. Its start
     (ATTENTION_ZERO_BYTES) is zero, and every call leaves it so: a program keeps one for calls that run in
-    order."""
+    order. The zeros are written on the current stream; calls on another one are the caller's to order after it."""
     n = attention_workspace_bytes(cache, q_heads, batch)
     if n == 0:
         raise ValueError(f"no workspace for {q_heads} query heads over {cache.kv_heads} key heads of {cache.head_dim}")
@@ -290,14 +314,17 @@ class QKNormRopePlan(_Plan):
         _err(err)
         _on(lead.device, q=q, k=k, positions=positions, q_out=q_out, k_out=k_out, err=err, q_weight=nr.q_weight,
             k_weight=nr.k_weight, table=nr.table)
+        made = []
         if q is not None and q_out is None:
             q_out = _alloc(q.shape, torch.bfloat16, q.device, stream)
+            made.append(q_out)
         if k is not None and k_out is None:
             k_out = _alloc(k.shape, torch.bfloat16, k.device, stream)
+            made.append(k_out)
         self.q_out, self.k_out = q_out, k_out
         ref = [None if t is None else C.byref(_heads(t)) for t in (q, k, q_out, k_out)]
         super().__init__("engram_qk_norm_rope", lead.device, (nr, q, k, positions, q_out, k_out, err), C.byref(nr._c), T, D,
-                         ref[0], ref[1], _ptr(positions), ref[2], ref[3], _ptr(err))
+                         ref[0], ref[1], _ptr(positions), ref[2], ref[3], _ptr(err), made=made, home=stream)
 
 
 class KVWritePlan(_Plan):
@@ -334,15 +361,20 @@ class KVReadPlan(_Plan):
         _err(err)
         _on(slots.device, slots=slots, k_out=k_out, v_out=v_out, err=err)
         cache._on(slots.device)
-        k_out = _alloc(shape, torch.bfloat16, slots.device, stream) if k_out is None else k_out
-        v_out = _alloc(shape, k_out.dtype, slots.device, stream) if v_out is None else v_out
+        made = []
+        if k_out is None:
+            k_out = _alloc(shape, torch.bfloat16, slots.device, stream)
+            made.append(k_out)
+        if v_out is None:
+            v_out = _alloc(shape, k_out.dtype, slots.device, stream)
+            made.append(v_out)
         self.k_out, self.v_out = k_out, v_out
         super().__init__("engram_kv_read", slots.device, (cache, slots, k_out, v_out, err), C.byref(cache._c), T, _ptr(slots),
-                         C.byref(_heads(k_out)), C.byref(_heads(v_out)), _ptr(err))
+                         C.byref(_heads(k_out)), C.byref(_heads(v_out)), _ptr(err), made=made, home=stream)
 
 
 def _attention_args(cache: KVCache, q, block_table, seq_lens, scale, window, out, lse, workspace, err, stream, need_batch: int):
-    """Checks and outputs of both attention plans: (seqs, scale, window, out, lse, workspace)."""
+    """Checks and outputs of both attention plans: (seqs, scale, window, out, lse, workspace, what was made here)."""
     _rows(q, "q")
     B, Hq, D = q.shape
     if D != cache.head_dim:
@@ -378,21 +410,25 @@ def _attention_args(cache: KVCache, q, block_table, seq_lens, scale, window, out
     _on(q.device, q=q, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse if isinstance(lse, torch.Tensor) else None,
         workspace=workspace, err=err)
     cache._on(q.device)
+    made = []
     if out is None:
         out = _alloc(q.shape, torch.bfloat16, q.device, stream)
+        made.append(out)
     if lse is True:
         lse = _alloc((B, Hq), torch.float32, q.device, stream)
+        made.append(lse)
     elif lse is False:
         lse = None
     if workspace is None:
         with torch.cuda.device(q.device), torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             workspace = attention_workspace(cache, Hq, need_batch)
+        made.append(workspace)
     # a table of one row, or of one column, may have any stride there
     stride = max(block_table.stride(0), block_table.shape[1]) if B > 1 else block_table.shape[1]
     if B > 1 and block_table.stride(0) < block_table.shape[1]:
         raise ValueError("block_table rows overlap")
     seqs = _Seqs(B, block_table.data_ptr(), stride, block_table.shape[1], seq_lens.data_ptr())
-    return seqs, (cache.head_dim ** -0.5 if scale is None else float(scale)), int(window), out, lse, workspace
+    return seqs, (cache.head_dim ** -0.5 if scale is None else float(scale)), int(window), out, lse, workspace, made
 
 
 class PagedAttentionPlan(_Plan):
@@ -403,12 +439,12 @@ class PagedAttentionPlan(_Plan):
 
     def __init__(self, cache: KVCache, q, block_table, seq_lens, scale=None, window: int = 0, out=None, lse=None, workspace=None,
                  err=None, stream=None):
-        seqs, scale, window, out, lse, workspace = _attention_args(cache, q, block_table, seq_lens, scale, window, out, lse,
-                                                                   workspace, err, stream, 0)
+        seqs, scale, window, out, lse, workspace, made = _attention_args(cache, q, block_table, seq_lens, scale, window, out, lse,
+                                                                         workspace, err, stream, 0)
         self.out, self.lse, self.workspace = out, lse, workspace
         super().__init__("engram_paged_attention", q.device, (cache, q, block_table, seq_lens, out, lse, workspace, err),
                          C.byref(cache._c), C.byref(seqs), C.byref(_heads(q)), scale, window, C.byref(_heads(out)), _ptr(lse),
-                         _ptr(workspace), workspace.numel(), _ptr(err))
+                         _ptr(workspace), workspace.numel(), _ptr(err), made=made, home=stream)
 
 
 class AttentionStepPlan(_Plan):
@@ -429,15 +465,15 @@ class AttentionStepPlan(_Plan):
         _vector(slots, B, torch.int64, "slots")
         if slots is None:
             raise ValueError("slots must be given")
-        seqs, scale, window, out, lse, workspace = _attention_args(cache, q, block_table, seq_lens, scale, window, out, lse,
-                                                                   workspace, err, stream, B)
+        seqs, scale, window, out, lse, workspace, made = _attention_args(cache, q, block_table, seq_lens, scale, window, out, lse,
+                                                                         workspace, err, stream, B)
         _on(q.device, k=k, v=v, positions=positions, slots=slots, q_weight=nr.q_weight, k_weight=nr.k_weight, table=nr.table)
         self.out, self.lse, self.workspace = out, lse, workspace
         super().__init__("engram_attention_step", q.device,
                          (nr, cache, q, k, v, positions, slots, block_table, seq_lens, out, lse, workspace, err), C.byref(nr._c),
                          C.byref(cache._c), C.byref(seqs), C.byref(_heads(q)), C.byref(_heads(k)), C.byref(_heads(v)),
                          _ptr(positions), _ptr(slots), scale, window, C.byref(_heads(out)), _ptr(lse), _ptr(workspace),
-                         workspace.numel(), _ptr(err))
+                         workspace.numel(), _ptr(err), made=made, home=stream)
 
 
 # ---------------------------------------------------------------------------------------------
