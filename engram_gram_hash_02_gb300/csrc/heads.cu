@@ -26,8 +26,10 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8]) {
   x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
 }
 
+// (Weights and angles too are read with ordinary loads: this kernel may start before the one that writes them ends,
+// and the non-coherent path wants data that nothing writes while a kernel lives.)
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
@@ -170,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
     }
     const float* row = p.nr.table + pos * p.nr.R;
     if (kPairs) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + (r0 >> 1)));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + (r0 >> 1)));
+      const float4 c = *reinterpret_cast<const float4*>(row + (r0 >> 1));
+      const float4 s = *reinterpret_cast<const float4*>(row + half + (r0 >> 1));
       A[0] = A[1] = c.x; A[2] = A[3] = c.y; A[4] = A[5] = c.z; A[6] = A[7] = c.w;
       B[0] = -s.x; B[1] = s.x; B[2] = -s.y; B[3] = s.y; B[4] = -s.z; B[5] = s.z; B[6] = -s.w; B[7] = s.w;
     } else {
@@ -188,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
   }
   if (wp != nullptr && live) {
     float w[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(wp + d0)), w);
+    unpack8(*reinterpret_cast<const uint4*>(wp + d0), w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) A[i] *= w[i];
     if (turned) {
-      if (!kPairs) unpack8(__ldg(reinterpret_cast<const uint4*>(wp + 8 * other)), w);
+      if (!kPairs) unpack8(*reinterpret_cast<const uint4*>(wp + 8 * other), w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) B[i] *= w[kPairs ? i ^ 1 : i];
     }

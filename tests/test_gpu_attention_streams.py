@@ -91,3 +91,30 @@ def test_the_function_forms_on_a_side_stream(fmt):
     side.synchronize()
     assert torch.equal(turned, q.bfloat16())
     H.check_attention(cache, table, lens, turned, out, lse, 0.125)
+
+
+def test_weights_and_angles_written_by_the_kernel_before():
+    # a call may start while the kernel that writes its weights and angles still runs: every call takes the new ones
+    E = H.pkg()
+    T, D = 600, 128
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k = torch.randn((T, 8, D), generator=g, device=DEV), torch.randn((T, 2, D), generator=g, device=DEV)
+    angles = [6.28 * torch.rand((64, D // 2), generator=g, device=DEV) for _ in range(3)]
+    tables = [torch.cat([a.cos(), a.sin()], 1) for a in angles]
+    weights = [(1 + 0.1 * torch.randn((2, D), generator=g, device=DEV)).bfloat16() for _ in range(3)]
+    pos = torch.randint(0, 64, (T,), generator=g, device=DEV, dtype=torch.int32)
+    want = []
+    for t, w in zip(tables, weights):
+        want.append(E.engram_qk_norm_rope(E.NormRope(w[0].clone(), w[1].clone(), 1e-6, t), q, k, pos))
+    table, weight = torch.empty_like(tables[0]), torch.empty_like(weights[0])
+    nr = E.NormRope(weight[0], weight[1], 1e-6, table)
+    outs = [tuple(torch.empty((T, h, D), dtype=torch.bfloat16, device=DEV) for h in (8, 2)) for _ in range(90)]
+    plans = [E.QKNormRopePlan(nr, q, k, pos, *o) for o in outs]
+    torch.cuda.synchronize()
+    for i, plan in enumerate(plans):
+        weight.copy_(weights[i % 3])
+        table.copy_(tables[i % 3])
+        plan.run()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(outs):
+        assert torch.equal(a, want[i % 3][0]) and torch.equal(b, want[i % 3][1]), f"call {i}"
