@@ -218,6 +218,7 @@ class KVCache:
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         _tensor(k, 4, "k")
+        _tensor(v, 4, "v")
         _shape(v, k.shape, "v")
         _typed(k, (torch.bfloat16, torch.uint8), "k")
         _typed(v, (k.dtype,), "v")
