@@ -400,7 +400,7 @@ def _attention_args(cache: KVCache, q, block_table, seq_lens, scale, window, out
         _typed(lse, (torch.float32,), "lse")
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
-    elif lse not in (None, True, False):
+    elif lse is not None and not isinstance(lse, bool):
         raise TypeError("lse must be a tensor, or True to return one")
     if workspace is not None:
         _tensor(workspace, 1, "workspace")
