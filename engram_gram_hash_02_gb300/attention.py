@@ -329,7 +329,8 @@ class QKNormRopePlan(_Plan):
 
 
 class KVWritePlan(_Plan):
-    """engram_kv_write for fixed tensors: k and v [T, kv_heads, D] of one type to int64 slots [T]."""
+    """engram_kv_write for fixed tensors: k and v [T, kv_heads, D] of one type to int64 slots [T], no two
+    of them the same (below 0: skipped)."""
 
     def __init__(self, cache: KVCache, k, v, slots, err=None):
         _rows(k, "k")

@@ -530,8 +530,9 @@ int engram_qk_norm_rope(const EngramNormRope* nr, int64_t T, int32_t head_dim, c
  * max|x| / 2^e <= 448 (byte 127 + e; 127 for an all-zero block) and each code is x / 2^e rounded to the
  * nearest e4m3 value, ties to even. NaN stays NaN; an infinity reads back as infinite (and the finite
  * values of its block as zero).
- *   slots  device int64 [T]: < 0 is skipped; past the cache is skipped and sets ENGRAM_ERR_SLOT. Two
- *          tokens with one slot leave one of the rows (which one is not defined)
+ *   slots  device int64 [T]: < 0 is skipped; past the cache is skipped and sets ENGRAM_ERR_SLOT. No two
+ *          tokens of a call may have one slot: rows are stored in pieces, in no order, so that place would
+ *          hold a mixture of both (in FP8 codes of one with scales of the other)
  */
 int engram_kv_write(const EngramKVCache* cache, int64_t T, const EngramHeads* k, const EngramHeads* v,
                     const int64_t* slots, int32_t* err_flag, engram_stream_t stream);
