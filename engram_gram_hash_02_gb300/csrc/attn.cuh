@@ -72,7 +72,8 @@ struct AttnParams {
   const int32_t* table;        // [B, width] page numbers
   int64_t table_stride;
   const int32_t* lens;         // [B]
-  int32_t lens_ready;          // 1: the preceding kernel does not write lens
+  int32_t lens_ready;          // 1: read before the wait: the preceding kernel does not write lens, and lets this one
+                               // start only after its own wait (what wrote them has finished)
   int32_t B, Hk, G, chunks;    // G query heads per key head, in `chunks` groups of at most 8 * NQ
   int32_t D;
   int32_t cap;                 // longest length the table holds (width * page_size, below 2^31)

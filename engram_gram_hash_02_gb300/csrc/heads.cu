@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 9) qkv_kernel(const __grid_constant_
   constexpr int kParts = kF32 ? 2 : 1;                // 16-byte chunks per lane
   __shared__ uint4 place_of[kRows][kThreads * kParts];
   pdl_wait();
-  pdl_trigger();
+  pdl_trigger();                                      // never before the wait: a step's attention reads lengths at its start
   const bool is_q = blockIdx.x < p.first_k, is_v = blockIdx.x >= p.first_v;
   const HeadRows in = is_q ? p.q : is_v ? p.v : p.k;
   const HeadRows out = is_q ? p.q_out : is_v ? HeadRows{} : p.k_out;

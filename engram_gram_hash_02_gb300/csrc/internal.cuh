@@ -65,7 +65,8 @@ class PerContextOnce {
 // their writes visible) before it reads anything a predecessor wrote or writes anything a
 // predecessor reads, and every CTA runs it before exiting; pdl_trigger() comes only after the
 // wait, so a dependent grid starts only once every earlier kernel but its immediate predecessor
-// has finished. Launched without the attribute (the single-stage entry points of the Engram path), both are
+// has finished. (A step's attention relies on that: it reads the lengths, which its predecessor does not
+// write, before its wait.) Launched without the attribute (the single-stage entry points of the Engram path), both are
 // no-ops. The attention calls always launch with it: their first kernel may start while whatever precedes it on
 // the stream finishes, which hides the launch (2 us of a call in a busy stream).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

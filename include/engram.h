@@ -450,7 +450,9 @@ int engram_forward_noalloc(const EngramDims* dims, const EngramHashTables* table
  * attention of one new token per sequence over that cache. Inference only.
  *
  * Every kernel is launched with programmatic stream serialization: it may start while its predecessor on
- * the stream finishes, and waits for it before it reads or writes anything of the caller's. All calls can be
+ * the stream finishes, and waits for it before it reads or writes anything of the caller's, with one exception:
+ * the second kernel of engram_attention_step reads seq_lens before it waits for the first. What wrote them is
+ * finished by then, because the first lets the second start only after its own wait. All calls can be
  * captured in CUDA graphs (after one call outside of capture on the device, which sets kernel attributes).
  */
 
