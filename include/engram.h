@@ -447,7 +447,8 @@ int engram_forward_noalloc(const EngramDims* dims, const EngramHashTables* table
  * The operators that stand next to an Engram layer when its model is served (no page counterpart;
  * the formulas are stated at each call): per-head norms of queries and keys with the position
  * rotation, rows written to a paged cache (bf16, or the FP8 tables' own format) and read back, and
- * attention of one new token per sequence over that cache. Inference only.
+ * attention of one new token per sequence over that cache. Inference only; for models with separate keys
+ * and values, each head's of one size up to 256 (one latent row shared by keys and values is another form).
  *
  * Every kernel is launched with programmatic stream serialization: it may start while its predecessor on
  * the stream finishes, and waits for it before it reads or writes anything of the caller's, with one exception:
@@ -572,16 +573,23 @@ size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_he
  * may come out as NaN (operands enter as sums of two parts).
  * Weights enter a bf16 cache's products with a relative error of 2^-16. Over an FP8 cache they enter each
  * block as an f16: with p_j = exp(s_j - lse), c the codes' values, 2^e_j the largest scale of row j's value
- * blocks that hold a value other than zero (2^-64 at least; a block of zeros has byte 127), value d is off by
+ * blocks (2^-64 at least; a block of zeros, known by its byte 127, has no part in it), value d is off by
  *     2^-11 sum_j p_j |v_jd| + 2^-39 max_j(p_j 2^e_j) sum_j |c_jd|
- * at most, and a value block whose scale is 2^-24 below its row's 2^e_j, or below 2^-88, counts as zero.
+ * at most, and a value block whose scale is 2^-24 below its row's 2^e_j, or below 2^-88, counts as zero. Its
+ * queries are f16 in units of their row (bf16) or two f16 (fp32): a value is off by 2^-38 of its row's largest
+ * at most, or 2^-22 of itself (fp32). The scores carry e_j while they are summed: lse is off by
+ * 2^-23 (|s_j| + |e_j| + 16) more than fp32 sums of s_j are.
  *   q          rows [B, q_heads, head_dim], bf16 or fp32; q_heads a multiple of kv_heads
  *   seqs       lengths outside [0, table_width * page_size] are clamped (ENGRAM_ERR_SEQ_LEN); a page
- *              number outside the cache hides its tokens (ENGRAM_ERR_PAGE)
+ *              number outside the cache hides its tokens (ENGRAM_ERR_PAGE). Refused if batch * kv_heads *
+ *              ceil(q_heads / kv_heads / 16) * ceil(n / 64) reaches 2^28, n the table's table_width *
+ *              page_size or a shorter window (tiles of 64 keys; of 128 over an FP8 cache with heads of up to
+ *              128 values or 9 or more query heads per key head): the division of the work counts in 32 bits
  *   out        bf16 rows [B, q_heads, head_dim]       lse  device fp32 [B, q_heads], or NULL
  *   workspace  device, 256-byte aligned, engram_attention_workspace_bytes. Its first
- *              ENGRAM_ATTENTION_ZERO_BYTES must be zero before the first use; every call leaves them zero. Calls that may overlap need
- *              workspaces of their own; calls in order may share one, whatever their shapes.
+ *              ENGRAM_ATTENTION_ZERO_BYTES must be zero before the first use; every call leaves them zero.
+ *              Calls that may overlap need workspaces of their own; calls in order may share one, whatever
+ *              their shapes.
  * Products take 16-bit operands with fp32 accumulation; scores, sums and lse are fp32. The work is cut
  * evenly over the GPU at token granularity and joined in the order of the tokens: results do not depend
  * on timing. One launch.
