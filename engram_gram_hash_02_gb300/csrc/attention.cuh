@@ -13,12 +13,12 @@
 // warp's chain from a landed copy to the next one short. (ncu: 11 to 17 % of that pipe's cycles in all of the shapes
 // below, tcgen05 or not: it has nothing to win here.)
 //
-// Work is cut at keys, not at sequences: the tiles (64 keys of bf16, 128 of FP8) of all sequences and key
-// heads form one row, sequence by sequence, and each CTA takes an equal run of it, so a batch of any mix of
-// lengths keeps every SM busy to the end. Each of a CTA's four warps owns a quarter of every tile and a
-// private ring of shared-memory stages filled by 16-byte cp.async (rows at the addresses their page gives;
-// any page size, stride or tail): no barrier joins the warps until a sequence's run ends. There the four
-// partial results are joined in shared memory. A run that is cut between CTAs is written to the workspace as
+// Work is cut at keys, not at sequences: the tiles of all sequences and key heads form one row, sequence by
+// sequence, and each CTA takes an equal run of it, so a batch of any mix of lengths keeps every SM busy to the
+// end. A tile is a step (step_keys: 16 or 32 keys) of each of a CTA's four rings of shared-memory stages, filled by
+// 16-byte cp.async (rows at the addresses their page gives; any page size, stride or tail). A ring belongs to one
+// warp, or to two (team_warps) that a named barrier joins at every step; no barrier joins the rings until a
+// sequence's run ends. There the four partial results are joined in shared memory. A run that is cut between CTAs is written to the workspace as
 // (unnormalised o, maximum, sum); the last CTA to arrive joins the parts in order of their keys, so results
 // do not depend on timing.
 //
@@ -37,12 +37,12 @@
 // said: one sequence of 131072 tokens, 4 key heads, bf16, 49 us, 5.5 TB/s (0.81): 3 us until the first rows are
 // there, then 7.3 TB/s, 5 us for the slowest SM and the join. 64 sequences of up to 8192 tokens, 2 key heads of 256,
 // bf16, 88 us, 6.1 TB/s (0.90). 256 sequences of up to 4096 tokens, 8 key heads with 4 query heads each, FP8, 173 us,
-// 6.4 TB/s (0.95): 690 instructions per 32 keys of 8448 bytes and twelve warps per SM to issue them. 48 windows of
-// 1024 tokens, 16 heads of 64, bf16, 38 us, 5.1 TB/s (0.75): 1.7 runs per CTA. One sequence of 777 tokens 6.1 us:
+// 6.4 TB/s (0.95): 710 instructions per 32 keys of 8448 bytes and twelve warps per SM to issue them. 48 windows of
+// 1024 tokens, 16 heads of 64, bf16, 37.3 us, 5.2 TB/s (0.77): 1.7 runs per CTA. One sequence of 777 tokens 6.1 us:
 // 1.2 us for lengths and page, 1 us for the rows, 0.5 us of computing, 2 us to join 13 parts.
 //
-// Roundings below 32 bits: with bf16 rows P is fed as the sum of two bf16 (hi + lo, 16 bits: 2^-17); with
-// FP8 rows as f16 (2^-12, an eighth of the output's own rounding). bf16 queries enter as they are; fp32
+// Roundings below 32 bits: with bf16 rows P is fed as the sum of two bf16 (hi + lo: 2^-16 at most); with
+// FP8 rows as f16 (2^-11, an eighth of the output's own rounding). bf16 queries enter as they are; fp32
 // queries as two bf16 or two f16; for f16 each query row is first scaled by a power of two (its largest
 // value below 2^14). Scores, maxima, sums and o are fp32.
 #pragma once
@@ -56,9 +56,10 @@ namespace attn {
 
 constexpr int kRings = 4;                             // of a CTA: its tile is a step of each
 constexpr int kGroup = 16;                            // parts of a cut run that one CTA joins
-// A run's fixed cost (its queries, the join of its warps), in tiles, when work is divided: with 2 (0), 64 sequences
-// of up to 8192 tokens, 2 key heads of 256, take 88 us (92), 256 of up to 4096 over FP8 189 (206), 48 windows of
-// 1024, 16 heads of 64, 38.7 (42.6)
+// A run's fixed cost (its queries, the join of its warps), in tiles, when work is divided. One constant for every
+// kernel, fitted on three shapes with 16 and more tiles per run (at an earlier state of the kernels): with 2 (0), 64
+// sequences of up to 8192 tokens, 2 key heads of 256, take 88 us (92), 256 of up to 4096 over FP8 189 (206), 48 windows
+// of 1024, 16 heads of 64, 38.7 (42.6). Runs of one or two tiles pay more than it says.
 constexpr int kRunCost = 2;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -126,7 +127,10 @@ constexpr int step_keys(bool fp8, int dp, int tiles) { return fp8 && !(dp == 256
 // CTAs per SM and stages per ring: as many warps as registers and shared memory allow, where instructions count
 // (FP8 in one tile: 256 sequences of heads of 128 take 173 us with three CTAs of two stages, 183 with two of three;
 // 64 of heads of 64 take 35.6 us with four of two, 37.2 with three of four), else three stages, which keep more
-// bytes in flight (bf16: one sequence of 131072 takes 49.3 us, 51.1 with three CTAs of two stages).
+// bytes in flight (bf16: one sequence of 131072 takes 49.3 us, 51.1 with three CTAs of two stages). All measured with
+// bf16 queries. Kernels for fp32 queries, which a decode step runs, take the same bounds; over FP8 those for one tile
+// of heads of 128 and of 64 spill 64 and 32 bytes, and a step of 256 sequences takes 198 us (its attention with bf16
+// queries 175).
 constexpr int resident_ctas(bool fp8, int dp, int tiles) {
   return tiles == 2 ? (dp == 256 ? 1 : 2) : (dp == 64 ? 3 : dp == 128 ? 2 : 1) + (fp8 ? 1 : 0);
 }
@@ -594,7 +598,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       // 254 and 255) has an infinite factor and no part in e: it spoils its own 32 values only. A block of zeros (byte
       // 127, however small the values around it) has no part in e either: with one, the other blocks' weights and
       // factors would be in units of a contribution that is not there. Byte 127 is rare else (values up to 224 to
-      // 448), so codes are looked at only in steps that have one.
+      // 448), so codes are looked at only in steps that have one (256 sequences of heads of 128 take 173 us, 185 if
+      // every scale is 1).
       if (C::kFp8) {
         const int own = lane & (kStep - 1);
         const bool writes = kTeam == 1 || own / (kStep / kTeam) == rank;   // two warps spread half of the keys each

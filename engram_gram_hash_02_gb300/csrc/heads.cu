@@ -106,7 +106,8 @@ __device__ __forceinline__ void wait_rows(int n) {
 // bytes in flight do not depend on registers, and the angles are fetched behind them. Norm and turn are
 //   out_i = r * (x_i * A_i + y_i * B_i),  r = 1 / sqrt(mean(x^2) + eps),  y_i the other value of x_i's pair,
 // with A_i = w_i cos, B_i = -+ w_y sin formed once per token; y comes from the partner lane's place. Nine CTAs
-// per SM (56 registers): with eight 118 us instead of 110 for 32768 tokens of 32 + 8 heads, with ten spills, 133.
+// per SM (registers for them: up to 56): with eight 118 us instead of 110 for 32768 tokens of 32 + 8 heads, with ten
+// spills, 133. That is bf16 rows; fp32 rows with 8 per group have 32 KB of places and six CTAs fit.
 // kPairs: values 2i and 2i + 1 are turned, else i and i + R/2 (one kernel for both has a quarter more instructions:
 // 110 us instead of 103 for the 32768 tokens above).
 template <int kLanes, bool kF32, bool kPairs, int kRows>
