@@ -575,7 +575,8 @@ size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_he
  * block as an f16: with p_j = exp(s_j - lse), c the codes' values, 2^e_j the largest scale of row j's value
  * blocks (2^-64 at least; a block of zeros, known by its byte 127, has no part in it), value d is off by
  *     2^-11 sum_j p_j |v_jd| + 2^-39 max_j(p_j 2^e_j) sum_j |c_jd|
- * at most, and a value block whose scale is 2^-24 below its row's 2^e_j, or below 2^-88, counts as zero. Its
+ * at most, and a value block whose scale is 2^-24 below its row's 2^e_j, or below 2^-88, counts as zero (in
+ * the sum, so does a p_j whose p_j 2^e_j is 2^-141 below the largest: rows' scales at least 2^117 apart). Its
  * queries are f16 in units of their row (bf16) or two f16 (fp32): a value is off by 2^-38 of its row's largest
  * at most, or 2^-22 of itself (fp32). The scores carry e_j while they are summed: lse is off by
  * 2^-23 (|s_j| + |e_j| + 16) more than fp32 sums of s_j are.
