@@ -138,8 +138,8 @@ def test_one_scale_for_every_value(D, G, q_type):
     attend(LENS, D, G, q_type, make, unit=True)
 
 
-def test_two_rows_of_codes_but_no_more():
-    """A block that looks like zeros at one place only, in each place of the 32, is not taken for one."""
+def test_a_block_of_one_value_is_not_taken_for_zeros():
+    """Scale 1, as a block of zeros has it, and one value, in each place of the 32."""
     D, G = 128, 4
 
     def make(g, n):
