@@ -3,7 +3,9 @@
 The layer's attention next to its Engram residual: per-head norms of queries and keys with the
 position rotation, rows written to a paged key-value cache (bf16, or e4m3 codes with one scale byte
 per 32 values) and read back, attention of one new token per sequence over the cache, and all of
-them as one decode step.
+them as one decode step; attention of all tokens of prompts (causal, with a window, documents or a
+prefix seen both ways), and of batches whose sequences share a prefix. Scores may be capped by a tanh
+(``cap``) and carry a bias that falls with distance (``slopes``).
 
 Every call has two forms, as ``engram_forward`` has: a function that checks, runs and returns its
 outputs, and a plan (``...Plan``) that marshals the call once for fixed tensors and runs it with one
@@ -47,6 +49,14 @@ class _NormRope(C.Structure):
 class _Seqs(C.Structure):
     _fields_ = [("batch", C.c_int32), ("block_table", C.c_void_p), ("table_stride", C.c_int64),
                 ("table_width", C.c_int32), ("seq_lens", C.c_void_p)]
+
+
+class _Scores(C.Structure):
+    _fields_ = [("cap", C.c_float), ("slopes", C.c_void_p)]
+
+
+class _Visible(C.Structure):
+    _fields_ = [("causal", C.c_int32), ("window", C.c_int32), ("doc_starts", C.c_void_p), ("prefix_ends", C.c_void_p)]
 
 
 # ---------------------------------------------------------------------------------------------
@@ -273,16 +283,39 @@ def attention_workspace_bytes(cache: KVCache, q_heads: int, batch: int) -> int:
     return int(lib().engram_attention_workspace_bytes(C.byref(cache._c), int(q_heads), int(batch)))
 
 
-def attention_workspace(cache: KVCache, q_heads: int, batch: int) -> torch.Tensor:
-    """A workspace of the attention calls on this cache for up to `batch` sequences. Its start
-    (ATTENTION_ZERO_BYTES) is zero, and every call leaves it so: a program keeps one for calls that run in
-    order. The zeros are written on the current stream; calls on another one are the caller's to order after it."""
-    n = attention_workspace_bytes(cache, q_heads, batch)
+def _workspace(n: int, cache: KVCache, q_heads: int) -> torch.Tensor:
     if n == 0:
         raise ValueError(f"no workspace for {q_heads} query heads over {cache.kv_heads} key heads of {cache.head_dim}")
     ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
     ws[:ATTENTION_ZERO_BYTES].zero_()
     return ws
+
+
+def attention_workspace(cache: KVCache, q_heads: int, batch: int) -> torch.Tensor:
+    """A workspace of the attention calls on this cache for up to `batch` sequences. Its start
+    (ATTENTION_ZERO_BYTES) is zero, and every call leaves it so: a program keeps one for calls that run in
+    order. The zeros are written on the current stream; calls on another one are the caller's to order after it."""
+    return _workspace(attention_workspace_bytes(cache, q_heads, batch), cache, q_heads)
+
+
+def prompt_workspace_bytes(cache: KVCache, q_heads: int, tokens: int, batch: int) -> int:
+    return int(lib().engram_prompt_workspace_bytes(C.byref(cache._c), int(q_heads), int(tokens), int(batch)))
+
+
+def prompt_workspace(cache: KVCache, q_heads: int, tokens: int, batch: int) -> torch.Tensor:
+    """A workspace of engram_prompt_attention on this cache for up to `tokens` new tokens of `batch` sequences; as
+    ``attention_workspace``, and one that is large enough serves all the attention calls in order."""
+    return _workspace(prompt_workspace_bytes(cache, q_heads, tokens, batch), cache, q_heads)
+
+
+def shared_workspace_bytes(cache: KVCache, q_heads: int, batch: int, groups: int) -> int:
+    return int(lib().engram_shared_workspace_bytes(C.byref(cache._c), int(q_heads), int(batch), int(groups)))
+
+
+def shared_workspace(cache: KVCache, q_heads: int, batch: int, groups: int) -> torch.Tensor:
+    """A workspace of engram_shared_attention on this cache for up to `batch` sequences in `groups` groups; as
+    ``attention_workspace``."""
+    return _workspace(shared_workspace_bytes(cache, q_heads, batch, groups), cache, q_heads)
 
 
 # ---------------------------------------------------------------------------------------------
@@ -375,29 +408,52 @@ class KVReadPlan(_Plan):
                          C.byref(_heads(k_out)), C.byref(_heads(v_out)), _ptr(err), made=made, home=stream)
 
 
-def _attention_args(cache: KVCache, q, block_table, seq_lens, scale, window, out, lse, workspace, err, stream, need_batch: int):
-    """Checks and outputs of both attention plans: (seqs, scale, window, out, lse, workspace, what was made here)."""
-    _rows(q, "q")
-    B, Hq, D = q.shape
-    if D != cache.head_dim:
-        raise ValueError(f"q has heads of {D} but the cache of {cache.head_dim}")
-    if Hq < 1 or Hq % cache.kv_heads:
-        raise ValueError(f"q must have a multiple of the cache's {cache.kv_heads} heads (got {Hq})")
-    _tensor(block_table, 2, "block_table")
-    _shape(block_table, (B, block_table.shape[1]), "block_table")
-    _typed(block_table, (torch.int32,), "block_table")
+def _scores(cap, slopes, q_heads: int):
+    """Checks of a form of scores: the EngramScores, or None without one."""
+    cap = float(cap)
+    if cap != 0.0 and not 2.0 ** -60 <= cap <= 2.0 ** 60:
+        raise ValueError(f"cap must be 0 or in [2^-60, 2^60] (got {cap})")
+    if slopes is not None:
+        _tensor(slopes, 1, "slopes")
+        _vector(slopes, q_heads, torch.float32, "slopes")
+    return None if cap == 0.0 and slopes is None else _Scores(cap, _ptr(slopes))
+
+
+def _paged_seqs(block_table, seq_lens, B: int, table: str = "block_table", lens: str = "seq_lens") -> _Seqs:
+    """Checks of a page table and its lengths."""
+    _tensor(block_table, 2, table)
+    _shape(block_table, (B, block_table.shape[1]), table)
+    _typed(block_table, (torch.int32,), table)
     if block_table.shape[1] > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table must have contiguous rows")
-    _vector(seq_lens, B, torch.int32, "seq_lens")
+        raise ValueError(f"{table} must have contiguous rows")
+    _vector(seq_lens, B, torch.int32, lens)
     if seq_lens is None:
-        raise ValueError("seq_lens must be given")
-    if int(window) < 0:
-        raise ValueError(f"window must be >= 0 (got {window})")
+        raise ValueError(f"{lens} must be given")
+    # a table of one row, or of one column, may have any stride there
+    stride = max(block_table.stride(0), block_table.shape[1]) if B > 1 else block_table.shape[1]
+    if B > 1 and block_table.stride(0) < block_table.shape[1]:
+        raise ValueError(f"{table} rows overlap")
+    return _Seqs(B, block_table.data_ptr(), stride, block_table.shape[1], seq_lens.data_ptr())
+
+
+def _query(cache: KVCache, q, dtypes=tuple(_TYPES)):
+    _rows(q, "q")
+    _typed(q, dtypes, "q")
+    if q.shape[2] != cache.head_dim:
+        raise ValueError(f"q has heads of {q.shape[2]} but the cache of {cache.head_dim}")
+    if q.shape[1] < 1 or q.shape[1] % cache.kv_heads:
+        raise ValueError(f"q must have a multiple of the cache's {cache.kv_heads} heads (got {q.shape[1]})")
+    return q.shape
+
+
+def _attention_outputs(cache: KVCache, q, out, lse, workspace, err, stream, make_workspace, **others):
+    """Checks and makes what an attention writes: (out, lse, workspace, what was made here). `others`: its other tensors."""
+    T, Hq, _ = q.shape
     if out is not None:
         _rows(out, "out", q.shape)
         _typed(out, (torch.bfloat16,), "out")
     if isinstance(lse, torch.Tensor):
-        _shape(lse, (B, Hq), "lse")
+        _shape(lse, (T, Hq), "lse")
         _typed(lse, (torch.float32,), "lse")
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
@@ -409,44 +465,58 @@ def _attention_args(cache: KVCache, q, block_table, seq_lens, scale, window, out
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     _err(err)
-    _on(q.device, q=q, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse if isinstance(lse, torch.Tensor) else None,
-        workspace=workspace, err=err)
+    _on(q.device, q=q, out=out, lse=lse if isinstance(lse, torch.Tensor) else None, workspace=workspace, err=err, **others)
     cache._on(q.device)
     made = []
     if out is None:
         out = _alloc(q.shape, torch.bfloat16, q.device, stream)
         made.append(out)
     if lse is True:
-        lse = _alloc((B, Hq), torch.float32, q.device, stream)
+        lse = _alloc((T, Hq), torch.float32, q.device, stream)
         made.append(lse)
     elif lse is False:
         lse = None
     if workspace is None:
         with torch.cuda.device(q.device), torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            workspace = attention_workspace(cache, Hq, need_batch)
+            workspace = make_workspace()
         made.append(workspace)
-    # a table of one row, or of one column, may have any stride there
-    stride = max(block_table.stride(0), block_table.shape[1]) if B > 1 else block_table.shape[1]
-    if B > 1 and block_table.stride(0) < block_table.shape[1]:
-        raise ValueError("block_table rows overlap")
-    seqs = _Seqs(B, block_table.data_ptr(), stride, block_table.shape[1], seq_lens.data_ptr())
-    return seqs, (cache.head_dim ** -0.5 if scale is None else float(scale)), int(window), out, lse, workspace, made
+    return out, lse, workspace, made
+
+
+def _scale(cache: KVCache, scale) -> float:
+    return cache.head_dim ** -0.5 if scale is None else float(scale)
+
+
+def _attention_args(cache: KVCache, q, block_table, seq_lens, scale, window, cap, slopes, out, lse, workspace, err, stream,
+                    need_batch: int):
+    """Checks and outputs of both one-token plans: (seqs, scale, window, scores, out, lse, workspace, what was made here)."""
+    B, Hq, _ = _query(cache, q)
+    seqs = _paged_seqs(block_table, seq_lens, B)
+    if int(window) < 0:
+        raise ValueError(f"window must be >= 0 (got {window})")
+    scores = _scores(cap, slopes, Hq)
+    out, lse, workspace, made = _attention_outputs(cache, q, out, lse, workspace, err, stream,
+                                                   lambda: attention_workspace(cache, Hq, need_batch), block_table=block_table,
+                                                   seq_lens=seq_lens, slopes=slopes)
+    return seqs, _scale(cache, scale), int(window), scores, out, lse, workspace, made
 
 
 class PagedAttentionPlan(_Plan):
     """engram_paged_attention for fixed tensors: q [B, Hq, D] (bf16 or fp32) over the cached tokens of B
     sequences (block_table int32 [B, width], seq_lens int32 [B]). scale defaults to D^-1/2; lse may be a
     tensor fp32 [B, Hq], or True to have one. Without a workspace the plan makes its own; plans that
-    share one must run in order."""
+    share one must run in order. With a cap (scores cap * tanh(s / cap)) or slopes (fp32 [Hq]: -slope per
+    token of distance) it is engram_paged_attention2."""
 
     def __init__(self, cache: KVCache, q, block_table, seq_lens, scale=None, window: int = 0, out=None, lse=None, workspace=None,
-                 err=None, stream=None):
-        seqs, scale, window, out, lse, workspace, made = _attention_args(cache, q, block_table, seq_lens, scale, window, out, lse,
-                                                                         workspace, err, stream, 0)
+                 err=None, stream=None, cap: float = 0.0, slopes=None):
+        seqs, scale, window, scores, out, lse, workspace, made = _attention_args(cache, q, block_table, seq_lens, scale, window, cap,
+                                                                                 slopes, out, lse, workspace, err, stream, 0)
         self.out, self.lse, self.workspace = out, lse, workspace
-        super().__init__("engram_paged_attention", q.device, (cache, q, block_table, seq_lens, out, lse, workspace, err),
-                         C.byref(cache._c), C.byref(seqs), C.byref(_heads(q)), scale, window, C.byref(_heads(out)), _ptr(lse),
-                         _ptr(workspace), workspace.numel(), _ptr(err), made=made, home=stream)
+        fn, form = ("engram_paged_attention", ()) if scores is None else ("engram_paged_attention2", (C.byref(scores),))
+        super().__init__(fn, q.device, (cache, q, block_table, seq_lens, slopes, out, lse, workspace, err), C.byref(cache._c),
+                         C.byref(seqs), C.byref(_heads(q)), scale, window, *form, C.byref(_heads(out)), _ptr(lse), _ptr(workspace),
+                         workspace.numel(), _ptr(err), made=made, home=stream)
 
 
 class AttentionStepPlan(_Plan):
@@ -454,7 +524,7 @@ class AttentionStepPlan(_Plan):
     type), positions int32 [B] and slots int64 [B]; the rest as PagedAttentionPlan."""
 
     def __init__(self, nr: NormRope, cache: KVCache, q, k, v, positions, slots, block_table, seq_lens, scale=None, window: int = 0,
-                 out=None, lse=None, workspace=None, err=None, stream=None):
+                 out=None, lse=None, workspace=None, err=None, stream=None, cap: float = 0.0, slopes=None):
         _rows(q, "q")
         B, _, D = q.shape
         nr._fits(D)
@@ -467,14 +537,80 @@ class AttentionStepPlan(_Plan):
         _vector(slots, B, torch.int64, "slots")
         if slots is None:
             raise ValueError("slots must be given")
-        seqs, scale, window, out, lse, workspace, made = _attention_args(cache, q, block_table, seq_lens, scale, window, out, lse,
-                                                                         workspace, err, stream, B)
+        seqs, scale, window, scores, out, lse, workspace, made = _attention_args(cache, q, block_table, seq_lens, scale, window, cap,
+                                                                                 slopes, out, lse, workspace, err, stream, B)
         _on(q.device, k=k, v=v, positions=positions, slots=slots, q_weight=nr.q_weight, k_weight=nr.k_weight, table=nr.table)
         self.out, self.lse, self.workspace = out, lse, workspace
-        super().__init__("engram_attention_step", q.device,
-                         (nr, cache, q, k, v, positions, slots, block_table, seq_lens, out, lse, workspace, err), C.byref(nr._c),
+        fn, form = ("engram_attention_step", ()) if scores is None else ("engram_attention_step2", (C.byref(scores),))
+        super().__init__(fn, q.device,
+                         (nr, cache, q, k, v, positions, slots, block_table, seq_lens, slopes, out, lse, workspace, err), C.byref(nr._c),
                          C.byref(cache._c), C.byref(seqs), C.byref(_heads(q)), C.byref(_heads(k)), C.byref(_heads(v)),
-                         _ptr(positions), _ptr(slots), scale, window, C.byref(_heads(out)), _ptr(lse), _ptr(workspace),
+                         _ptr(positions), _ptr(slots), scale, window, *form, C.byref(_heads(out)), _ptr(lse), _ptr(workspace),
+                         workspace.numel(), _ptr(err), made=made, home=stream)
+
+
+class PromptAttentionPlan(_Plan):
+    """engram_prompt_attention for fixed tensors: all new tokens q [T, Hq, D] (bf16) of B sequences, sequence b's the rows
+    [cu_seqlens[b], cu_seqlens[b + 1]), over their cached tokens (block_table int32 [B, width], seq_lens int32 [B] with the
+    new ones). New token i of n stands at position p = len - n + i and sees the keys [lo, hi): up to itself (causal), or up to
+    prefix_ends[t] if that is further (int32 [T]); from doc_starts[t] on (int32 [T]), and at most `window` of them up to
+    itself. out and lse keep what they hold in rows that belong to no sequence. The rest as PagedAttentionPlan."""
+
+    def __init__(self, cache: KVCache, q, cu_seqlens, block_table, seq_lens, scale=None, causal: bool = True, window: int = 0,
+                 doc_starts=None, prefix_ends=None, cap: float = 0.0, slopes=None, out=None, lse=None, workspace=None, err=None,
+                 stream=None):
+        T, Hq, _ = _query(cache, q, (torch.bfloat16,))
+        _tensor(cu_seqlens, 1, "cu_seqlens")
+        B = cu_seqlens.shape[0] - 1
+        if B < 0:
+            raise ValueError("cu_seqlens must have an entry for each sequence, and the end")
+        _vector(cu_seqlens, B + 1, torch.int32, "cu_seqlens")
+        seqs = _paged_seqs(block_table, seq_lens, B)
+        if int(window) < 0:
+            raise ValueError(f"window must be >= 0 (got {window})")
+        _vector(doc_starts, T, torch.int32, "doc_starts")
+        _vector(prefix_ends, T, torch.int32, "prefix_ends")
+        if prefix_ends is not None and not causal:
+            raise ValueError("prefix_ends are for causal attention")
+        scores = _scores(cap, slopes, Hq)
+        out, lse, workspace, made = _attention_outputs(cache, q, out, lse, workspace, err, stream,
+                                                       lambda: prompt_workspace(cache, Hq, T, B), cu_seqlens=cu_seqlens,
+                                                       block_table=block_table, seq_lens=seq_lens, doc_starts=doc_starts,
+                                                       prefix_ends=prefix_ends, slopes=slopes)
+        self.out, self.lse, self.workspace = out, lse, workspace
+        visible = _Visible(1 if causal else 0, int(window), _ptr(doc_starts), _ptr(prefix_ends))
+        super().__init__("engram_prompt_attention", q.device,
+                         (cache, q, cu_seqlens, block_table, seq_lens, doc_starts, prefix_ends, slopes, out, lse, workspace, err),
+                         C.byref(cache._c), C.byref(seqs), T, _ptr(cu_seqlens), C.byref(_heads(q)), _scale(cache, scale),
+                         C.byref(visible), None if scores is None else C.byref(scores), C.byref(_heads(out)), _ptr(lse),
+                         _ptr(workspace), workspace.numel(), _ptr(err), made=made, home=stream)
+
+
+class SharedAttentionPlan(_Plan):
+    """engram_shared_attention for fixed tensors: one new token q [B, Hq, D] (bf16) of each of B sequences, those of group g
+    the rows [groups[g], groups[g + 1]) (int32 [n + 1]), over the group's prefix (prefix_table int32 [n, width], prefix_lens
+    int32 [n]) and then over the sequence's own tokens (block_table, seq_lens). The rest as PagedAttentionPlan."""
+
+    def __init__(self, cache: KVCache, q, prefix_table, prefix_lens, groups, block_table, seq_lens, scale=None, cap: float = 0.0,
+                 slopes=None, out=None, lse=None, workspace=None, err=None, stream=None):
+        B, Hq, _ = _query(cache, q, (torch.bfloat16,))
+        _tensor(groups, 1, "groups")
+        n = groups.shape[0] - 1
+        if n < 0:
+            raise ValueError("groups must have an entry for each group, and the end")
+        _vector(groups, n + 1, torch.int32, "groups")
+        prefix = _paged_seqs(prefix_table, prefix_lens, n, "prefix_table", "prefix_lens")
+        seqs = _paged_seqs(block_table, seq_lens, B)
+        scores = _scores(cap, slopes, Hq)
+        out, lse, workspace, made = _attention_outputs(cache, q, out, lse, workspace, err, stream,
+                                                       lambda: shared_workspace(cache, Hq, B, n), prefix_table=prefix_table,
+                                                       prefix_lens=prefix_lens, groups=groups, block_table=block_table,
+                                                       seq_lens=seq_lens, slopes=slopes)
+        self.out, self.lse, self.workspace = out, lse, workspace
+        super().__init__("engram_shared_attention", q.device,
+                         (cache, q, prefix_table, prefix_lens, groups, block_table, seq_lens, slopes, out, lse, workspace, err),
+                         C.byref(cache._c), C.byref(prefix), _ptr(groups), C.byref(seqs), C.byref(_heads(q)), _scale(cache, scale),
+                         None if scores is None else C.byref(scores), C.byref(_heads(out)), _ptr(lse), _ptr(workspace),
                          workspace.numel(), _ptr(err), made=made, home=stream)
 
 
@@ -502,18 +638,37 @@ def engram_kv_read(cache: KVCache, slots, k_out=None, v_out=None, err=None, stre
 
 
 def engram_paged_attention(cache: KVCache, q, block_table, seq_lens, scale=None, window: int = 0, out=None, lse=None, workspace=None,
-                           err=None, stream=None):
+                           err=None, stream=None, cap: float = 0.0, slopes=None):
     """Attention of one token per sequence; returns out, or (out, lse) if lse was asked for. See
     PagedAttentionPlan."""
-    plan = PagedAttentionPlan(cache, q, block_table, seq_lens, scale, window, out, lse, workspace, err, stream)
+    plan = PagedAttentionPlan(cache, q, block_table, seq_lens, scale, window, out, lse, workspace, err, stream, cap, slopes)
     plan.run(stream)
     return plan.out if plan.lse is None else (plan.out, plan.lse)
 
 
 def engram_attention_step(nr: NormRope, cache: KVCache, q, k, v, positions, slots, block_table, seq_lens, scale=None, window: int = 0,
-                          out=None, lse=None, workspace=None, err=None, stream=None):
+                          out=None, lse=None, workspace=None, err=None, stream=None, cap: float = 0.0, slopes=None):
     """One decode step of a layer's attention; returns out, or (out, lse). See AttentionStepPlan."""
     plan = AttentionStepPlan(nr, cache, q, k, v, positions, slots, block_table, seq_lens, scale, window, out, lse, workspace, err,
-                             stream)
+                             stream, cap, slopes)
+    plan.run(stream)
+    return plan.out if plan.lse is None else (plan.out, plan.lse)
+
+
+def engram_prompt_attention(cache: KVCache, q, cu_seqlens, block_table, seq_lens, scale=None, causal: bool = True, window: int = 0,
+                            doc_starts=None, prefix_ends=None, cap: float = 0.0, slopes=None, out=None, lse=None, workspace=None,
+                            err=None, stream=None):
+    """Attention of all new tokens of ragged sequences; returns out, or (out, lse). See PromptAttentionPlan."""
+    plan = PromptAttentionPlan(cache, q, cu_seqlens, block_table, seq_lens, scale, causal, window, doc_starts, prefix_ends, cap, slopes,
+                               out, lse, workspace, err, stream)
+    plan.run(stream)
+    return plan.out if plan.lse is None else (plan.out, plan.lse)
+
+
+def engram_shared_attention(cache: KVCache, q, prefix_table, prefix_lens, groups, block_table, seq_lens, scale=None, cap: float = 0.0,
+                            slopes=None, out=None, lse=None, workspace=None, err=None, stream=None):
+    """Attention of one token per sequence where groups share a prefix; returns out, or (out, lse). See SharedAttentionPlan."""
+    plan = SharedAttentionPlan(cache, q, prefix_table, prefix_lens, groups, block_table, seq_lens, scale, cap, slopes, out, lse,
+                               workspace, err, stream)
     plan.run(stream)
     return plan.out if plan.lse is None else (plan.out, plan.lse)

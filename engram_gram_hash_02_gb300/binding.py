@@ -122,6 +122,14 @@ def lib() -> C.CDLL:
         L.engram_attention_workspace_bytes.restype = SZ
         L.engram_paged_attention.argtypes = [P, P, P, C.c_float, I32, P, P, P, SZ, P, P]
         L.engram_attention_step.argtypes = [P, P, P, P, P, P, P, P, C.c_float, I32, P, P, P, SZ, P, P]
+        L.engram_paged_attention2.argtypes = [P, P, P, C.c_float, I32, P, P, P, P, SZ, P, P]
+        L.engram_attention_step2.argtypes = [P, P, P, P, P, P, P, P, C.c_float, I32, P, P, P, P, SZ, P, P]
+        L.engram_prompt_workspace_bytes.argtypes = [P, I32, I64, I32]
+        L.engram_prompt_workspace_bytes.restype = SZ
+        L.engram_prompt_attention.argtypes = [P, P, I64, P, P, C.c_float, P, P, P, P, P, SZ, P, P]
+        L.engram_shared_workspace_bytes.argtypes = [P, I32, I32, I32]
+        L.engram_shared_workspace_bytes.restype = SZ
+        L.engram_shared_attention.argtypes = [P, P, P, P, P, C.c_float, P, P, P, P, SZ, P, P]
         _lib = L
     return _lib
 

@@ -110,11 +110,6 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
   asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // exp2(x - m) for m = max(x, ...): a maximum of -inf (nothing attended yet) gives 0
 __device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
 
@@ -136,7 +131,7 @@ constexpr int resident_ctas(bool fp8, int dp, int tiles) {
 }
 constexpr int ring_stages(bool fp8, int dp, int tiles) { return fp8 && tiles == 1 && dp <= 128 ? 2 : 3; }
 
-template <int DP_, bool kFp8_, int kTiles_, bool kSplit_>
+template <int DP_, bool kFp8_, int kTiles_, bool kSplit_, bool kForm_>
 struct Cfg {
   static constexpr int DP = DP_;                      // head_dim rounded up to 64, 128 or 256
   static constexpr bool kFp8 = kFp8_;
@@ -147,6 +142,7 @@ struct Cfg {
   static constexpr int kWarps = kRings * kTeam;
   static constexpr int kThreads = kWarps * 32;
   static constexpr bool kSplit = kSplit_;             // fp32 queries: high and low parts
+  static constexpr bool kForm = kForm_;               // scores with a form, or a part of the keys attended before
   static constexpr int kStep = step_keys(kFp8, DP, kTiles);   // keys per ring and step
   static constexpr int kTile = kRings * kStep;
   static constexpr int kRowB = kFp8 ? DP : 2 * DP;
@@ -181,11 +177,35 @@ struct Meta {
   uint32_t mask;               // keys of the step that are attended
   uint32_t ends;               // bit 0: first tile of its run, bit 1: last
   int32_t seq, hc, run0, tiles;// sequence, head * chunks + chunk, place of the run's first tile and its tiles
-  int32_t pad[2];
+  int32_t back, pad;           // kForm: the step's first key is `back` tokens before the sequence's last
 };
 
 __device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : len > cap ? cap : len; }
 __device__ __forceinline__ int attended(int len, int window) { return window > 0 && len > window ? window : len; }
+
+// log2(l 2^m), l a positive float: l's exponent joins m before the logarithm, as the two may be large and of opposite
+// sign (FP8). -inf for l = 0; a NaN or an infinite l comes back as it is.
+__device__ __forceinline__ float log2_of_sum(float m, float l) {
+  const uint32_t b = __float_as_uint(l);
+  const float y = (m + (float)((int)(b >> 23) - 127)) + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u));
+  return l == 0.f ? -INFINITY : l - l == 0.f ? y : l;
+}
+
+// A head's attended values x (four from value d on) over its own keys, whose exponentials sum to 2^own, joined with
+// those over the keys that were attended before (prior_o, prior_lse)
+__device__ __forceinline__ void emit_joined(const AttnParams& p, int seq, int head, int d, const float (&x)[4], float own) {
+  const int64_t row = (int64_t)seq * (p.Hk * p.G) + head;
+  const float before = __ldcg(p.prior_lse + row);
+  const float4 y = __ldcg(reinterpret_cast<const float4*>(p.prior_o + row * p.D + d));
+  const float m = fmaxf(own, before);
+  const float a = ex2_rel(own, m), b = ex2_rel(before, m), sum = a + b;
+  const float fa = sum == 0.f ? 0.f : a / sum, fb = sum == 0.f ? 0.f : b / sum;
+  uint2 w;
+  w.x = pack_bf16(x[0] * fa + y.x * fb, x[1] * fa + y.y * fb);
+  w.y = pack_bf16(x[2] * fa + y.z * fb, x[3] * fa + y.w * fb);
+  *reinterpret_cast<uint2*>(p.out + (int64_t)seq * p.out_ts + (int64_t)head * p.out_hs + d) = w;
+  if (d == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(sum));
+}
 
 template <typename C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const AttnParams p) {
@@ -358,6 +378,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       Meta m;
       m.mask = mask; m.ends = (tile == 0 ? 1u : 0u) | (tile + 1 == tiles ? 2u : 0u);
       m.seq = seq; m.hc = hc; m.run0 = run0; m.tiles = tiles;
+      if (C::kForm) m.back = end - 1 - (first + tile * C::kTile + my_ring * kStep);
       meta[stage] = m;
     }
     if (mask == 0) return;                            // no keys for this warp: the stage is not read
@@ -438,6 +459,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
   float m_run[NQ][2], l_run[NQ][2];
   uint32_t qf[C::kQRegs ? NQ : 1][C::kQRegs ? DP / 16 : 1][C::kSplit ? 4 : 2];
   int rows = 0;                                       // query heads of this run
+  // Scores with a form, in units of log 2
+  float slope[C::kForm ? NQ : 1][2];                  // of this lane's two heads per tile
+  auto form = [&](float x, float slope, int back) {
+    if (p.form.cap2 > 0.f) x = capped(x, p.form.cap2, p.form.cap_inv);
+    return p.form.slopes != nullptr ? fmaf(-slope, (float)back, x) : x;
+  };
 
   auto q_frag = [&](int nq, int ks, uint32_t (&b)[4]) {
     const uint8_t* row = qs + (((rank * NQ + nq) * 8 + g) * C::kQPitch + ks * 16) * 2;
@@ -498,6 +525,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     cp_async_wait<kStages - 2>();
     sync_ring();
     const uint32_t mask = meta[stage].mask, ends = meta[stage].ends;
+    const int back = C::kForm ? meta[stage].back : 0;
 
     if (i == 0 || (ends & 1u)) {
       // a new run: its query rows to shared memory (16-bit, zero rows and columns as padding)
@@ -547,6 +575,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
             q_frag(nq, ks, b);
 #pragma unroll
             for (int e = 0; e < (C::kSplit ? 4 : 2); ++e) qf[nq][ks][e] = b[e];
+          }
+      }
+      if (C::kForm && p.form.slopes != nullptr) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int h = (rank * NQ + nq) * 8 + 2 * j + e;
+            slope[C::kForm ? nq : 0][e] = h < rows ? p.form.slopes[first_head(meta[stage].hc) + h] * 1.44269504f : 0.f;
           }
       }
 #pragma unroll
@@ -745,9 +782,24 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
             const float e0 = v0.x, e1 = v1.x;
             un[kt][0] = v0.y;
             un[kt][1] = v1.y;
-            x[0] = x[0] * c0 + e0; x[1] = x[1] * c1 + e0; x[2] = x[2] * c0 + e1; x[3] = x[3] * c1 + e1;
+            if (C::kForm) {
+              const float s0 = slope[C::kForm ? nq : 0][0], s1 = slope[C::kForm ? nq : 0][1];
+              x[0] = form(x[0] * c0, s0, back - (kt * 16 + k0)) + e0;
+              x[1] = form(x[1] * c1, s1, back - (kt * 16 + k0)) + e0;
+              x[2] = form(x[2] * c0, s0, back - (kt * 16 + k8)) + e1;
+              x[3] = form(x[3] * c1, s1, back - (kt * 16 + k8)) + e1;
+            } else {
+              x[0] = x[0] * c0 + e0; x[1] = x[1] * c1 + e0; x[2] = x[2] * c0 + e1; x[3] = x[3] * c1 + e1;
+            }
           } else {
             x[0] *= c0; x[1] *= c1; x[2] *= c0; x[3] *= c1;
+            if (C::kForm) {
+              const float s0 = slope[C::kForm ? nq : 0][0], s1 = slope[C::kForm ? nq : 0][1];
+              x[0] = form(x[0], s0, back - (kt * 16 + k0));
+              x[1] = form(x[1], s1, back - (kt * 16 + k0));
+              x[2] = form(x[2], s0, back - (kt * 16 + k8));
+              x[3] = form(x[3], s1, back - (kt * 16 + k8));
+            }
           }
           if (mask != (kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
             if (!((mask >> (kt * 16 + k0)) & 1u)) x[0] = x[1] = -INFINITY;
@@ -901,15 +953,18 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
       auto slot_of = [&](int cta) { return p.part + (int64_t)(2 * cta + (cta == c_first ? 1 : 0)) * kSlot; };
       auto emit = [&](int q, int d, const float (&x)[4], float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (C::kForm && p.prior_lse != nullptr) {
+          const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+          emit_joined(p, me.seq, h0 + q, d, y, log2_of_sum(m, l));
+          return;
+        }
         uint2 w;
         w.x = pack_bf16(x[0] * inv, x[1] * inv);
         w.y = pack_bf16(x[2] * inv, x[3] * inv);
         *reinterpret_cast<uint2*>(p.out + (int64_t)me.seq * p.out_ts + (int64_t)(h0 + q) * p.out_hs + d) = w;
         if (d == 0 && p.lse != nullptr) {
-          // m + log2(l) with l's exponent added to m first: the two may be large and of opposite sign (FP8)
-          const uint32_t b = __float_as_uint(l);
-          const float log2_sum = (m + (float)((int)(b >> 23) - 127)) + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u));
-          p.lse[(int64_t)me.seq * q_heads + h0 + q] = l == 0.f ? -INFINITY : l - l == 0.f ? 0.6931471805599453f * log2_sum : l;
+          const float sum = log2_of_sum(m, l);
+          p.lse[(int64_t)me.seq * q_heads + h0 + q] = l == 0.f ? -INFINITY : l - l == 0.f ? 0.6931471805599453f * sum : l;
         }
       };
       auto put = [&](float* part, int q, int d, const float (&x)[4], float m, float l) {
@@ -1024,6 +1079,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attention_kernel(const 
     if (clamp_len(__ldcg(p.lens + b), p.cap) > 0) continue;
     for (int e = tid; e < q_heads * (p.D / 4); e += kThreads) {
       const int h = e / (p.D / 4), d = (e % (p.D / 4)) * 4;
+      if (C::kForm && p.prior_lse != nullptr) {
+        const float none[4] = {0.f, 0.f, 0.f, 0.f};
+        emit_joined(p, b, h, d, none, -INFINITY);
+        continue;
+      }
       *reinterpret_cast<uint2*>(p.out + (int64_t)b * p.out_ts + (int64_t)h * p.out_hs + d) = make_uint2(0, 0);
       if (d == 0 && p.lse != nullptr) p.lse[(int64_t)b * q_heads + h] = -INFINITY;
     }
@@ -1051,20 +1111,20 @@ cudaError_t launch(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles,
   return launch_k(attention_kernel<C>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmemB, stream, pdl, p);
 }
 
-template <int DP, bool kFp8>
+template <int DP, bool kFp8, bool kForm>
 cudaError_t launch_nq(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
   if (plan.nq == 1)
-    return p.q.f32 ? launch<Cfg<DP, kFp8, 1, true>>(p, plan, max_tiles, stream, pdl)
-                   : launch<Cfg<DP, kFp8, 1, false>>(p, plan, max_tiles, stream, pdl);
-  return p.q.f32 ? launch<Cfg<DP, kFp8, 2, true>>(p, plan, max_tiles, stream, pdl)
-                 : launch<Cfg<DP, kFp8, 2, false>>(p, plan, max_tiles, stream, pdl);
+    return p.q.f32 ? launch<Cfg<DP, kFp8, 1, true, kForm>>(p, plan, max_tiles, stream, pdl)
+                   : launch<Cfg<DP, kFp8, 1, false, kForm>>(p, plan, max_tiles, stream, pdl);
+  return p.q.f32 ? launch<Cfg<DP, kFp8, 2, true, kForm>>(p, plan, max_tiles, stream, pdl)
+                 : launch<Cfg<DP, kFp8, 2, false, kForm>>(p, plan, max_tiles, stream, pdl);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kForm>
 cudaError_t launch_any(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
-  return p.D <= 64    ? launch_nq<64, kFp8>(p, plan, max_tiles, stream, pdl)
-         : p.D <= 128 ? launch_nq<128, kFp8>(p, plan, max_tiles, stream, pdl)
-                      : launch_nq<256, kFp8>(p, plan, max_tiles, stream, pdl);
+  return p.D <= 64    ? launch_nq<64, kFp8, kForm>(p, plan, max_tiles, stream, pdl)
+         : p.D <= 128 ? launch_nq<128, kFp8, kForm>(p, plan, max_tiles, stream, pdl)
+                      : launch_nq<256, kFp8, kForm>(p, plan, max_tiles, stream, pdl);
 }
 
 }  // namespace attn

@@ -21,7 +21,7 @@ size_t attn_workspace_bytes(int32_t G, int32_t D, bool fp8, int sms) {
 }
 
 cudaError_t launch_attention_bf16(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
-  return attn::launch_any<false>(p, plan, max_tiles, stream, pdl);
+  return attn::launch_any<false, false>(p, plan, max_tiles, stream, pdl);
 }
 
 }  // namespace engram

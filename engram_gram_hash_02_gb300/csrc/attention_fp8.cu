@@ -4,7 +4,7 @@
 namespace engram {
 
 cudaError_t launch_attention_fp8(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl) {
-  return attn::launch_any<true>(p, plan, max_tiles, stream, pdl);
+  return attn::launch_any<true, false>(p, plan, max_tiles, stream, pdl);
 }
 
 }  // namespace engram

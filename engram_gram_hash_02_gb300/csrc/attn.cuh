@@ -66,6 +66,13 @@ struct KvReadParams {
 };
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream);
 
+// The form of scores, in units of log 2: cap2 * tanh(x * cap_inv) (cap2 0: x itself), less slopes[head] log2(e) per token
+// of distance (NULL: none)
+struct ScoreForm {
+  float cap2, cap_inv;
+  const float* slopes;
+};
+
 struct AttnParams {
   HeadRows q;                  // [B, Hq, D]
   CacheRef cache;
@@ -85,6 +92,10 @@ struct AttnParams {
   uint32_t* counters;          // 3 * kMaxAttnCtas words, zero between calls
   float* part;                 // partial results, two slots per CTA
   int32_t* err;
+  // with a form (kernels of their own; see ScoreForm), or joined with the keys that were attended before
+  ScoreForm form;
+  const float* prior_o;        // fp32 [B, Hq, D], or NULL: attended values over those keys
+  const float* prior_lse;      // fp32 [B, Hq]: log2 of their exponentials' sum
 };
 constexpr int kMaxAttnCtas = 1024;
 constexpr size_t kAttnZeroBytes = ENGRAM_ATTENTION_ZERO_BYTES;
@@ -97,6 +108,53 @@ AttnPlan attn_plan(int32_t G, int32_t D, bool fp8, int sms);
 size_t attn_workspace_bytes(int32_t G, int32_t D, bool fp8, int sms);
 cudaError_t launch_attention_bf16(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl);
 cudaError_t launch_attention_fp8(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl);
+// the same with a form of scores or a prior part
+cudaError_t launch_attention_form_bf16(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl);
+cudaError_t launch_attention_form_fp8(const AttnParams& p, const AttnPlan& plan, int64_t max_tiles, cudaStream_t stream, bool pdl);
+
+// Attention of all new tokens of ragged sequences (prompt.cu), or of one token for each row of a group that shares its
+// keys (a prefix): rows [T, Hq, D], those of sequence b are [cu[b], cu[b + 1])
+struct PromptParams {
+  HeadRows q;                  // bf16
+  int64_t T;
+  const int32_t* cu;           // [B + 1]
+  CacheRef cache;
+  const int32_t* table;        // [B, width]
+  int64_t table_stride;
+  const int32_t* lens;         // [B]
+  int32_t B, Hk, G, D;
+  int32_t cap;                 // longest length the table holds
+  int32_t causal, window;
+  const int32_t *doc_starts, *prefix_ends;   // [T] or NULL
+  const int32_t* own_lens;     // [T], or NULL. Shared prefix: a row's own tokens, which its position counts behind the prefix
+  int32_t own_cap;             // and their longest length
+  float scale_log2;
+  ScoreForm form;
+  uint16_t* out;               // bf16 rows, or (NULL) the prior part of an attention over the rows' own keys:
+  int64_t out_ts, out_hs;
+  float* lse;                  // [T, Hq] or NULL
+  float *prior_o, *prior_lse;  // fp32 [T, Hq, D], [T, Hq] (see AttnParams)
+  uint8_t* workspace;
+  int32_t* err;
+};
+size_t prompt_workspace_bytes(int32_t Hk, int32_t G, int32_t D, bool fp8, int64_t T, int32_t B, int sms);
+cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream);
+
+// ---- exponentials and scores ----------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// cap tanh(x / cap) with cap and x in one unit, inv = 1 / cap. With y = x / cap: 1 - 2 / (1 + exp(2 y)), and below 1/4, where
+// that difference loses bits, y - y^3/3 + 2 y^5/15 - 17 y^7/315 (the next term is 3e-7 of it). Off by 2^-19 of itself at most:
+// 2^-22 of exp, of the reciprocal and of the difference, against a value of 0.245 and more.
+__device__ __forceinline__ float capped(float x, float cap, float inv) {
+  const float y = x * inv, t = y * y;
+  const float near = y * fmaf(t, fmaf(t, fmaf(t, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float far = fmaf(-2.f, __fdividef(1.f, 1.f + ex2(y * 2.88539008f)), 1.f);
+  return cap * (fabsf(y) < 0.25f ? near : far);
+}
 
 // ---- asynchronous copies of 16 bytes to shared memory --------------------------------------
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

@@ -145,22 +145,58 @@ struct Attn {
   int64_t max_tiles;
 };
 
-// everything but q, err and the stream
-int check_attention(const char* fn, const EngramKVCache* cache, const EngramPagedSeqs* s, int32_t q_heads, float scale,
-                    int32_t window, const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes, size_t ws_need, Attn* a) {
-  AttnParams& p = a->p;
-  int rc = check_cache(fn, cache, &p.cache);
-  if (rc) return rc;
-  ENGRAM_CHECK_ARG(s != nullptr, "%s: seqs is NULL", fn);
+int check_seqs(const char* fn, const char* name, const EngramPagedSeqs* s) {
+  ENGRAM_CHECK_ARG(s != nullptr, "%s: %s is NULL", fn, name);
   ENGRAM_CHECK_ARG(s->batch >= 0, "%s: batch must be >= 0 (got %d)", fn, s->batch);
-  ENGRAM_CHECK_ARG(q_heads >= 1 && q_heads % cache->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn,
-                   q_heads, cache->kv_heads);
   ENGRAM_CHECK_ARG(s->table_width >= 0 && s->table_stride >= s->table_width, "%s: the page table's stride (%lld) must be >= its width (%d >= 0)",
                    fn, (long long)s->table_stride, s->table_width);
   ENGRAM_CHECK_ARG((s->seq_lens != nullptr || s->batch == 0) && aligned(s->seq_lens, 4) &&
                        (s->block_table != nullptr || s->table_width == 0 || s->batch == 0) &&
                        aligned(s->block_table, 4),
                    "%s: block_table and seq_lens must be non-NULL, aligned int32 arrays", fn);
+  return ENGRAM_OK;
+}
+
+int32_t capacity(const EngramPagedSeqs* s, const EngramKVCache* c) {
+  const int64_t cap = (int64_t)s->table_width * c->page_size;
+  return (int32_t)(cap < 0x7FFFFF00 ? cap : 0x7FFFFF00);
+}
+
+int check_workspace(const char* fn, const void* workspace, size_t ws_bytes, size_t ws_need) {
+  ENGRAM_CHECK_ARG(workspace != nullptr && aligned(workspace, 256), "%s: workspace must be non-NULL and 256-byte aligned", fn);
+  ENGRAM_CHECK_ARG(ws_bytes >= ws_need, "%s: workspace holds %zu bytes, needs %zu", fn, ws_bytes, ws_need);
+  return ENGRAM_OK;
+}
+
+constexpr double kLog2e = 1.4426950408889634;
+
+// `to` stays zero (no form) without one; returns whether there is one in `*any`
+int check_scores(const char* fn, const EngramScores* scores, ScoreForm* to, bool* any) {
+  *any = false;
+  *to = ScoreForm{};
+  if (scores == nullptr) return ENGRAM_OK;
+  const float cap = scores->cap;
+  ENGRAM_CHECK_ARG(cap == 0.f || (cap >= 0x1p-60f && cap <= 0x1p60f), "%s: cap must be 0 or in [2^-60, 2^60] (got %g)", fn, (double)cap);
+  ENGRAM_CHECK_ARG(aligned(scores->slopes, 4), "%s: slopes must be 4-byte aligned", fn);
+  if (cap > 0.f) {
+    to->cap2 = (float)(cap * kLog2e);
+    to->cap_inv = (float)(1.0 / (cap * kLog2e));
+  }
+  to->slopes = scores->slopes;
+  *any = cap > 0.f || scores->slopes != nullptr;
+  return ENGRAM_OK;
+}
+
+// everything but q, err and the stream
+int check_attention(const char* fn, const EngramKVCache* cache, const EngramPagedSeqs* s, int32_t q_heads, float scale,
+                    int32_t window, const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes, size_t ws_need, Attn* a) {
+  AttnParams& p = a->p;
+  int rc = check_cache(fn, cache, &p.cache);
+  if (rc) return rc;
+  rc = check_seqs(fn, "seqs", s);
+  if (rc) return rc;
+  ENGRAM_CHECK_ARG(q_heads >= 1 && q_heads % cache->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn,
+                   q_heads, cache->kv_heads);
   ENGRAM_CHECK_ARG(isfinite(scale), "%s: scale must be finite", fn);
   ENGRAM_CHECK_ARG(window >= 0, "%s: window must be >= 0 (got %d)", fn, window);
   HeadRows o;
@@ -168,8 +204,8 @@ int check_attention(const char* fn, const EngramKVCache* cache, const EngramPage
   if (rc) return rc;
   ENGRAM_CHECK_ARG(!o.f32 && o.heads == q_heads, "%s: out must be bf16 with %d heads", fn, q_heads);
   ENGRAM_CHECK_ARG(aligned(lse, 4), "%s: lse must be 4-byte aligned", fn);
-  ENGRAM_CHECK_ARG(workspace != nullptr && aligned(workspace, 256), "%s: workspace must be non-NULL and 256-byte aligned", fn);
-  ENGRAM_CHECK_ARG(ws_bytes >= ws_need, "%s: workspace holds %zu bytes, needs %zu", fn, ws_bytes, ws_need);
+  rc = check_workspace(fn, workspace, ws_bytes, ws_need);
+  if (rc) return rc;
 
   p.table = s->block_table;
   p.table_stride = s->table_stride;
@@ -178,10 +214,9 @@ int check_attention(const char* fn, const EngramKVCache* cache, const EngramPage
   p.Hk = cache->kv_heads;
   p.G = q_heads / cache->kv_heads;
   p.D = cache->head_dim;
-  const int64_t cap = (int64_t)s->table_width * cache->page_size;
-  p.cap = (int32_t)(cap < 0x7FFFFF00 ? cap : 0x7FFFFF00);
+  p.cap = capacity(s, cache);
   p.window = window;
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.scale_log2 = (float)((double)scale * kLog2e);
   p.out = static_cast<uint16_t*>(o.data);
   p.out_ts = o.ts;
   p.out_hs = o.hs;
@@ -199,14 +234,128 @@ int check_attention(const char* fn, const EngramKVCache* cache, const EngramPage
 }
 
 int run_attention(const char* fn, const Attn& a, cudaStream_t stream, bool pdl) {
-  const cudaError_t e = a.p.cache.fp8 ? launch_attention_fp8(a.p, a.plan, a.max_tiles, stream, pdl)
-                                      : launch_attention_bf16(a.p, a.plan, a.max_tiles, stream, pdl);
+  // kernels of their own, so that those without keep their registers
+  const bool form = a.p.form.cap2 > 0.f || a.p.form.slopes != nullptr || a.p.prior_lse != nullptr;
+  const auto launch = a.p.cache.fp8 ? (form ? launch_attention_form_fp8 : launch_attention_fp8)
+                                    : (form ? launch_attention_form_bf16 : launch_attention_bf16);
+  const cudaError_t e = launch(a.p, a.plan, a.max_tiles, stream, pdl);
   return e == cudaSuccess ? ENGRAM_OK : fail_cuda(e, fn);
+}
+
+// what prompts and shared prefixes have in common, but for the outputs; q is checked
+int check_prompt(const char* fn, const EngramKVCache* c, const EngramPagedSeqs* s, const char* starts, const int32_t* cu, int64_t T,
+                 float scale, const EngramScores* scores, PromptParams* p) {
+  ENGRAM_CHECK_ARG(!p->q.f32, "%s: q must be bf16", fn);
+  ENGRAM_CHECK_ARG(p->q.heads % c->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn, p->q.heads, c->kv_heads);
+  const int32_t G = p->q.heads / c->kv_heads;
+  ENGRAM_CHECK_ARG(T * G < (int64_t)1 << 31, "%s: T * q_heads / kv_heads must be below 2^31", fn);
+  ENGRAM_CHECK_ARG((cu != nullptr || s->batch == 0) && aligned(cu, 4), "%s: %s must be a non-NULL, aligned int32 array", fn, starts);
+  ENGRAM_CHECK_ARG(isfinite(scale), "%s: scale must be finite", fn);
+  bool any;
+  const int rc = check_scores(fn, scores, &p->form, &any);
+  if (rc) return rc;
+  p->T = T;
+  p->cu = cu;
+  p->table = s->block_table;
+  p->table_stride = s->table_stride;
+  p->lens = s->seq_lens;
+  p->B = s->batch;
+  p->Hk = c->kv_heads;
+  p->G = G;
+  p->D = c->head_dim;
+  p->cap = capacity(s, c);
+  p->scale_log2 = (float)((double)scale * kLog2e);
+  return ENGRAM_OK;
+}
+
+bool sized(const EngramKVCache* c, int32_t q_heads) {
+  return c != nullptr && c->kv_heads >= 1 && q_heads >= 1 && q_heads % c->kv_heads == 0 && c->head_dim >= 1 && c->head_dim <= kMaxHeadDim;
+}
+
+size_t prompt_bytes(const EngramKVCache* c, int32_t q_heads, int64_t T, int32_t batch) {
+  return round256(prompt_workspace_bytes(c->kv_heads, q_heads / c->kv_heads, c->head_dim, c->format == ENGRAM_CACHE_FP8_E8M0, T, batch,
+                                         num_sms()));
 }
 
 // the join's scratch, then the step's turned queries (fp32 [batch, q_heads, head_dim])
 size_t join_bytes(const EngramKVCache* c, int32_t q_heads) {
   return round256(attn_workspace_bytes(q_heads / c->kv_heads, c->head_dim, c->format == ENGRAM_CACHE_FP8_E8M0, num_sms()));
+}
+
+// a shared prefix's scratch: its own and the attention's lie in one place (they run in order), then the prefix's part,
+// fp32 [batch, q_heads, head_dim] and [batch, q_heads]
+struct SharedBytes {
+  size_t prior, all;
+};
+SharedBytes shared_bytes(const EngramKVCache* c, int32_t q_heads, int32_t batch, int32_t groups) {
+  const size_t a = prompt_bytes(c, q_heads, batch, groups), b = join_bytes(c, q_heads), prior = a > b ? a : b;
+  return {prior, prior + round256((size_t)batch * q_heads * (c->head_dim + 1) * sizeof(float))};
+}
+
+int paged_attention(const char* fn, const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q, float scale,
+                    int32_t window, const EngramScores* scores, const EngramHeads* out, float* lse, void* workspace,
+                    size_t ws_bytes, int32_t* err_flag, engram_stream_t stream) {
+  Attn a{};
+  CacheRef c;
+  int rc = check_cache(fn, cache, &c);
+  if (rc) return rc;
+  ENGRAM_CHECK_ARG(seqs != nullptr, "%s: seqs is NULL", fn);
+  rc = check_heads(fn, "q", q, seqs->batch, cache->head_dim, false, &a.p.q);
+  if (rc) return rc;
+  ENGRAM_CHECK_ARG(q->heads % cache->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn, q->heads,
+                   cache->kv_heads);
+  rc = check_attention(fn, cache, seqs, q->heads, scale, window, out, lse, workspace, ws_bytes, join_bytes(cache, q->heads), &a);
+  bool any;
+  if (!rc) rc = check_scores(fn, scores, &a.p.form, &any);
+  if (rc) return rc;
+  if (seqs->batch == 0) return ENGRAM_OK;
+  a.p.err = err_flag;
+  return run_attention(fn, a, static_cast<cudaStream_t>(stream), true);
+}
+
+int attention_step(const char* fn, const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q,
+                   const EngramHeads* k, const EngramHeads* v, const int32_t* positions, const int64_t* slots, float scale,
+                   int32_t window, const EngramScores* scores, const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes,
+                   int32_t* err_flag, engram_stream_t stream) {
+  Attn a{};
+  QkvParams p{};
+  int rc = check_cache(fn, cache, &p.cache);
+  if (rc) return rc;
+  ENGRAM_CHECK_ARG(seqs != nullptr, "%s: seqs is NULL", fn);
+  const int32_t B = seqs->batch, D = cache->head_dim;
+  rc = check_nr(fn, nr, B, D, positions, &p.nr);
+  if (!rc) rc = check_heads(fn, "q", q, B, D, false, &p.q);
+  if (!rc) rc = check_heads(fn, "k", k, B, D, false, &p.k);
+  if (!rc) rc = check_heads(fn, "v", v, B, D, false, &p.v);
+  if (!rc) rc = check_kv(fn, cache, p.k, p.v);
+  if (!rc) rc = check_slots(fn, slots, B);
+  if (rc) return rc;
+  ENGRAM_CHECK_ARG(p.q.f32 == p.k.f32, "%s: q, k and v must have one type", fn);
+  ENGRAM_CHECK_ARG(q->heads % cache->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn, q->heads,
+                   cache->kv_heads);
+  const size_t join = join_bytes(cache, q->heads);
+  rc = check_attention(fn, cache, seqs, q->heads, scale, window, out, lse, workspace, ws_bytes,
+                       engram_attention_workspace_bytes(cache, q->heads, B), &a);
+  bool any;
+  if (!rc) rc = check_scores(fn, scores, &a.p.form, &any);
+  if (rc) return rc;
+  if (B == 0) return ENGRAM_OK;
+  p.T = B;
+  p.D = D;
+  p.q_out.data = static_cast<uint8_t*>(workspace) + join;
+  p.q_out.hs = D;
+  p.q_out.ts = (int64_t)q->heads * D;
+  p.q_out.heads = q->heads;
+  p.q_out.f32 = 1;
+  p.positions = positions;
+  p.slots = slots;
+  p.err = err_flag;
+  const cudaError_t e = launch_qkv(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail_cuda(e, fn);
+  a.p.q = p.q_out;
+  a.p.lens_ready = 1;
+  a.p.err = err_flag;
+  return run_attention(fn, a, static_cast<cudaStream_t>(stream), true);
 }
 
 }  // namespace
@@ -291,72 +440,120 @@ int engram_kv_read(const EngramKVCache* cache, int64_t T, const int64_t* slots, 
 }
 
 size_t engram_attention_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int32_t batch) {
-  if (cache == nullptr || cache->kv_heads < 1 || q_heads < 1 || q_heads % cache->kv_heads != 0 || cache->head_dim < 1 ||
-      cache->head_dim > kMaxHeadDim || batch < 0)
-    return 0;
+  if (!sized(cache, q_heads) || batch < 0) return 0;
   return join_bytes(cache, q_heads) + round256((size_t)batch * q_heads * cache->head_dim * sizeof(float));
 }
 
 int engram_paged_attention(const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q, float scale,
                            int32_t window, const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes,
                            int32_t* err_flag, engram_stream_t stream) {
-  const char* fn = "engram_paged_attention";
-  Attn a{};
-  CacheRef c;
-  int rc = check_cache(fn, cache, &c);
-  if (rc) return rc;
-  ENGRAM_CHECK_ARG(seqs != nullptr, "%s: seqs is NULL", fn);
-  rc = check_heads(fn, "q", q, seqs->batch, cache->head_dim, false, &a.p.q);
-  if (rc) return rc;
-  ENGRAM_CHECK_ARG(q->heads % cache->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn, q->heads,
-                   cache->kv_heads);
-  rc = check_attention(fn, cache, seqs, q->heads, scale, window, out, lse, workspace, ws_bytes, join_bytes(cache, q->heads), &a);
-  if (rc) return rc;
-  if (seqs->batch == 0) return ENGRAM_OK;
-  a.p.err = err_flag;
-  return run_attention(fn, a, static_cast<cudaStream_t>(stream), true);
+  return paged_attention("engram_paged_attention", cache, seqs, q, scale, window, nullptr, out, lse, workspace, ws_bytes, err_flag, stream);
+}
+
+int engram_paged_attention2(const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q, float scale,
+                            int32_t window, const EngramScores* scores, const EngramHeads* out, float* lse, void* workspace,
+                            size_t ws_bytes, int32_t* err_flag, engram_stream_t stream) {
+  return paged_attention("engram_paged_attention2", cache, seqs, q, scale, window, scores, out, lse, workspace, ws_bytes, err_flag, stream);
 }
 
 int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q,
                           const EngramHeads* k, const EngramHeads* v, const int32_t* positions, const int64_t* slots, float scale,
                           int32_t window, const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes, int32_t* err_flag,
                           engram_stream_t stream) {
-  const char* fn = "engram_attention_step";
-  Attn a{};
-  QkvParams p{};
+  return attention_step("engram_attention_step", nr, cache, seqs, q, k, v, positions, slots, scale, window, nullptr, out, lse, workspace,
+                        ws_bytes, err_flag, stream);
+}
+
+int engram_attention_step2(const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q,
+                           const EngramHeads* k, const EngramHeads* v, const int32_t* positions, const int64_t* slots, float scale,
+                           int32_t window, const EngramScores* scores, const EngramHeads* out, float* lse, void* workspace,
+                           size_t ws_bytes, int32_t* err_flag, engram_stream_t stream) {
+  return attention_step("engram_attention_step2", nr, cache, seqs, q, k, v, positions, slots, scale, window, scores, out, lse, workspace,
+                        ws_bytes, err_flag, stream);
+}
+
+size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int64_t T, int32_t batch) {
+  if (!sized(cache, q_heads) || T < 0 || T >= (int64_t)1 << 31 || T * (q_heads / cache->kv_heads) >= (int64_t)1 << 31 || batch < 0) return 0;
+  return prompt_bytes(cache, q_heads, T, batch);
+}
+
+int engram_prompt_attention(const EngramKVCache* cache, const EngramPagedSeqs* seqs, int64_t T, const int32_t* cu_seqlens,
+                            const EngramHeads* q, float scale, const EngramVisible* visible, const EngramScores* scores,
+                            const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes, int32_t* err_flag,
+                            engram_stream_t stream) {
+  const char* fn = "engram_prompt_attention";
+  PromptParams p{};
   int rc = check_cache(fn, cache, &p.cache);
+  if (!rc) rc = check_seqs(fn, "seqs", seqs);
+  if (!rc) rc = check_tokens(fn, T);
+  if (!rc) rc = check_heads(fn, "q", q, T, cache->head_dim, false, &p.q);
+  if (!rc) rc = check_prompt(fn, cache, seqs, "cu_seqlens", cu_seqlens, T, scale, scores, &p);
   if (rc) return rc;
-  ENGRAM_CHECK_ARG(seqs != nullptr, "%s: seqs is NULL", fn);
-  const int32_t B = seqs->batch, D = cache->head_dim;
-  rc = check_nr(fn, nr, B, D, positions, &p.nr);
-  if (!rc) rc = check_heads(fn, "q", q, B, D, false, &p.q);
-  if (!rc) rc = check_heads(fn, "k", k, B, D, false, &p.k);
-  if (!rc) rc = check_heads(fn, "v", v, B, D, false, &p.v);
-  if (!rc) rc = check_kv(fn, cache, p.k, p.v);
-  if (!rc) rc = check_slots(fn, slots, B);
+  ENGRAM_CHECK_ARG(visible != nullptr, "%s: visible is NULL", fn);
+  ENGRAM_CHECK_ARG(visible->window >= 0, "%s: window must be >= 0 (got %d)", fn, visible->window);
+  ENGRAM_CHECK_ARG(aligned(visible->doc_starts, 4) && aligned(visible->prefix_ends, 4),
+                   "%s: doc_starts and prefix_ends must be 4-byte aligned", fn);
+  ENGRAM_CHECK_ARG(visible->prefix_ends == nullptr || visible->causal, "%s: prefix_ends are for causal attention", fn);
+  HeadRows o;
+  rc = check_heads(fn, "out", out, T, cache->head_dim, true, &o);
   if (rc) return rc;
-  ENGRAM_CHECK_ARG(p.q.f32 == p.k.f32, "%s: q, k and v must have one type", fn);
-  ENGRAM_CHECK_ARG(q->heads % cache->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn, q->heads,
-                   cache->kv_heads);
-  const size_t join = join_bytes(cache, q->heads);
-  rc = check_attention(fn, cache, seqs, q->heads, scale, window, out, lse, workspace, ws_bytes,
-                       engram_attention_workspace_bytes(cache, q->heads, B), &a);
+  ENGRAM_CHECK_ARG(!o.f32 && o.heads == q->heads, "%s: out must be bf16 with %d heads", fn, q->heads);
+  ENGRAM_CHECK_ARG(aligned(lse, 4), "%s: lse must be 4-byte aligned", fn);
+  rc = check_workspace(fn, workspace, ws_bytes, prompt_bytes(cache, q->heads, T, seqs->batch));
   if (rc) return rc;
-  if (B == 0) return ENGRAM_OK;
-  p.T = B;
-  p.D = D;
-  p.q_out.data = static_cast<uint8_t*>(workspace) + join;
-  p.q_out.hs = D;
-  p.q_out.ts = (int64_t)q->heads * D;
-  p.q_out.heads = q->heads;
-  p.q_out.f32 = 1;
-  p.positions = positions;
-  p.slots = slots;
+  if (T == 0 || seqs->batch == 0) return ENGRAM_OK;
+  p.causal = visible->causal != 0;
+  p.window = visible->window;
+  p.doc_starts = visible->doc_starts;
+  p.prefix_ends = visible->prefix_ends;
+  p.out = static_cast<uint16_t*>(o.data);
+  p.out_ts = o.ts;
+  p.out_hs = o.hs;
+  p.lse = lse;
+  p.workspace = static_cast<uint8_t*>(workspace);
   p.err = err_flag;
-  const cudaError_t e = launch_qkv(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prompt(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ENGRAM_OK : fail_cuda(e, fn);
+}
+
+size_t engram_shared_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int32_t batch, int32_t groups) {
+  if (!sized(cache, q_heads) || batch < 0 || groups < 0 || (int64_t)batch * (q_heads / cache->kv_heads) >= (int64_t)1 << 31) return 0;
+  return shared_bytes(cache, q_heads, batch, groups).all;
+}
+
+int engram_shared_attention(const EngramKVCache* cache, const EngramPagedSeqs* prefix, const int32_t* group_starts,
+                            const EngramPagedSeqs* seqs, const EngramHeads* q, float scale, const EngramScores* scores,
+                            const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes, int32_t* err_flag,
+                            engram_stream_t stream) {
+  const char* fn = "engram_shared_attention";
+  PromptParams p{};
+  Attn a{};
+  int rc = check_cache(fn, cache, &p.cache);
+  if (!rc) rc = check_seqs(fn, "prefix", prefix);
+  if (!rc) rc = check_seqs(fn, "seqs", seqs);
+  if (rc) return rc;
+  const int32_t B = seqs->batch;
+  rc = check_heads(fn, "q", q, B, cache->head_dim, false, &p.q);
+  if (!rc) rc = check_prompt(fn, cache, prefix, "group_starts", group_starts, B, scale, scores, &p);
+  if (rc) return rc;
+  const SharedBytes need = shared_bytes(cache, q->heads, B, prefix->batch);
+  rc = check_attention(fn, cache, seqs, q->heads, scale, 0, out, lse, workspace, ws_bytes, need.all, &a);
+  if (rc) return rc;
+  ENGRAM_CHECK_ARG(p.cap <= 0x7FFFFF00 - a.p.cap, "%s: a prefix and a sequence's own tokens may come to 2^31 - 256", fn);
+  if (B == 0) return ENGRAM_OK;
+  uint8_t* prior = static_cast<uint8_t*>(workspace) + need.prior;
+  p.own_lens = seqs->seq_lens;
+  p.own_cap = a.p.cap;
+  p.prior_o = reinterpret_cast<float*>(prior);
+  p.prior_lse = p.prior_o + (size_t)B * q->heads * cache->head_dim;
+  p.workspace = static_cast<uint8_t*>(workspace);
+  p.err = err_flag;
+  const cudaError_t e = launch_prompt(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, fn);
-  a.p.q = p.q_out;
-  a.p.lens_ready = 1;
+  a.p.q = p.q;
+  a.p.form = p.form;
+  a.p.prior_o = p.prior_o;
+  a.p.prior_lse = p.prior_lse;
   a.p.err = err_flag;
   return run_attention(fn, a, static_cast<cudaStream_t>(stream), true);
 }

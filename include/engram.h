@@ -616,6 +616,101 @@ int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, 
                           const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes,
                           int32_t* err_flag, engram_stream_t stream);
 
+/*
+ * ---- Scores with a form, prompts, and shared prefixes ----------------------------------------------
+ *
+ * A form of scores, for the calls that take one (NULL: none). With x_j = scale * <q_h, k_j>, query position p
+ * and key position j:
+ *     s_j = (cap > 0 ? cap * tanh(x_j / cap) : x_j) - slopes_h * |p - j|
+ *   cap     0: scores are not capped. Else in [2^-60, 2^60]; a capped score is off by 2^-19 of itself at most
+ *   slopes  device fp32 [q_heads], 4-byte aligned, or NULL: no bias
+ */
+typedef struct EngramScores {
+  float cap;
+  const float* slopes;
+} EngramScores;
+
+/* engram_paged_attention with a form of scores; a sequence's query is at position len - 1. scores NULL, or
+ * cap 0 without slopes: engram_paged_attention itself, bit for bit. */
+int engram_paged_attention2(const EngramKVCache* cache, const EngramPagedSeqs* seqs, const EngramHeads* q,
+                            float scale, int32_t window, const EngramScores* scores, const EngramHeads* out,
+                            float* lse, void* workspace, size_t ws_bytes, int32_t* err_flag,
+                            engram_stream_t stream);
+
+/* engram_attention_step with a form of scores: equal to its parts with engram_paged_attention2. */
+int engram_attention_step2(const EngramNormRope* nr, const EngramKVCache* cache, const EngramPagedSeqs* seqs,
+                           const EngramHeads* q, const EngramHeads* k, const EngramHeads* v,
+                           const int32_t* positions, const int64_t* slots, float scale, int32_t window,
+                           const EngramScores* scores, const EngramHeads* out, float* lse, void* workspace,
+                           size_t ws_bytes, int32_t* err_flag, engram_stream_t stream);
+
+/* Which keys a prompt's tokens see. Token t is new token i of a sequence with n new of len cached tokens: its
+ * position is p = len - n + i, and it sees the keys [lo, hi) of its sequence's cached tokens with
+ *     lo = max(0, p + 1 - window (window > 0), doc_starts[t])      hi = min(len, causal ? max(p + 1, prefix_ends[t]) : len)
+ * doc_starts: the first position of the document that t lies in. prefix_ends: the end of a prefix that is seen
+ * both ways (only with causal). Any values: an empty interval is a token that sees nothing. */
+typedef struct EngramVisible {
+  int32_t causal;
+  int32_t window;              /* 0: none */
+  const int32_t* doc_starts;   /* device [T], or NULL */
+  const int32_t* prefix_ends;  /* device [T], or NULL */
+} EngramVisible;
+
+/* Workspace bytes of engram_prompt_attention (on the current device) for q_heads query heads over this cache, up
+ * to T tokens of up to `batch` sequences of any lengths. 0 on bad sizes. */
+size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int64_t T, int32_t batch);
+
+/*
+ * Attention of all new tokens of ragged sequences over their cached tokens: prompts, chunks of prompts, drafted
+ * tokens. Their keys and values are in the cache already (seq_lens counts them). Query head h reads key head
+ * h / (q_heads / kv_heads); out_h = sum_j exp(s_j) v_j / sum_j exp(s_j), lse_h = log sum_j exp(s_j) over the keys
+ * that the token sees. A token that sees nothing, or whose scores are all -inf, gives zeros and lse -inf. What
+ * lies in keys and values that a token does not see has no part in its result, whatever it is.
+ *   q           bf16 rows [T, q_heads, head_dim]; q_heads a multiple of kv_heads
+ *   cu_seqlens  device int32 [batch + 1]: sequence b's new tokens are rows [cu[b], cu[b + 1]). Rows before cu[0] and
+ *               from cu[batch] on belong to no sequence and are left as they were. Values outside [0, T] are clamped
+ *               and a sequence that ends before it starts has no tokens (ENGRAM_ERR_SEQ_LEN); sequences may not share rows.
+ *               A sequence of more new tokens than its length holds (ENGRAM_ERR_SEQ_LEN) has the first ones before
+ *               position 0.
+ *   seqs        as engram_paged_attention: lengths are clamped to [0, table_width * page_size], a page outside the
+ *               cache hides its tokens. table_width * page_size counts up to 2^31 - 256 tokens
+ *   scores      NULL or a form of scores
+ *   out         bf16 rows [T, q_heads, head_dim]       lse  device fp32 [T, q_heads], or NULL
+ *   workspace   as engram_paged_attention (the same zeroed start); one may serve all the attention calls in order
+ * T * q_heads / kv_heads < 2^31. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
+ * (a code times a power of two; below 2^-133 rounded), and weights exp(s_j - m), m the running maximum as it was last
+ * moved (within 2^8 of the true one), are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32.
+ * Results do not depend on timing. Two launches, the first of one CTA, chained with programmatic dependent launch.
+ */
+int engram_prompt_attention(const EngramKVCache* cache, const EngramPagedSeqs* seqs, int64_t T,
+                            const int32_t* cu_seqlens, const EngramHeads* q, float scale, const EngramVisible* visible,
+                            const EngramScores* scores, const EngramHeads* out, float* lse, void* workspace,
+                            size_t ws_bytes, int32_t* err_flag, engram_stream_t stream);
+
+/* Workspace bytes of engram_shared_attention for q_heads query heads over this cache, up to `batch` sequences in up
+ * to `groups` groups. 0 on bad sizes. */
+size_t engram_shared_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int32_t batch, int32_t groups);
+
+/*
+ * Attention of one new token per sequence where groups of sequences share a prefix: the prefix's keys and values are
+ * read once for the whole group. Sequence b of group g attends prefix tokens [0, P) (P = prefix->seq_lens[g], at
+ * the pages of row g of prefix->block_table), then its own tokens [0, len) (seqs); its query is at position
+ * P + len - 1, prefix key j at j, own key j at P + j. With a prefix of whole pages, seqs may be a view of page
+ * tables of the whole sequences, behind the prefix's columns.
+ *   prefix        groups: batch is their number. Lengths and pages as in seqs
+ *   group_starts  device int32 [groups + 1]: group g's sequences are [starts[g], starts[g + 1]); clamped and reported
+ *                 like cu_seqlens. A sequence that is in no group has no prefix. Groups may not share sequences
+ *   q             bf16 rows [batch, q_heads, head_dim]
+ *   out, lse, scores, err_flag  as engram_paged_attention2; over all of a sequence's keys
+ *   workspace     engram_shared_workspace_bytes; its zeroed start as engram_paged_attention
+ * The prefix's part is summed as in engram_prompt_attention, the own part as in engram_paged_attention; they are
+ * joined in fp32. Three launches.
+ */
+int engram_shared_attention(const EngramKVCache* cache, const EngramPagedSeqs* prefix, const int32_t* group_starts,
+                            const EngramPagedSeqs* seqs, const EngramHeads* q, float scale, const EngramScores* scores,
+                            const EngramHeads* out, float* lse, void* workspace, size_t ws_bytes, int32_t* err_flag,
+                            engram_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -102,3 +102,57 @@ def attention(q, keys, values, scale, q_rel: float = 0.0, p_rel: float = 0.0):
         tol[h] = (2 * ds + 2.0 ** -21 + p_rel + n * 2.0 ** -24) * (w @ np.abs(v))
         tol_lse[h] = ds + 2.0 ** -21 + n * 2.0 ** -24 + 2.0 ** -22 * abs(lse[h])
     return out, lse, tol, tol_lse
+
+
+def visible(n: int, length: int, causal: bool = True, window: int = 0, doc_starts=None, prefix_ends=None):
+    """Positions and intervals [lo, hi) of the keys that n new tokens of a sequence of `length` see."""
+    p = length - n + np.arange(n, dtype=np.int64)
+    lo, hi = np.zeros(n, np.int64), np.full(n, length, np.int64)
+    if causal:
+        hi = p + 1
+        if prefix_ends is not None:
+            hi = np.maximum(hi, prefix_ends)
+        hi = np.minimum(hi, length)
+    if window:
+        lo = np.maximum(lo, p + 1 - window)
+    if doc_starts is not None:
+        lo = np.maximum(lo, doc_starts)
+    return p, lo, hi
+
+
+def attention_rows(q, keys, values, seen, p, scale, cap: float = 0.0, slopes=None, q_rel: float = 0.0, p_rel: float = 0.0):
+    """Rows q [T, Hq, D] at positions p over keys and values [n, Hk, D] at positions 0 .. n - 1; seen: bool [T, n]. Scores
+    cap * tanh(x / cap) - slope |p - j|. Returns (out, lse, a bound of out's error, a bound of lse's) as `attention` does; beside
+    its terms a capped score is off by 2^-19 of itself (tanh's slope is at most 1), a bias by 2^-22 of itself (its slope in
+    other units, the product)."""
+    q = np.asarray(q, dtype=np.float64)
+    T, Hq, D = q.shape
+    n, Hk, _ = keys.shape
+    out, lse = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf)
+    tol, tol_lse = np.zeros((T, Hq, D)), np.zeros((T, Hq))
+    some = seen.any(1) if n else np.zeros(T, bool)
+    if not some.any():
+        return out, lse, tol, tol_lse
+    far = np.abs(np.asarray(p)[:, None] - np.arange(n)[None, :]).astype(np.float64)
+    for h in range(Hq):
+        k, v = keys[:, h * Hk // Hq].astype(np.float64), values[:, h * Hk // Hq].astype(np.float64)
+        x = q[:, h] @ k.T * scale
+        ds = ((D + 8) * 2.0 ** -24 + q_rel) * abs(scale) * (np.abs(q[:, h]) @ np.abs(k).T) + 2.0 ** -22 * np.abs(x)
+        s = cap * np.tanh(x / cap) if cap else x
+        if cap:
+            ds += 2.0 ** -19 * np.abs(s)
+        if slopes is not None:
+            s = s - slopes[h] * far
+            ds += 2.0 ** -22 * (slopes[h] * far + np.abs(s))
+        s = np.where(seen, s, -np.inf)
+        m = np.where(some, s.max(1), 0.0)
+        w = np.exp(s - m[:, None])
+        total = np.where(some, w.sum(1), 1.0)
+        lse[:, h] = np.where(some, m + np.log(total), -np.inf)
+        w /= total[:, None]
+        out[:, h] = w @ v
+        # every weight by its own score's error, and all of them by their mean error in the sum
+        mean = (w * ds).sum(1)
+        tol[:, h] = (w * (ds + mean[:, None])) @ np.abs(v) * 1.01 + (2.0 ** -21 + p_rel + n * 2.0 ** -24) * (w @ np.abs(v))
+        tol_lse[:, h] = 1.01 * mean + 2.0 ** -21 + n * 2.0 ** -24 + 2.0 ** -22 * np.abs(np.where(some, lse[:, h], 0.0))
+    return out, lse, tol, tol_lse
