@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libengram.so")
 
 SOURCES = ["abi.cu", "hash.cu", "gather.cu", "gemm.cu", "gemm_mx.cu", "mx.cu", "gate.cu", "order.cu", "layout.cpp",
            "forward_noalloc.cu", "heads.cu", "attention_bf16.cu", "attention_fp8.cu", "attention_form_bf16.cu", "attention_form_fp8.cu",
-           "prompt.cu", "attn_abi.cu"]
+           "prompt.cu", "prompt_bf16.cu", "prompt_fp8.cu", "attn_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

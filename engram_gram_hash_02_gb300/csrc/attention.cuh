@@ -196,7 +196,8 @@ __device__ __forceinline__ float log2_of_sum(float m, float l) {
 __device__ __forceinline__ void emit_joined(const AttnParams& p, int seq, int head, int d, const float (&x)[4], float own) {
   const int64_t row = (int64_t)seq * (p.Hk * p.G) + head;
   const float before = __ldcg(p.prior_lse + row);
-  const float4 y = __ldcg(reinterpret_cast<const float4*>(p.prior_o + row * p.D + d));
+  // (nothing attended before: prior_o holds nothing)
+  const float4 y = before == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(reinterpret_cast<const float4*>(p.prior_o + row * p.D + d));
   const float m = fmaxf(own, before);
   const float a = ex2_rel(own, m), b = ex2_rel(before, m), sum = a + b;
   const float fa = sum == 0.f ? 0.f : a / sum, fb = sum == 0.f ? 0.f : b / sum;

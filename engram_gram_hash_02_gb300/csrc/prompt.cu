@@ -1,112 +1,209 @@
-// Attention of all new tokens of ragged sequences over the paged cache: a warp per row and head, key after key.
-#include "attn.cuh"
+// Attention of prompts: the list of its work (one CTA), the join of pairs that many CTAs share, and the launches.
+#include "prompt.cuh"
 
 namespace engram {
+namespace prompt {
 namespace {
 
-__global__ void __launch_bounds__(256) prompt_kernel(const PromptParams p) {
-  const int lane = threadIdx.x & 31;
-  const int Hq = p.Hk * p.G;
+constexpr int kPlanThreads = 1024;
+constexpr int kEntryLanes = 8;                        // of the plan for one entry: they look at its tokens in turn
+
+// inclusive sum over the block; `total` for all
+__device__ int64_t block_scan(int64_t x, int64_t* warps, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();                                    // the last call's sums are read
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll 4
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += warps[w];
+    total += warps[w];
+  }
+  return before + x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
+  __shared__ int64_t warps[kPlanThreads / 32];
+  const PromptParams& p = a.p;
+  const int R = pair_rows(p.D);
   pdl_wait();
-  if (blockIdx.x == 0 && p.err != nullptr)
-    for (int b = threadIdx.x; b < p.B; b += 256) {
-      const int s0 = __ldcg(p.cu + b), s1 = __ldcg(p.cu + b + 1), len = __ldcg(p.lens + b);
-      if (s0 < 0 || s0 > p.T || s1 > p.T || s1 < s0 || len < 0 || len > p.cap) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
+  pdl_trigger();
+  auto bounds = [&](int b, int& s0, int& n, int& len) {
+    const int c0 = __ldcg(p.cu + b), c1 = __ldcg(p.cu + b + 1), raw = __ldcg(p.lens + b);
+    s0 = (int)min((int64_t)max(c0, 0), p.T);
+    n = (int)min((int64_t)max(c1, 0), p.T) - s0;
+    len = clamp_len(raw, p.cap);
+    const bool odd = c0 < 0 || c0 > p.T || c1 > p.T || c1 < c0 || raw != len || (p.own_lens == nullptr && n > len);
+    n = max(n, 0);
+    return odd;
+  };
+  // ---- the sequences' pairs of tiles
+  int64_t run = 0, total;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t pairs = 0;
+    if (b < p.B) {
+      int s0, n, len;
+      if (bounds(b, s0, n, len) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
+      pairs = ((int64_t)n * p.G + R - 1) / R;
     }
-  const int64_t warps = (int64_t)gridDim.x * 8;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < p.T * Hq; w += warps) {
-    const int64_t t = w / Hq;
-    const int h = (int)(w % Hq), kh = h / p.G;
-    int lo_b = 0, hi_b = p.B;                          // the last sequence that starts at t or before
-    while (hi_b - lo_b > 1) {
-      const int mid = (lo_b + hi_b) / 2;
-      (__ldcg(p.cu + mid) <= t ? lo_b : hi_b) = mid;
-    }
-    const int b = lo_b;
-    const int64_t s0 = p.B > 0 ? max(__ldcg(p.cu + b), 0) : 0, s1 = p.B > 0 ? min((int64_t)__ldcg(p.cu + b + 1), p.T) : 0;
-    const bool mine = p.B > 0 && t >= s0 && t < s1;
-    if (!mine && p.out != nullptr) continue;
-    int lo = 0, hi = 0, pos = 0;
-    if (mine) {
-      int len = __ldcg(p.lens + b);
-      len = min(max(len, 0), p.cap);
-      if (p.own_lens != nullptr) {
-        pos = len + min(max(__ldcg(p.own_lens + t), 0), p.own_cap) - 1;
-        hi = len;
-      } else {
-        pos = len - (int)(s1 - t);
-        if (len < s1 - s0 && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_SEQ_LEN);
-        hi = p.causal ? min(len, max(pos + 1, p.prefix_ends != nullptr ? __ldcg(p.prefix_ends + t) : 0)) : len;
-        if (p.window > 0) lo = max(lo, pos + 1 - p.window);
-        if (p.doc_starts != nullptr) lo = max(lo, __ldcg(p.doc_starts + t));
+    const int64_t sum = block_scan(pairs, warps, total);
+    // (sequences that share rows, against the rules, may come to more pairs than there are rows for: the rest is left out)
+    if (b < p.B) a.offsets[b] = (int32_t)min(run + sum - pairs, a.max_entries);
+    run += total;
+  }
+  const int E = (int)min(run, a.max_entries);
+  __syncthreads();
+  // ---- what their rows see
+  for (int e0 = 0; e0 < E; e0 += kPlanThreads / kEntryLanes) {
+    const int e = e0 + threadIdx.x / kEntryLanes, sub = threadIdx.x % kEntryLanes;
+    Entry x{};
+    int lo = 0x7FFFFFFF, hi = 0, max_lo = 0, min_hi = 0x7FFFFFFF;
+    if (e < E) {
+      int first = 0, past = p.B;                      // the last sequence whose first pair is e or before
+      while (past - first > 1) {
+        const int mid = (first + past) / 2;
+        (a.offsets[mid] <= e ? first : past) = mid;
+      }
+      x.b = first;
+      bounds(x.b, x.s0, x.n, x.len);
+      x.row0 = (e - a.offsets[x.b]) * R;
+      x.rows = (int)min((int64_t)x.n * p.G, (int64_t)x.row0 + R);
+      const int i0 = x.row0 / p.G, i1 = (x.rows - 1) / p.G;
+      // without arrays lo and hi only grow along the tokens: the first that sees anything and the last say it all
+      const bool arrays = p.doc_starts != nullptr || p.prefix_ends != nullptr;
+      const int from = arrays ? i0 : p.own_lens == nullptr && p.causal ? max(i0, x.n - x.len) : i0;
+      for (int i = from + (arrays ? sub : sub * max(i1 - from, 1)); i <= i1; i += arrays ? kEntryLanes : max(i1 - from, 1) * kEntryLanes) {
+        int l, h, pos;
+        visible(p, x.s0, x.n, x.len, i, l, h, pos);
+        if (l < h) {
+          lo = min(lo, l);
+          hi = max(hi, h);
+          max_lo = max(max_lo, l);
+          min_hi = min(min_hi, h);
+        }
       }
     }
-    const float slope = p.form.slopes != nullptr ? p.form.slopes[h] * 1.44269504f : 0.f;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + t * p.q.ts + (int64_t)h * p.q.hs;
-    float x[8], o[8], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = lane + 32 * i < p.D ? __uint_as_float((uint32_t)q[lane + 32 * i] << 16) : 0.f;
-      o[i] = 0.f;
+    for (int o = 1; o < kEntryLanes; o <<= 1) {
+      lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+      max_lo = max(max_lo, __shfl_xor_sync(0xFFFFFFFFu, max_lo, o));
+      min_hi = min(min_hi, __shfl_xor_sync(0xFFFFFFFFu, min_hi, o));
     }
-    for (int j = lo; j < hi; ++j) {
-      const int n = (int)fast_div((uint32_t)j, p.cache.div_page), at = j - n * p.cache.page_size;
-      const int page = p.table[(int64_t)b * p.table_stride + n];
-      if (page < 0 || page >= p.cache.num_pages) {
-        if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
-        continue;
-      }
-      const int64_t row = page * p.cache.page_b + kh * p.cache.head_b + at * p.cache.tok_b;
-      const int64_t srow = page * p.cache.spage_b + kh * p.cache.shead_b + at * p.cache.stok_b;
-      auto value = [&](const uint8_t* base, const uint8_t* scales, int d) {
-        if (!p.cache.fp8) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base + row)[d] << 16);
-        uint32_t a, c;
-        e4m3x4_to_f16x2(base[row + d], a, c);
-        return __low2float(*reinterpret_cast<const __half2*>(&a)) * __uint_as_float((uint32_t)scales[srow + d / 32] << 23);
-      };
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (lane + 32 * i < p.D) s += x[i] * value(p.cache.k, p.cache.ks, lane + 32 * i);
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
-      s *= p.scale_log2;
-      if (p.form.cap2 > 0.f) s = capped(s, p.form.cap2, p.form.cap_inv);
-      s -= slope * (float)abs(pos - j);
-      const float mn = fmaxf(m, s);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - base), e = ex2(s - base);
-      m = mn;
-      l = l * f + e;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (lane + 32 * i < p.D) o[i] = o[i] * f + e * value(p.cache.v, p.cache.vs, lane + 32 * i);
+    if (e < E && sub == 0) {
+      x.lo = lo;
+      x.hi = hi;
+      x.max_lo = max_lo;
+      x.min_hi = min_hi;
+      x.units = lo < hi ? (hi - lo + kKeys - 1) / kKeys : 0;
+      a.entries[e] = x;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l, sum = l == 0.f ? -INFINITY : m + log2f(l);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = lane + 32 * i;
-      if (d >= p.D) continue;
-      if (p.out != nullptr)
-        p.out[t * p.out_ts + (int64_t)h * p.out_hs + d] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-      else
-        p.prior_o[(t * Hq + h) * p.D + d] = o[i] * inv;
-    }
-    if (lane == 0) {
-      if (p.out == nullptr) p.prior_lse[t * Hq + h] = sum;
-      else if (p.lse != nullptr) p.lse[t * Hq + h] = 0.6931471805599453f * sum;
-    }
+  }
+  __syncthreads();
+  // ---- their places, and what every CTA takes
+  run = 0;
+  for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
+    const int e = e0 + threadIdx.x;
+    const int units = e < E ? a.entries[e].units : 0;
+    const int64_t mine = units > 0 ? units + kRunCost : 0;
+    const int64_t sum = block_scan(mine, warps, total);
+    if (e < E) a.entries[e].place = run + sum - mine;
+    run += total;
+  }
+  const int64_t U = run, all = U * p.Hk, per = max((all + a.ctas - 1) / a.ctas, (int64_t)1);
+  if (threadIdx.x == 0) {
+    a.header->entries = E;
+    a.header->places = U;
+    a.header->per_cta = per;
+  }
+  __syncthreads();
+  for (int64_t k = threadIdx.x; k < (int64_t)E * p.Hk; k += kPlanThreads) {
+    const int head = (int)(k / E), e = (int)(k % E);
+    const int units = a.entries[e].units;
+    if (units == 0) continue;
+    const int64_t first = head * U + a.entries[e].place, past = first + units + kRunCost;
+    for (int64_t c = (first + per - 1) / per; c < a.ctas && c * per < past; ++c) a.starts[c] = Start{head, e};
   }
 }
 
-}  // namespace
+// rows of pairs that were cut, joined by as many warps as there are blocks of 32 rows by 16 values
+__global__ void __launch_bounds__(256) join_kernel(const Args a) {
+  const PromptParams& p = a.p;
+  const int R = pair_rows(p.D), lane = threadIdx.x & 31;
+  pdl_wait();
+  const int64_t E = a.header->entries, U = a.header->places, per = a.header->per_cta;
+  const int blocks = (R / 32) * (p.D / 16);
+  const int64_t warps = (int64_t)gridDim.x * 8, all = E * p.Hk * blocks;
+  for (int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); k < all; k += warps) {
+    const int64_t item = k / blocks;
+    const int block = (int)(k % blocks), head = (int)(item / E);
+    const Entry& x = a.entries[item % E];
+    if (x.units == 0) continue;
+    const int64_t run0 = head * U + x.place + kRunCost;
+    const int first = (int)(run0 / per), last = (int)((run0 + x.units - 1) / per);
+    if (first == last) continue;
+    const int r_in = (block % (R / 32)) * 32 + lane, r = x.row0 + r_in;
+    if (r >= x.rows) continue;
+    const int i = (int)fast_div((uint32_t)r, a.div_g);
+    join16(a, first, last, R, r_in, (int64_t)x.s0 + i, head * p.G + r - i * p.G, (block / (R / 32)) * 16);
+  }
+}
 
-size_t prompt_workspace_bytes(int32_t Hk, int32_t G, int32_t D, bool fp8, int64_t T, int32_t B, int sms) { return kAttnZeroBytes; }
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+Layout layout_of(int32_t G, int32_t D, int64_t T, int32_t B, int ctas) {
+  Layout l;
+  const int R = pair_rows(D);
+  l.max_entries = (T * G + R - 1) / R + B;
+  l.slot_floats = R * (D + 2);
+  l.header = kAttnZeroBytes;
+  l.starts = l.header + 256;
+  l.offsets = l.starts + round256((size_t)ctas * sizeof(Start));
+  l.entries = l.offsets + round256(((size_t)B + 1) * sizeof(int32_t));
+  l.parts = l.entries + round256((size_t)l.max_entries * sizeof(Entry));
+  l.all = l.parts + (size_t)2 * ctas * l.slot_floats * sizeof(float);
+  return l;
+}
+int ctas_of(int sms) { return sms < (int)(kAttnZeroBytes / 32) ? sms : (int)(kAttnZeroBytes / 32); }   // eight counters each
+
+}  // namespace
+}  // namespace prompt
+
+size_t prompt_workspace_bytes(int32_t Hk, int32_t G, int32_t D, bool fp8, int64_t T, int32_t B, int sms) {
+  return prompt::layout_of(G, D, T, B, prompt::ctas_of(sms)).all;
+}
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
-  const int64_t blocks = (p.T * p.Hk * p.G + 7) / 8;
-  const int64_t most = (int64_t)num_sms() * 8;
-  return launch_k(prompt_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, stream, true, p);
+  using namespace prompt;
+  Args a{};
+  a.p = p;
+  a.ctas = ctas_of(num_sms());
+  const Layout l = layout_of(p.G, p.D, p.T, p.B, a.ctas);
+  a.header = reinterpret_cast<Header*>(p.workspace + l.header);
+  a.starts = reinterpret_cast<Start*>(p.workspace + l.starts);
+  a.offsets = reinterpret_cast<int32_t*>(p.workspace + l.offsets);
+  a.entries = reinterpret_cast<Entry*>(p.workspace + l.entries);
+  a.counters = reinterpret_cast<uint32_t*>(p.workspace);
+  a.parts = reinterpret_cast<float*>(p.workspace + l.parts);
+  a.slot_floats = l.slot_floats;
+  a.max_entries = l.max_entries;
+  a.div_g = make_fastdiv((uint32_t)p.G);
+  // Few pairs have many parts each: a kernel behind this one joins them on all SMs. With a pair per CTA and more a pair is
+  // cut once or twice, and the last to arrive joins it.
+  const int R = pair_rows(p.D);
+  a.join = (p.T * p.G + R - 1) / R * p.Hk >= a.ctas;
+  cudaError_t e = launch_k(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
+  if (e == cudaSuccess) e = p.cache.fp8 ? launch_fp8(a, stream) : launch_bf16(a, stream);
+  if (e == cudaSuccess && !a.join) e = launch_k(join_kernel, dim3((unsigned)a.ctas * 2), dim3(256), 0, stream, true, a);
+  return e;
 }
 
 }  // namespace engram

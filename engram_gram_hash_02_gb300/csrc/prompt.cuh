@@ -1,0 +1,1033 @@
+// Attention of all new tokens of ragged sequences over a paged cache, on the tensor cores (tcgen05).
+//
+// For a token's query head h and the keys [lo, hi) that it sees:
+//   s_j = form(scale q_h . k_j),   o_h = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse_h = log sum_j exp(s_j)
+// with a running maximum m (units of log 2, every exponential one ex2). Rows are tokens times the G query heads of a key
+// head, so that a key row is used by all of them; 128 rows make a tile (the MMA's M), two tiles share every key and value
+// tile that is brought in (heads of up to 128; one tile for wider heads, whose sums fill tensor memory).
+//
+// One CTA per SM, 16 warps with roles of their own, joined by mbarriers only:
+//   warps 0..3, 4..7   softmax of tile 0 and 1: a thread has a row. S (fp32) comes from tensor memory, P goes back there
+//                      as bf16, in S's place; o is multiplied there only when the maximum grows by more than 2^8
+//   warp 8             issues the MMAs:  S = Q K^T (both from shared memory),  O += P V (P from tensor memory, V as it
+//                      lies, by rows of keys: an MN-major operand)
+//   warp 9             walks the CTA's share of the work and hands segments (a run of key tiles of one pair of tiles) out
+//   warps 12..15       bring rows in: Q, then K and V tiles in the order in which they are used, into a ring of 32 KB
+//                      slots. A row is where its page says: 16-byte copies (cp.async) at any page size and stride; FP8
+//                      rows are converted to bf16 on the way (exact)
+// While the softmax of one tile runs, the tensor cores work on the other; with one tile, on the next key tile.
+//
+// Work is cut at key tiles: a first kernel (one CTA) lists the pairs of tiles with the hull of their keys, and every CTA
+// takes an equal run of the list. A pair that is cut leaves (o, m, sum) per CTA; the last warp to arrive joins them, or a
+// kernel behind this one where pairs are few and their parts many (prompt.cu says when).
+//
+// Keys outside of a row's interval are masked in S. P is zero there, but 0 * inf is not: in a value tile that some row sees
+// only in part, infinities and NaN are replaced by zeros, and the softmax warps add their products to the rows that see
+// them.
+//
+// Roundings below 32 bits: P to bf16 (2^-8 of itself at most). The sums take P before that.
+#pragma once
+
+#include "attn.cuh"
+#include "tc_common.cuh"
+
+namespace engram {
+namespace prompt {
+
+constexpr int kKeys = 128;                            // of a tile
+constexpr int kSlotBytes = 32768;                     // 128 keys of up to 128 values, as two blocks of 128-byte rows
+constexpr int kBlockBytes = 16384;
+constexpr int kSlots = 5;
+constexpr int kQBytes = 65536;
+constexpr int kThreads = 512;
+constexpr int kProducers = 4;                         // warps
+constexpr int kMeta = 16;                             // key tiles whose masks are kept
+constexpr int kRunCost = 1;                           // a pair's fixed cost in key tiles, when work is divided
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;                       // S of buffer b at column 128 b, O of tile t at 256 + 128 t
+
+// one pair of tiles of a sequence, equal for all key heads
+struct Entry {
+  int32_t b, row0, rows;                              // sequence; rows [row0, rows) of its n * G, at most a pair's
+  int32_t s0, n, len;
+  int32_t lo, hi;                                     // hull of the keys that its rows see (lo = hi: none)
+  int32_t max_lo, min_hi;                             // keys from max_lo to min_hi are seen by every row that sees any
+  int32_t units, pad;                                 // key tiles
+  int64_t place;                                      // in the row of a head's work
+};
+struct Header {
+  int64_t entries, places, per_cta;                   // places per head, places per CTA
+};
+struct Start {                                        // a CTA's first entry
+  int32_t head, entry;
+};
+// workspace behind the zeroed counters
+struct Layout {
+  size_t header, starts, offsets, entries, parts, all;
+  int64_t max_entries;
+  int32_t slot_floats;
+};
+__host__ __device__ constexpr int pair_rows(int D) { return D > 128 ? 128 : 256; }
+
+struct Args {
+  PromptParams p;
+  Header* header;
+  Start* starts;
+  int32_t* offsets;                                   // [B + 1] first entries of the sequences
+  Entry* entries;
+  uint32_t* counters;                                 // [CTA][8 warps], zero between calls
+  float* parts;
+  int64_t max_entries;
+  int32_t slot_floats;
+  int32_t join;                                       // 1: the last warp to arrive joins a cut pair's rows
+  int32_t ctas;
+  FastDiv div_g;
+};
+
+struct Row {                                          // what a row is and sees
+  int64_t token;
+  int32_t head, lo, hi, pos;                          // head among its key head's
+};
+__device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : len > cap ? cap : len; }
+
+// token i (row0 .. of sequence rows) of an entry's sequence
+__device__ __forceinline__ void visible(const PromptParams& p, int s0, int n, int len, int i, int& lo, int& hi, int& pos) {
+  const int64_t t = (int64_t)s0 + i;
+  lo = 0;
+  if (p.own_lens != nullptr) {
+    pos = len + clamp_len(__ldcg(p.own_lens + t), p.own_cap) - 1;
+    hi = len;
+    return;
+  }
+  pos = len - n + i;
+  hi = len;
+  if (p.causal) hi = min(len, max(pos + 1, p.prefix_ends != nullptr ? __ldcg(p.prefix_ends + t) : 0));
+  if (p.window > 0 && pos + 1 > p.window) lo = pos + 1 - p.window;
+  if (p.doc_starts != nullptr) lo = max(lo, __ldcg(p.doc_starts + t));
+}
+
+// ---- parts of cut pairs: o [D / 4][rows of a pair] of 4 floats, then (m, sum) [rows] ------------------------------
+__device__ __forceinline__ float4* part_o(float* slot, int R, int d4, int r) { return reinterpret_cast<float4*>(slot) + (int64_t)d4 * R + r; }
+__device__ __forceinline__ float2* part_ml(float* slot, int R, int D, int r) {
+  return reinterpret_cast<float2*>(reinterpret_cast<float4*>(slot) + (int64_t)(D / 4) * R) + r;
+}
+__device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
+
+// 16 values of a row from value d on, and (with d 0) its log-sum-exp
+__device__ __forceinline__ void emit16(const PromptParams& p, int64_t token, int h, int d, const float (&o)[16], float m, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t row = token * (p.Hk * p.G) + h;
+  if (p.out != nullptr) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+    uint4* dst = reinterpret_cast<uint4*>(p.out + token * p.out_ts + (int64_t)h * p.out_hs + d);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(p.prior_o + row * p.D + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+  }
+  if (d == 0) {
+    const float sum = l == 0.f ? -INFINITY : m + log2f(l);
+    if (p.out == nullptr)
+      p.prior_lse[row] = sum;
+    else if (p.lse != nullptr)
+      p.lse[row] = 0.6931471805599453f * sum;
+  }
+}
+
+// joins 16 values of a pair's row r from the parts of CTAs first .. last, in the order of their keys
+__device__ __forceinline__ void join16(const Args& a, int first, int last, int R, int r, int64_t token, int h, int d) {
+  auto slot = [&](int c) { return a.parts + (int64_t)(2 * c + (c == first ? 1 : 0)) * a.slot_floats; };
+  float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+  constexpr int kBatch = 4;
+  for (int c0 = first; c0 <= last; c0 += kBatch) {
+    float2 ml[kBatch];
+    float4 y[kBatch][4];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c0 + k <= last) {
+        float* s = slot(c0 + k);
+        ml[k] = __ldcg(part_ml(s, R, a.p.D, r));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[k][i] = __ldcg(part_o(s, R, d / 4 + i, r));
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+    const float f0 = ex2_rel(m, mn);
+    m = mn;
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= f0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = ex2_rel(ml[k].x, mn);
+      l += ml[k].y * f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[4 * i] += y[k][i].x * f;
+        o[4 * i + 1] += y[k][i].y * f;
+        o[4 * i + 2] += y[k][i].z * f;
+        o[4 * i + 3] += y[k][i].w * f;
+      }
+    }
+  }
+  emit16(a.p, token, h, d, o, m, l);
+}
+
+// ---- tensor memory -------------------------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
+        "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]),
+        "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]),
+        "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return r;
+}
+// nothing moves what uses x before the wait that this stands behind
+template <int N>
+__device__ __forceinline__ void hold(float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// S = Q K^T: both operands K-major from shared memory (tc_mma). O += P V: A from tensor memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// V as it lies: rows of keys (the products' K), 64 values to a 128-byte row (N), 128B swizzle; the next 8 keys are 1024
+// bytes on (stride offset), the next 64 values a block of 128 rows (leading offset)
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kBlockBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// bf16 operands, fp32 sums, M = 128
+__device__ __forceinline__ uint32_t idesc_of(int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+// mbar_wait without a call: a function call's registers do not go together with setmaxnreg
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      if (*abort_flag) return false;
+      if ((uint64_t)clock64() - t0 > kWaitLimitCycles) {
+        *abort_flag = 1;
+        if (err != nullptr) atomicOr(err, ENGRAM_ERR_PIPE_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// ---- shared memory behind the ring -----------------------------------------------------------------------------
+struct Segment {
+  int32_t tiles;                                      // key tiles (0: no more work)
+  int32_t nt;                                         // tiles of rows: 1 or 2
+  int32_t b, head;
+  int32_t row0, rows, s0, n, len;
+  int32_t key0;                                       // first key of the segment
+  int32_t hull_lo, hull_hi, max_lo, min_hi;
+  int32_t whole;                                      // all of its pair's keys
+  int32_t c_first, c_last;                            // CTAs of a cut pair
+};
+struct Ctl {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t k_meta[kMeta], v_meta[kMeta];
+  uint64_t s_full[2], p_full[2], o_final[2], o_done;
+  uint64_t seg_full[2], seg_empty[2];
+  uint64_t drained;
+  Segment seg[2];
+  uint32_t live[kMeta][4];                            // which keys of a tile are there
+  uint32_t v_bad[kMeta][kProducers];                  // keys whose values are not all finite (in tiles that some row sees partly)
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + (int)sizeof(Ctl);
+static_assert(kSmemBytes <= kSmemBudget, "one CTA's shared memory");
+constexpr int kSegReaders = 8 + 1 + kProducers;
+
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+// 16-byte piece c of row r in blocks of 128-byte rows, 128B swizzle
+__device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)((c >> 3) * kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
+
+// kWide: heads of more than 128 values (one tile of rows, two slots per key or value tile). kForm: scores with a form, or a
+// scale that is not positive
+template <bool kWide, bool kFp8, bool kForm>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
+  const PromptParams& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t q_smem = (raw + 1023u) & ~1023u;
+  const uint32_t ring = q_smem + kQBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (ring + kSlots * kSlotBytes - raw));
+  volatile int32_t* abort_flag = &ctl->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = p.D, G = p.G;
+  constexpr int kSlotsPerTile = kWide ? 2 : 1;
+  constexpr int kPair = kWide ? 128 : 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), kProducers);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl->q_full), kProducers);
+    mbar_init(smem_u32(&ctl->q_empty), 1);
+    for (int i = 0; i < kMeta; ++i) {
+      mbar_init(smem_u32(&ctl->k_meta[i]), kProducers);
+      mbar_init(smem_u32(&ctl->v_meta[i]), kProducers);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->s_full[i]), 1);
+      mbar_init(smem_u32(&ctl->p_full[i]), 4);
+      mbar_init(smem_u32(&ctl->o_final[i]), 1);
+      mbar_init(smem_u32(&ctl->seg_full[i]), 1);
+      mbar_init(smem_u32(&ctl->seg_empty[i]), kSegReaders);
+    }
+    mbar_init(smem_u32(&ctl->o_done), 1);
+    ctl->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)), "n"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  pdl_wait();
+
+  auto wait = [&](uint64_t& bar, uint32_t parity) { return wait_inline(smem_u32(&bar), parity & 1u, abort_flag, p.err); };
+  // the same for a whole warp, with one answer for all of it
+  auto wait_warp = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+  // whether some row that sees keys at all does not see all of the tile's, and whether values there were not finite
+  auto partly_seen = [&](const Segment& s, int n) {
+    const int first = s.key0 + n * kKeys;
+    return max(first, s.hull_lo) < s.max_lo || min(first + kKeys, s.hull_hi) > s.min_hi;
+  };
+  auto not_finite = [&](uint32_t kn) {
+    const volatile uint32_t* f = ctl->v_bad[kn % kMeta];
+    return (f[0] | f[1] | f[2] | f[3]) != 0;
+  };
+  auto arrive = [&](uint64_t& bar) { mbar_arrive(smem_u32(&bar)); };
+  uint32_t seg_n = 0;                                 // segments read so far
+  auto next_segment = [&](bool whole_warp) {
+    uint64_t& bar = ctl->seg_full[seg_n & 1];
+    if (!(whole_warp ? wait_warp(bar, seg_n >> 1) : wait(bar, seg_n >> 1))) return false;
+    return ctl->seg[seg_n & 1].tiles > 0;
+  };
+  auto done_segment = [&] {                           // one lane of each reader
+    arrive(ctl->seg_empty[seg_n & 1]);
+    ++seg_n;
+  };
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    more_registers<184>();
+    const int tile = warp >> 2, wl = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
+    const uint32_t o_t = lanes + kOCol + (uint32_t)(tile * 128);
+    uint32_t used[2] = {0, 0};                        // tiles that went through the S buffers
+    uint32_t finals = 0, dones = 0, keys_n = 0;       // o_final and o_done phases; key tiles
+    bool ok = true;
+    while (ok && next_segment(true)) {
+      const Segment& s = ctl->seg[seg_n & 1];         // read where it lies: registers are for the scores
+      const bool mine = tile < s.nt;
+      if (mine) {
+        const int r_in = tile * 128 + wl * 32 + lane;             // row of the pair
+        const int r = s.row0 + r_in;
+        const bool valid = r < s.rows;
+        int lo = 0, hi = 0x7FFFFFFF, pos = 0, g = 0;
+        if (valid) {
+          const int i = (int)fast_div((uint32_t)r, a.div_g);
+          g = r - i * G;
+          visible(p, s.s0, s.n, s.len, i, lo, hi, pos);
+        }
+        const float slope = kForm && p.form.slopes != nullptr && valid ? p.form.slopes[s.head * G + g] * 1.44269504f : 0.f;
+        float m = -INFINITY, l = 0.f;
+        for (int n = 0; n < s.tiles; ++n) {
+          const int buf = s.nt == 2 ? tile : n & 1;
+          const uint32_t nth = used[buf] + (s.nt == 2 ? n : n >> 1);
+          const uint32_t s_t = lanes + (uint32_t)(buf * 128);
+          const uint32_t kn = keys_n + n;
+          const int key0 = s.key0 + n * kKeys;
+          if (!wait_warp(ctl->k_meta[kn % kMeta], kn / kMeta) || !wait_warp(ctl->s_full[buf], nth)) { ok = false; break; }
+          tc_fence_after();
+          float x[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, x + 32 * c);
+          uint32_t mask[4];
+          uint32_t all = 0xFFFFFFFFu;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            mask[w] = *(volatile uint32_t*)&ctl->live[kn % kMeta][w] & bits_below(hi - key0 - 32 * w) & ~bits_below(lo - key0 - 32 * w);
+            all &= mask[w];
+          }
+          const bool full = __all_sync(0xFFFFFFFFu, all == 0xFFFFFFFFu);
+          tmem_ld_wait();
+          hold(x);
+          if (kForm) {
+            const float back = (float)(pos - key0);
+#pragma unroll
+            for (int j = 0; j < 128; ++j) {
+              float y = x[j] * p.scale_log2;
+              if (p.form.cap2 > 0.f) y = capped(y, p.form.cap2, p.form.cap_inv);
+              x[j] = fmaf(-slope, fabsf(back - (float)j), y);
+            }
+          }
+          if (!full) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (!((mask[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (!kForm) top *= p.scale_log2;
+          // o stays in units of 2^m until the maximum has grown by 8: weights up to 2^8, and hardly ever a pass over o
+          const bool grown = top > m + 8.f;
+          if (__any_sync(0xFFFFFFFFu, grown)) {
+            const float to = grown ? top : m;
+            const float alpha = grown ? ex2(m - to) : 1.f;
+            m = to;
+            l *= alpha;
+            if (n > 0) {
+              if (s.nt == 1 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
+              tc_fence_after();
+              for (int d = 0; d < D; d += 16) {
+                float y[16];
+                tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+                tmem_ld_wait();
+                hold(y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] *= alpha;
+                tmem_st16(o_t + d, reinterpret_cast<const uint32_t*>(y));
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float x0 = x[32 * c + 2 * j], x1 = x[32 * c + 2 * j + 1];
+              const float p0 = ex2(kForm ? x0 - base : fmaf(x0, p.scale_log2, -base));
+              const float p1 = ex2(kForm ? x1 - base : fmaf(x1, p.scale_log2, -base));
+              sum[j & 1] += p0;
+              sum[2 + (j & 1)] += p1;
+              w[j] = pack_bf16(p0, p1);
+            }
+            tmem_st16(s_t + 16 * c, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          if (partly_seen(s, n)) {
+            // some row does not see all of the tile's keys: values that are not finite must not reach it
+            if (!wait_warp(ctl->v_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
+            if (not_finite(kn)) {
+              if (s.nt == 1 && n > 0 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
+              tc_fence_after();
+              for (int d = 0; d < D; d += 16) {
+                float y[16];
+                if (n > 0) {
+                  tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+                  tmem_ld_wait();
+                  hold(y);
+                } else {                              // (the products of a first tile are then added, too)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) y[e] = 0.f;
+                }
+                for (int w = 0; w < 4; ++w) {
+                  const uint32_t sees = w == 0 ? mask[0] : w == 1 ? mask[1] : w == 2 ? mask[2] : mask[3];
+                  for (uint32_t left = *(volatile uint32_t*)&ctl->v_bad[kn % kMeta][w]; left != 0; left &= left - 1) {
+                    const int j = 32 * w + __ffs(left) - 1;
+                    uint32_t pw = tmem_ld1(s_t + (j >> 1));
+                    tmem_ld_wait();
+                    asm volatile("" : "+r"(pw));
+                    const float pj = (j & 1) ? engram::bf16_hi(pw) : engram::bf16_lo(pw);
+                    const int at = (int)fast_div((uint32_t)(key0 + j), p.cache.div_page), place = key0 + j - at * p.cache.page_size;
+                    const int64_t page = p.table[(int64_t)s.b * p.table_stride + at];
+                    const uint8_t* row = p.cache.v + page * p.cache.page_b + s.head * p.cache.head_b + place * p.cache.tok_b;
+                    const uint8_t* scales = p.cache.vs + page * p.cache.spage_b + s.head * p.cache.shead_b + place * p.cache.stok_b;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                      float v;
+                      if (kFp8) {
+                        uint32_t f0, f1;
+                        e4m3x4_to_f16x2(row[d + e], f0, f1);
+                        v = __low2float(*reinterpret_cast<const __half2*>(&f0)) * __uint_as_float((uint32_t)scales[(d + e) / 32] << 23);
+                      } else {
+                        v = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[d + e] << 16);
+                      }
+                      if (((sees >> (j & 31)) & 1u) && !(fabsf(v) <= 3.3895314e38f)) y[e] = fmaf(pj, v, y[e]);
+                    }
+                  }
+                }
+                tmem_st16(o_t + d, reinterpret_cast<const uint32_t*>(y));
+              }
+              tmem_st_wait();
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(ctl->p_full[buf]);
+        }
+        if (!ok) break;
+        // ---- the segment's result
+        if (!wait_warp(ctl->o_final[tile], finals)) { ok = false; break; }
+        tc_fence_after();
+        const int64_t token = (int64_t)s.s0 + (valid ? (int)fast_div((uint32_t)r, a.div_g) : 0);
+        const int h = s.head * G + g;
+        if (s.whole) {
+          for (int d = 0; d < D; d += 16) {
+            float y[16];
+            tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+            tmem_ld_wait();
+            hold(y);
+            if (valid) emit16(p, token, h, d, y, m, l);
+          }
+        } else {
+          float* slot = a.parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == s.c_first ? 1 : 0)) * a.slot_floats;
+          for (int d = 0; d < D; d += 16) {
+            float y[16];
+            tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+            tmem_ld_wait();
+            hold(y);
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) __stcg(part_o(slot, kPair, d / 4 + e, r_in), make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+            }
+          }
+          if (valid) __stcg(part_ml(slot, kPair, D, r_in), make_float2(m, l));
+          if (a.join) {
+            __syncwarp();
+            uint32_t last = 0;
+            if (lane == 0) {
+              uint32_t* counter = a.counters + s.c_first * 8 + warp;
+              __threadfence();
+              asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(last) : "l"(counter) : "memory");
+              last = last == (uint32_t)(s.c_last - s.c_first);
+              if (last) *counter = 0;                 // the next call finds it zero
+              __threadfence();
+            }
+            if (__shfl_sync(0xFFFFFFFFu, last, 0) && valid)
+              for (int d = 0; d < D; d += 16) join16(a, s.c_first, s.c_last, kPair, r_in, token, h, d);
+          }
+        }
+        tc_fence_before();
+        ++finals;
+      }
+      if (s.nt == 2) {
+        used[0] += s.tiles;
+        used[1] += s.tiles;
+      } else {
+        used[0] += (s.tiles + 1) >> 1;
+        used[1] += s.tiles >> 1;
+        dones += s.tiles;
+      }
+      keys_n += s.tiles;
+      __syncwarp();
+      if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);
+      ++seg_n;
+    }
+  } else if (warp < 12) {
+    fewer_registers<72>();
+    if (warp == 8) {
+      // -------------------------------------------------------------- MMA
+      if (lane == 0) {
+        uint32_t used[2] = {0, 0}, kn = 0, q_n = 0;
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t id_s = idesc_of(kKeys, false);
+        while (ok && next_segment(false)) {
+          const Segment s = ctl->seg[seg_n & 1];
+          const int T = s.tiles;
+          auto next_slot = [&] {
+            if (++slot == kSlots) { slot = 0; phase ^= 1u; }
+          };
+          // S(buf) (+)= Q(t) K^T over the part of the heads that lies in a slot
+          auto qk = [&](int t, int buf, int at, int part) {
+            const uint32_t q0 = q_smem + (uint32_t)(t * 2 + part * 2) * kBlockBytes, k0 = ring + (uint32_t)at * kSlotBytes;
+            const int steps = min(8, (D - part * 128 + 15) / 16);
+            for (int k = 0; k < steps; ++k) {
+              const uint32_t off = (uint32_t)((k >> 2) * kBlockBytes + (k & 3) * 32);
+              tc_mma(tmem + buf * 128, smem_desc_sw128(q0 + off), smem_desc_sw128(k0 + off), id_s, part > 0 || k > 0 ? 1u : 0u);
+            }
+          };
+          // O(t) (+)= P(buf) V for the values that lie in a slot
+          auto pv = [&](int t, int buf, int at, int part, bool add) {
+            const uint32_t v0 = ring + (uint32_t)at * kSlotBytes;
+            const uint32_t id = idesc_of(min(128, D - part * 128), true);
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              tc_mma_ts(tmem + kOCol + t * 128 + part * 128, tmem + buf * 128 + k * 8, smem_desc_mn(v0 + k * 2048), id, add || k > 0 ? 1u : 0u);
+          };
+          if (!wait(ctl->q_full, q_n)) break;
+          if (!kWide && s.nt == 2) {
+            if (!wait(ctl->full[slot], phase)) break;
+            tc_fence_after();
+            for (int t = 0; t < 2; ++t) {
+              qk(t, t, slot, 0);
+              tc_commit(smem_u32(&ctl->s_full[t]));
+            }
+            tc_commit(smem_u32(&ctl->empty[slot]));
+            if (T == 1) tc_commit(smem_u32(&ctl->q_empty));
+            next_slot();
+            for (int n = 0; n < T; ++n) {
+              const int v = slot;
+              if (!wait(ctl->full[slot], phase)) { ok = false; break; }
+              next_slot();
+              if (n + 1 < T && !wait(ctl->full[slot], phase)) { ok = false; break; }
+              const bool partly = partly_seen(s, n);
+              if (partly && !wait(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
+              const bool add = n > 0 || (partly && not_finite(kn + n));
+              for (int t = 0; t < 2; ++t) {
+                if (!wait(ctl->p_full[t], used[t] + n)) { ok = false; break; }
+                tc_fence_after();
+                pv(t, t, v, 0, add);
+                if (t == 1) tc_commit(smem_u32(&ctl->empty[v]));
+                if (n + 1 < T) {
+                  qk(t, t, slot, 0);
+                  tc_commit(smem_u32(&ctl->s_full[t]));
+                } else {
+                  tc_commit(smem_u32(&ctl->o_final[t]));
+                }
+              }
+              if (!ok) break;
+              if (n + 1 < T) {
+                tc_commit(smem_u32(&ctl->empty[slot]));
+                if (n + 2 == T) tc_commit(smem_u32(&ctl->q_empty));
+                next_slot();
+              }
+            }
+            used[0] += T;
+            used[1] += T;
+          } else {
+            auto keys = [&](int n) {                  // the scores of key tile n, into its buffer
+              for (int part = 0; part < kSlotsPerTile; ++part) {
+                if (!wait(ctl->full[slot], phase)) return false;
+                tc_fence_after();
+                qk(0, n & 1, slot, part);
+                tc_commit(smem_u32(&ctl->empty[slot]));
+                next_slot();
+              }
+              tc_commit(smem_u32(&ctl->s_full[n & 1]));
+              if (n + 1 == T) tc_commit(smem_u32(&ctl->q_empty));
+              return true;
+            };
+            ok = keys(0) && (T < 2 || keys(1));
+            for (int n = 0; ok && n < T; ++n) {
+              if (!wait(ctl->p_full[n & 1], used[n & 1] + (n >> 1))) { ok = false; break; }
+              const bool partly = partly_seen(s, n);
+              if (partly && !wait(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
+              const bool add = n > 0 || (partly && not_finite(kn + n));
+              for (int part = 0; part < kSlotsPerTile; ++part) {
+                if (!wait(ctl->full[slot], phase)) { ok = false; break; }
+                tc_fence_after();
+                pv(0, n & 1, slot, part, add);
+                tc_commit(smem_u32(&ctl->empty[slot]));
+                next_slot();
+              }
+              if (!ok) break;
+              tc_commit(smem_u32(&ctl->o_done));
+              if (n + 1 == T) tc_commit(smem_u32(&ctl->o_final[0]));
+              if (n + 2 < T) ok = keys(n + 2);
+            }
+            used[0] += (T + 1) >> 1;
+            used[1] += T >> 1;
+          }
+          if (!ok) break;
+          kn += T;
+          ++q_n;
+          done_segment();
+        }
+      }
+    } else if (warp == 9) {
+      // -------------------------------------------------------------- the CTA's share
+      const int64_t U = a.header->places, per = a.header->per_cta;
+      const int64_t total = U * p.Hk, at0 = per * blockIdx.x, at1 = min(total, at0 + per);
+      if (lane == 0) {
+        bool ok = true;
+        auto put = [&](const Segment& s) {
+          if (seg_n >= 2 && !wait(ctl->seg_empty[seg_n & 1], (seg_n >> 1) - 1)) return false;
+          ctl->seg[seg_n & 1] = s;
+          arrive(ctl->seg_full[seg_n & 1]);
+          ++seg_n;
+          return true;
+        };
+        if (at0 < at1) {
+          Start st = a.starts[blockIdx.x];
+          int64_t base = st.head * U;
+          const int E = (int)a.header->entries;
+          while (ok && st.head < p.Hk) {
+            const Entry e = a.entries[st.entry];
+            const int64_t run0 = base + e.place + kRunCost;       // its first tile's place
+            if (e.units > 0) {
+              if (base + e.place >= at1) break;
+              const int64_t from = max(run0, at0), to = min(run0 + e.units, at1);
+              if (from < to) {
+                Segment s;
+                s.tiles = (int)(to - from);
+                s.nt = !kWide && e.rows - e.row0 > 128 ? 2 : 1;
+                s.b = e.b;
+                s.head = st.head;
+                s.row0 = e.row0;
+                s.rows = e.rows;
+                s.s0 = e.s0;
+                s.n = e.n;
+                s.len = e.len;
+                s.key0 = e.lo + (int)(from - run0) * kKeys;
+                s.hull_lo = e.lo;
+                s.hull_hi = e.hi;
+                s.max_lo = e.max_lo;
+                s.min_hi = e.min_hi;
+                s.c_first = (int)(run0 / per);
+                s.c_last = (int)((run0 + e.units - 1) / per);
+                s.whole = s.c_first == s.c_last;
+                ok = put(s);
+              }
+            }
+            if (++st.entry == E) {
+              st.entry = 0;
+              ++st.head;
+              base += U;
+            }
+          }
+        }
+        Segment end;
+        end.tiles = 0;
+        if (ok) put(end);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- rows of Q, K and V
+    fewer_registers<72>();
+    const int w = warp - 12;                          // rows 32 w .. 32 w + 31 of every tile
+    int slot = 0;
+    uint32_t phase = 0, kn = 0, q_n = 0;
+    // copies that are under way: what to do once they have landed, oldest first
+    constexpr uint32_t kHasQ = 1u << 8, kIsV = 1u << 9, kScan = 1u << 10, kLast = 1u << 11;   // | slot | tile of kMeta << 16
+    uint32_t queue[4] = {0, 0, 0, 0};
+    int queued = 0;
+    uint32_t bad = 0;                                 // rows of this warp in which this thread has found a value that is not finite
+    auto signal = [&](uint32_t what) {
+      const int at = what & 0xFF;
+      if (what & kScan) {
+        const int pieces = min(16, (D - ((what & kLast) && kWide ? 128 : 0)) / 8);
+        for (int k = lane; k < 32 * pieces; k += 32) {
+          // rows of this warp, all landed: each lane waited for its own copies before the __syncwarp of the caller
+          const uint32_t from = ring + (uint32_t)at * kSlotBytes + piece(32 * w + k / pieces, k % pieces);
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(from) : "memory");
+          bool found = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = (v[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (v[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+            found |= (lo | hi) != 0;
+            v[e] &= ~(lo | hi);
+          }
+          if (found) {
+            bad |= 1u << (k / pieces);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(from), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+          }
+        }
+      }
+      if ((what & kIsV) && (what & kLast)) {
+        const int m = what >> 16;
+        const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, bad);
+        bad = 0;
+        if (lane == 0) {
+          ctl->v_bad[m][w] = any;
+          arrive(ctl->v_meta[m]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (what & kHasQ) arrive(ctl->q_full);
+        arrive(ctl->full[at]);
+      }
+    };
+    auto signal_oldest = [&] {
+      __syncwarp();
+      signal(queue[0]);
+      queue[0] = queue[1];
+      queue[1] = queue[2];
+      queue[2] = queue[3];
+      --queued;
+    };
+    auto signal_all = [&] {
+      cp_async_wait<0>();
+      while (queued > 0) signal_oldest();
+    };
+    auto push = [&](uint32_t what) {
+      cp_async_commit();
+      if (queued == 0) queue[0] = what;
+      else if (queued == 1) queue[1] = what;
+      else if (queued == 2) queue[2] = what;
+      else queue[3] = what;
+      if (++queued == 4) {
+        cp_async_wait<3>();
+        signal_oldest();
+      }
+    };
+    // waits for a barrier; while it is not there, what has been copied is handed on
+    auto wait_or_signal = [&](uint64_t& bar, uint32_t parity) {
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&bar), parity & 1u))) return true;
+      signal_all();
+      return wait_warp(bar, parity);
+    };
+    bool ok = true;
+    while (ok && next_segment(true)) {
+      const Segment& s = ctl->seg[seg_n & 1];
+      const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
+      const int64_t head_b = s.head * p.cache.head_b, shead_b = s.head * p.cache.shead_b;
+      // ---- Q
+      if (q_n > 0 && !wait_or_signal(ctl->q_empty, q_n - 1)) break;
+      {
+        const int pieces = D / 8;
+        for (int t = 0; t < s.nt; ++t) {
+          const int r = s.row0 + t * 128 + 32 * w + lane;
+          int64_t off = -1;
+          if (r < s.rows) {
+            const int i = (int)fast_div((uint32_t)r, a.div_g);
+            off = ((int64_t)s.s0 + i) * p.q.ts + (int64_t)(s.head * G + (r - i * G)) * p.q.hs;
+          }
+          for (int k = 0; k < 32; ++k) {
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, k);
+            if (lane < pieces)
+              copy16_or_zero(q_smem + (uint32_t)(t * 2) * kBlockBytes + piece(32 * w + k, lane),
+                             static_cast<const uint16_t*>(p.q.data) + (o < 0 ? 0 : o) + lane * 8, o >= 0);
+          }
+        }
+      }
+      bool has_q = true;
+      // ---- K and V in the order in which they are used: keys run `lead` tiles ahead of values
+      int pg[3], at[3];                               // page and place of this lane's row in the next values' tile and those behind it
+      auto request = [&](int n, int& page, int& place) {
+        const int pos = s.key0 + n * kKeys + 32 * w + lane;
+        page = -1;
+        place = 0;
+        if (n < T && pos < s.hull_hi) {
+          const int i = (int)fast_div((uint32_t)pos, p.cache.div_page);
+          place = pos - i * p.cache.page_size;
+          page = p.table[(int64_t)s.b * p.table_stride + i];
+          if ((page < 0 || page >= p.cache.num_pages) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
+        }
+      };
+      request(0, pg[0], at[0]);
+      request(1, pg[1], at[1]);
+      request(2, pg[2], at[2]);
+      int next_k = 0, next_v = 0;
+      while (ok && next_v < T) {
+        const bool values = next_k == min(T, next_v + lead);
+        const int n = values ? next_v : next_k;
+        const int page = n == next_v ? pg[0] : pg[1], place = n == next_v ? at[0] : at[1];
+        const bool live = page >= 0 && page < p.cache.num_pages;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
+        const int m = (kn + n) % kMeta;
+        if (!values && lane == 0) {
+          ctl->live[m][w] = mask;
+          arrive(ctl->k_meta[m]);
+        }
+        const bool partly = values && partly_seen(s, n);
+        const int64_t off = live ? ((int64_t)((uint64_t)(uint32_t)page * p.cache.page_u + (uint64_t)(uint32_t)place * p.cache.tok_u) << 4) + head_b : -1;
+        const uint8_t* from = values ? p.cache.v : p.cache.k;
+        for (int part = 0; part < kSlotsPerTile; ++part) {
+          const int pieces = min(16, (D - part * 128) / 8);
+          if (!wait_or_signal(ctl->empty[slot], phase ^ 1u)) { ok = false; break; }
+          const uint32_t dst = ring + (uint32_t)slot * kSlotBytes;
+          if (!kFp8) {
+            const int c = lane & 15, sub = lane >> 4;
+#pragma unroll 4
+            for (int k = 0; k < 16; ++k) {
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 2 * k + sub);
+              if (c < pieces) copy16_or_zero(dst + piece(32 * w + 2 * k + sub, c), from + (o < 0 ? 0 : o) + part * 256 + c * 16, o >= 0);
+            }
+          } else {
+            uint32_t word = 0;
+            if (live) {
+              const int64_t so = ((int64_t)((uint64_t)(uint32_t)page * p.cache.spage_u + (uint64_t)(uint32_t)place * p.cache.stok_u) << 2) + shead_b;
+              word = *reinterpret_cast<const uint32_t*>((values ? p.cache.vs : p.cache.ks) + so + 4 * part);
+            }
+            const int c = lane & 7, sub = lane >> 3;  // 16 codes of a row, row of four
+            uint4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 4 * k + sub);
+              x[k] = make_uint4(0, 0, 0, 0);
+              if (o >= 0 && 2 * c < pieces) x[k] = *reinterpret_cast<const uint4*>(from + o + part * 128 + c * 16);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t sw = __shfl_sync(0xFFFFFFFFu, word, 4 * k + sub);
+              const float scale = (mask >> (4 * k + sub)) & 1u ? __uint_as_float(((sw >> (8 * (c >> 1))) & 0xFFu) << 23) : 0.f;
+              const uint32_t codes[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t f0, f1;
+                e4m3x4_to_f16x2(codes[e], f0, f1);
+                const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&f0)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+                y[2 * e] = pack_bf16(g0.x * scale, g0.y * scale);
+                y[2 * e + 1] = pack_bf16(g1.x * scale, g1.y * scale);
+              }
+              if (2 * c < pieces) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(32 * w + 4 * k + sub, 2 * c + e)), "r"(y[4 * e]),
+                               "r"(y[4 * e + 1]), "r"(y[4 * e + 2]), "r"(y[4 * e + 3])
+                               : "memory");
+              }
+            }
+          }
+          push((uint32_t)slot | (has_q ? kHasQ : 0u) | (values ? kIsV : 0u) | (partly ? kScan : 0u) |
+               (part + 1 == kSlotsPerTile ? kLast : 0u) | ((uint32_t)m << 16));
+          if (kFp8) signal_all();
+          has_q = false;
+          if (++slot == kSlots) { slot = 0; phase ^= 1u; }
+        }
+        if (values) {
+          ++next_v;
+          pg[0] = pg[1];
+          at[0] = at[1];
+          pg[1] = pg[2];
+          at[1] = at[2];
+          request(next_v + 2, pg[2], at[2]);
+        } else {
+          ++next_k;
+        }
+      }
+      if (!ok) break;
+      kn += T;
+      ++q_n;
+      // nothing of this segment may wait for the next one's rows
+      signal_all();
+      if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);
+      ++seg_n;
+    }
+    cp_async_wait<0>();
+  }
+
+  // ---- rows that see nothing, and (a shared prefix) rows of no group
+  if (warp < 8) {
+    const int64_t E = a.header->entries;
+    const int Hq = p.Hk * G;
+    for (int64_t e = blockIdx.x; e < E; e += gridDim.x) {
+      const Entry x = a.entries[e];
+      if (x.units > 0) continue;
+      const int n = min(x.rows - x.row0, kPair);
+      for (int k = warp; k < n * p.Hk; k += 8) {
+        const int r = x.row0 + k % n, i = r / G, h = (k / n) * G + r - i * G;
+        const int64_t token = (int64_t)x.s0 + i;
+        float z[16];
+#pragma unroll
+        for (int d = 0; d < 16; ++d) z[d] = 0.f;
+        for (int d = lane * 16; d < D; d += 512) emit16(p, token, h, d, z, 0.f, 0.f);
+      }
+    }
+    if (p.out == nullptr) {
+      const int64_t first = p.B > 0 ? min((int64_t)max(__ldcg(p.cu), 0), p.T) : 0;
+      const int64_t past = p.B > 0 ? min((int64_t)max(__ldcg(p.cu + p.B), 0), p.T) : 0;
+      for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < p.T * Hq; k += (int64_t)gridDim.x * 256) {
+        const int64_t t = k / Hq;
+        if (t < first || t >= past) p.prior_lse[k] = -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    if (*abort_flag) {
+      // what has been issued may still run: a commit behind it, waited for with a limit
+      if (lane == 0) {
+        volatile int32_t never = 0;
+        mbar_init(smem_u32(&ctl->drained), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tc_commit(smem_u32(&ctl->drained));
+        wait_inline(smem_u32(&ctl->drained), 0, &never, nullptr);
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+  }
+}
+
+template <bool kWide, bool kFp8, bool kForm>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  static PerContextOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(prompt_kernel<kWide, kFp8, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(kThreads), kSmemBytes, stream, true, a);
+}
+
+template <bool kFp8>
+cudaError_t launch_any(const Args& a, cudaStream_t stream) {
+  const bool form = a.p.form.cap2 > 0.f || a.p.form.slopes != nullptr || !(a.p.scale_log2 > 0.f);
+  if (a.p.D > 128) return form ? launch<true, kFp8, true>(a, stream) : launch<true, kFp8, false>(a, stream);
+  return form ? launch<false, kFp8, true>(a, stream) : launch<false, kFp8, false>(a, stream);
+}
+
+cudaError_t launch_bf16(const Args& a, cudaStream_t stream);
+cudaError_t launch_fp8(const Args& a, cudaStream_t stream);
+
+}  // namespace prompt
+}  // namespace engram
