@@ -240,6 +240,12 @@ __device__ __forceinline__ uint32_t idesc_of(int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// one lane of a warp that is together
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(is));
+  return is != 0;
+}
 template <int kRegs>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
@@ -365,10 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
     uint64_t& bar = ctl->seg_full[seg_n & 1];
     if (!(whole_warp ? wait_warp(bar, seg_n >> 1) : wait(bar, seg_n >> 1))) return false;
     return ctl->seg[seg_n & 1].tiles > 0;
-  };
-  auto done_segment = [&] {                           // one lane of each reader
-    arrive(ctl->seg_empty[seg_n & 1]);
-    ++seg_n;
   };
 
   if (warp < 8) {
@@ -587,70 +589,86 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
     fewer_registers<72>();
     if (warp == 8) {
       // -------------------------------------------------------------- MMA
-      if (lane == 0) {
+      // The warp stays together: every lane waits, one issues. (Uniform registers hold the descriptors.)
+      {
+        const bool leader = elect_one();
         uint32_t used[2] = {0, 0}, kn = 0, q_n = 0;
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t id_s = idesc_of(kKeys, false);
-        while (ok && next_segment(false)) {
+        const uint32_t id_s = idesc_of(kKeys, false), id_o = idesc_of(min(128, D), true), id_o2 = idesc_of(kWide ? D - 128 : 16, true);
+        const uint64_t ring_k = smem_desc_sw128(ring), ring_v = smem_desc_mn(ring);
+        while (ok && next_segment(true)) {
           const Segment s = ctl->seg[seg_n & 1];
           const int T = s.tiles;
           auto next_slot = [&] {
             if (++slot == kSlots) { slot = 0; phase ^= 1u; }
           };
-          // S(buf) (+)= Q(t) K^T over the part of the heads that lies in a slot
+          // S(buf) (+)= Q(t) K^T over the part of the heads that lies in a slot. (One thread issues all of it: descriptors
+          // are sums with constants, 16 MMAs without a loop.)
           auto qk = [&](int t, int buf, int at, int part) {
-            const uint32_t q0 = q_smem + (uint32_t)(t * 2 + part * 2) * kBlockBytes, k0 = ring + (uint32_t)at * kSlotBytes;
-            const int steps = min(8, (D - part * 128 + 15) / 16);
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t off = (uint32_t)((k >> 2) * kBlockBytes + (k & 3) * 32);
-              tc_mma(tmem + buf * 128, smem_desc_sw128(q0 + off), smem_desc_sw128(k0 + off), id_s, part > 0 || k > 0 ? 1u : 0u);
+            const uint64_t q0 = smem_desc_sw128(q_smem) + (uint64_t)((t + part) * (2 * kBlockBytes >> 4));
+            const uint64_t k0 = ring_k + (uint64_t)(at * (kSlotBytes >> 4));
+            const uint32_t to = tmem + buf * 128;
+            const int steps = kWide && part == 0 ? 8 : (kWide ? D - 128 : D) / 16;
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t off = (uint64_t)(((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4);
+                if (k < steps) tc_mma(to, q0 + off, k0 + off, id_s, part > 0 || k > 0 ? 1u : 0u);
+              }
             }
+            __syncwarp();
           };
           // O(t) (+)= P(buf) V for the values that lie in a slot
           auto pv = [&](int t, int buf, int at, int part, bool add) {
-            const uint32_t v0 = ring + (uint32_t)at * kSlotBytes;
-            const uint32_t id = idesc_of(min(128, D - part * 128), true);
+            const uint64_t v0 = ring_v + (uint64_t)(at * (kSlotBytes >> 4));
+            const uint32_t to = tmem + kOCol + t * 128 + part * 128, from = tmem + buf * 128, id = part == 0 ? id_o : id_o2;
+            if (leader) {
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              tc_mma_ts(tmem + kOCol + t * 128 + part * 128, tmem + buf * 128 + k * 8, smem_desc_mn(v0 + k * 2048), id, add || k > 0 ? 1u : 0u);
+              for (int k = 0; k < kKeys / 16; ++k) tc_mma_ts(to, from + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id, add || k > 0 ? 1u : 0u);
+            }
+            __syncwarp();
           };
-          if (!wait(ctl->q_full, q_n)) break;
+          auto commit = [&](uint64_t& bar) {
+            if (leader) tc_commit(smem_u32(&bar));
+            __syncwarp();
+          };
+          if (!wait_warp(ctl->q_full, q_n)) break;
           if (!kWide && s.nt == 2) {
-            if (!wait(ctl->full[slot], phase)) break;
+            if (!wait_warp(ctl->full[slot], phase)) break;
             tc_fence_after();
             for (int t = 0; t < 2; ++t) {
               qk(t, t, slot, 0);
-              tc_commit(smem_u32(&ctl->s_full[t]));
+              commit(ctl->s_full[t]);
             }
-            tc_commit(smem_u32(&ctl->empty[slot]));
-            if (T == 1) tc_commit(smem_u32(&ctl->q_empty));
+            commit(ctl->empty[slot]);
+            if (T == 1) commit(ctl->q_empty);
             next_slot();
             for (int n = 0; n < T; ++n) {
               const int v = slot;
-              if (!wait(ctl->full[slot], phase)) { ok = false; break; }
+              if (!wait_warp(ctl->full[slot], phase)) { ok = false; break; }
               next_slot();
-              if (n + 1 < T && !wait(ctl->full[slot], phase)) { ok = false; break; }
+              if (n + 1 < T && !wait_warp(ctl->full[slot], phase)) { ok = false; break; }
               const bool partly = partly_seen(s, n);
-              if (partly && !wait(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
+              if (partly && !wait_warp(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
               const bool add = n > 0 || (partly && not_finite(kn + n));
               for (int t = 0; t < 2; ++t) {
-                if (!wait(ctl->p_full[t], used[t] + n)) { ok = false; break; }
+                if (!wait_warp(ctl->p_full[t], used[t] + n)) { ok = false; break; }
                 tc_fence_after();
                 pv(t, t, v, 0, add);
-                if (t == 1) tc_commit(smem_u32(&ctl->empty[v]));
+                if (t == 1) commit(ctl->empty[v]);
                 if (n + 1 < T) {
                   qk(t, t, slot, 0);
-                  tc_commit(smem_u32(&ctl->s_full[t]));
+                  commit(ctl->s_full[t]);
                 } else {
-                  tc_commit(smem_u32(&ctl->o_final[t]));
+                  commit(ctl->o_final[t]);
                 }
               }
               if (!ok) break;
               if (n + 1 < T) {
-                tc_commit(smem_u32(&ctl->empty[slot]));
-                if (n + 2 == T) tc_commit(smem_u32(&ctl->q_empty));
+                commit(ctl->empty[slot]);
+                if (n + 2 == T) commit(ctl->q_empty);
                 next_slot();
               }
             }
@@ -659,32 +677,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
           } else {
             auto keys = [&](int n) {                  // the scores of key tile n, into its buffer
               for (int part = 0; part < kSlotsPerTile; ++part) {
-                if (!wait(ctl->full[slot], phase)) return false;
+                if (!wait_warp(ctl->full[slot], phase)) return false;
                 tc_fence_after();
                 qk(0, n & 1, slot, part);
-                tc_commit(smem_u32(&ctl->empty[slot]));
+                commit(ctl->empty[slot]);
                 next_slot();
               }
-              tc_commit(smem_u32(&ctl->s_full[n & 1]));
-              if (n + 1 == T) tc_commit(smem_u32(&ctl->q_empty));
+              commit(ctl->s_full[n & 1]);
+              if (n + 1 == T) commit(ctl->q_empty);
               return true;
             };
             ok = keys(0) && (T < 2 || keys(1));
             for (int n = 0; ok && n < T; ++n) {
-              if (!wait(ctl->p_full[n & 1], used[n & 1] + (n >> 1))) { ok = false; break; }
+              if (!wait_warp(ctl->p_full[n & 1], used[n & 1] + (n >> 1))) { ok = false; break; }
               const bool partly = partly_seen(s, n);
-              if (partly && !wait(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
+              if (partly && !wait_warp(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
               const bool add = n > 0 || (partly && not_finite(kn + n));
               for (int part = 0; part < kSlotsPerTile; ++part) {
-                if (!wait(ctl->full[slot], phase)) { ok = false; break; }
+                if (!wait_warp(ctl->full[slot], phase)) { ok = false; break; }
                 tc_fence_after();
                 pv(0, n & 1, slot, part, add);
-                tc_commit(smem_u32(&ctl->empty[slot]));
+                commit(ctl->empty[slot]);
                 next_slot();
               }
               if (!ok) break;
-              tc_commit(smem_u32(&ctl->o_done));
-              if (n + 1 == T) tc_commit(smem_u32(&ctl->o_final[0]));
+              commit(ctl->o_done);
+              if (n + 1 == T) commit(ctl->o_final[0]);
               if (n + 2 < T) ok = keys(n + 2);
             }
             used[0] += (T + 1) >> 1;
@@ -693,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
           if (!ok) break;
           kn += T;
           ++q_n;
-          done_segment();
+          if (leader) arrive(ctl->seg_empty[seg_n & 1]);
+          ++seg_n;
         }
       }
     } else if (warp == 9) {
@@ -752,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
         end.tiles = 0;
         if (ok) put(end);
       }
+      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------------- rows of Q, K and V
@@ -995,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
   if (warp == 8) {
     if (*abort_flag) {
       // what has been issued may still run: a commit behind it, waited for with a limit
-      if (lane == 0) {
+      if (elect_one()) {
         volatile int32_t never = 0;
         mbar_init(smem_u32(&ctl->drained), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
