@@ -1,6 +1,8 @@
 // Attention of prompts: the list of its work (one CTA), the join of pairs that many CTAs share, and the launches.
 #include "prompt.cuh"
 
+#include <mutex>
+
 namespace engram {
 namespace prompt {
 namespace {
@@ -99,11 +101,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
       min_hi = min(min_hi, __shfl_xor_sync(0xFFFFFFFFu, min_hi, o));
     }
     if (e < E && sub == 0) {
-      x.lo = lo;
       x.hi = hi;
       x.max_lo = max_lo;
       x.min_hi = min_hi;
-      x.units = lo < hi ? (hi - lo + kKeys - 1) / kKeys : 0;
+      x.key0 = a.box > 0 ? lo & ~(a.box - 1) : lo;    // boxes start where they do in their pages
+      x.units = lo < hi ? (hi - x.key0 + kKeys - 1) / kKeys : 0;
       a.entries[e] = x;
     }
   }
@@ -157,6 +159,44 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   }
 }
 
+// Tokens of a TMA box: the largest power of two up to 64 that divides a page, 8 at least (eight 128-byte rows are the
+// swizzle's pattern); 0: rows are fetched one by one. (Larger boxes would only start key tiles further ahead of a window.)
+int box_of(const CacheRef& c) {
+  int box = 64;
+  while (c.page_size % box != 0) box /= 2;
+  return box >= 8 && c.num_pages > 0 ? box : 0;
+}
+
+// The cache's keys or values as [page][head][place][value], boxes of `box` tokens by 128 bytes: bf16 in the MMAs' swizzle,
+// codes as they are. False if the strides do not fit a tensor map.
+bool make_map_pages(CUtensorMap* m, const void* base, const PromptParams& p, int box) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Encode fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<Encode>(f);
+  });
+  if (fn == nullptr) return false;
+  const CacheRef& c = p.cache;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)c.page_size, (cuuint64_t)p.Hk, (cuuint64_t)c.num_pages};
+  const int64_t row = (int64_t)p.D * (c.fp8 ? 1 : 2);
+  // an axis of one entry is never stepped along: any stride that a map takes
+  cuuint64_t strides[3] = {(cuuint64_t)c.tok_b, (cuuint64_t)c.head_b, (cuuint64_t)c.page_b};
+  for (int i = 0; i < 3; ++i) {
+    if (dims[i + 1] == 1) strides[i] = (cuuint64_t)row;
+    if (strides[i] == 0 || strides[i] >= (cuuint64_t)1 << 40) return false;
+  }
+  const cuuint32_t boxes[4] = {c.fp8 ? 128u : 64u, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+  return fn(m, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes,
+            steps, CU_TENSOR_MAP_INTERLEAVE_NONE, c.fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 Layout layout_of(int32_t G, int32_t D, int64_t T, int32_t B, int ctas) {
@@ -200,8 +240,11 @@ cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   // cut once or twice, and the last to arrive joins it.
   const int R = pair_rows(p.D);
   a.join = (p.T * p.G + R - 1) / R * p.Hk >= a.ctas;
+  CUtensorMap tm_k{}, tm_v{};
+  a.box = box_of(p.cache);
+  if (a.box > 0 && !(make_map_pages(&tm_k, p.cache.k, p, a.box) && make_map_pages(&tm_v, p.cache.v, p, a.box))) a.box = 0;
   cudaError_t e = launch_k(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
-  if (e == cudaSuccess) e = p.cache.fp8 ? launch_fp8(a, stream) : launch_bf16(a, stream);
+  if (e == cudaSuccess) e = p.cache.fp8 ? launch_fp8(tm_k, tm_v, a, stream) : launch_bf16(tm_k, tm_v, a, stream);
   if (e == cudaSuccess && !a.join) e = launch_k(join_kernel, dim3((unsigned)a.ctas * 2), dim3(256), 0, stream, true, a);
   return e;
 }

@@ -12,9 +12,11 @@
 //   warp 8             issues the MMAs:  S = Q K^T (both from shared memory),  O += P V (P from tensor memory, V as it
 //                      lies, by rows of keys: an MN-major operand)
 //   warp 9             walks the CTA's share of the work and hands segments (a run of key tiles of one pair of tiles) out
-//   warps 12..15       bring rows in: Q, then K and V tiles in the order in which they are used, into a ring of 32 KB
-//                      slots. A row is where its page says: 16-byte copies (cp.async) at any page size and stride; FP8
-//                      rows are converted to bf16 on the way (exact)
+//   warp 12            looks pages up and requests K and V tiles in the order in which they are used: TMA boxes of the
+//                      cache's own layout, up to 64 tokens of a page at once. bf16 goes to a ring of 32 KB slots that
+//                      the MMAs read, FP8 to stages
+//   warps 10, 11, 13..15   bring Q in (16-byte copies); FP8: convert a stage's rows to bf16 into the ring (exact). Pages
+//                      that are no multiple of 8 tokens do not divide into boxes: these warps then fetch the rows themselves
 // While the softmax of one tile runs, the tensor cores work on the other; with one tile, on the next key tile.
 //
 // Work is cut at key tiles: a first kernel (one CTA) lists the pairs of tiles with the hull of their keys, and every CTA
@@ -37,11 +39,13 @@ namespace prompt {
 constexpr int kKeys = 128;                            // of a tile
 constexpr int kSlotBytes = 32768;                     // 128 keys of up to 128 values, as two blocks of 128-byte rows
 constexpr int kBlockBytes = 16384;
-constexpr int kSlots = 5;
+__host__ __device__ constexpr int slots_of(bool fp8) { return fp8 ? 3 : 5; }
+constexpr int kStages = 3;                            // FP8: of 128 codes and their scale word for each of 128 keys
+constexpr int kStageBytes = kBlockBytes + 512;
 constexpr int kQBytes = 65536;
 constexpr int kThreads = 512;
-constexpr int kProducers = 4;                         // warps
-constexpr int kMeta = 16;                             // key tiles whose masks are kept
+constexpr int kHelpers = 5;                           // warps
+constexpr int kMeta = 8;                              // key tiles whose masks are kept
 constexpr int kRunCost = 1;                           // a pair's fixed cost in key tiles, when work is divided
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;                       // S of buffer b at column 128 b, O of tile t at 256 + 128 t
@@ -50,9 +54,9 @@ constexpr uint32_t kOCol = 256;                       // S of buffer b at column
 struct Entry {
   int32_t b, row0, rows;                              // sequence; rows [row0, rows) of its n * G, at most a pair's
   int32_t s0, n, len;
-  int32_t lo, hi;                                     // hull of the keys that its rows see (lo = hi: none)
+  int32_t hi;                                         // past the last key that any of its rows sees
   int32_t max_lo, min_hi;                             // keys from max_lo to min_hi are seen by every row that sees any
-  int32_t units, pad;                                 // key tiles
+  int32_t key0, units;                                // first key and number of its key tiles
   int64_t place;                                      // in the row of a head's work
 };
 struct Header {
@@ -81,6 +85,7 @@ struct Args {
   int32_t slot_floats;
   int32_t join;                                       // 1: the last warp to arrive joins a cut pair's rows
   int32_t ctas;
+  int32_t box;                                        // tokens per TMA box, a power of two that divides a page (0: rows one by one)
   FastDiv div_g;
 };
 
@@ -255,6 +260,11 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+               : "memory");
+}
 // mbar_wait without a call: a function call's registers do not go together with setmaxnreg
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -279,12 +289,13 @@ struct Segment {
   int32_t b, head;
   int32_t row0, rows, s0, n, len;
   int32_t key0;                                       // first key of the segment
-  int32_t hull_lo, hull_hi, max_lo, min_hi;
+  int32_t hull_hi, max_lo, min_hi;                    // see Entry
   int32_t whole;                                      // all of its pair's keys
   int32_t c_first, c_last;                            // CTAs of a cut pair
 };
 struct Ctl {
-  uint64_t full[kSlots], empty[kSlots];
+  uint64_t full[5], empty[5];
+  uint64_t st_full[kStages], st_empty[kStages];
   uint64_t q_full, q_empty;
   uint64_t k_meta[kMeta], v_meta[kMeta];
   uint64_t s_full[2], p_full[2], o_final[2], o_done;
@@ -292,13 +303,13 @@ struct Ctl {
   uint64_t drained;
   Segment seg[2];
   uint32_t live[kMeta][4];                            // which keys of a tile are there
-  uint32_t v_bad[kMeta][kProducers];                  // keys whose values are not all finite (in tiles that some row sees partly)
+  uint32_t v_bad[kMeta][kHelpers][4];                 // keys whose values are not all finite (in tiles that some row sees partly)
   uint32_t tmem_base;
   int32_t abort_flag;
 };
-constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + (int)sizeof(Ctl);
-static_assert(kSmemBytes <= kSmemBudget, "one CTA's shared memory");
-constexpr int kSegReaders = 8 + 1 + kProducers;
+constexpr int smem_bytes(bool fp8) { return 1024 + kQBytes + slots_of(fp8) * kSlotBytes + (fp8 ? kStages * kStageBytes : 0) + (int)sizeof(Ctl); }
+static_assert(smem_bytes(false) <= kSmemBudget && smem_bytes(true) <= kSmemBudget, "one CTA's shared memory");
+constexpr int kSegReaders = 8 + 1 + 1 + kHelpers;
 
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 // 16-byte piece c of row r in blocks of 128-byte rows, 128B swizzle
@@ -307,13 +318,16 @@ __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)((c >
 // kWide: heads of more than 128 values (one tile of rows, two slots per key or value tile). kForm: scores with a form, or a
 // scale that is not positive
 template <bool kWide, bool kFp8, bool kForm>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                                                             const __grid_constant__ Args a) {
   const PromptParams& p = a.p;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t q_smem = (raw + 1023u) & ~1023u;
   const uint32_t ring = q_smem + kQBytes;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (ring + kSlots * kSlotBytes - raw));
+  constexpr int kSlots = slots_of(kFp8);
+  const uint32_t stages = ring + kSlots * kSlotBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (stages + (kFp8 ? kStages * kStageBytes : 0) - raw));
   volatile int32_t* abort_flag = &ctl->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = p.D, G = p.G;
@@ -322,14 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), kProducers);
+      mbar_init(smem_u32(&ctl->full[s]), !kFp8 && a.box > 0 ? 1 : kHelpers);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
-    mbar_init(smem_u32(&ctl->q_full), kProducers);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&ctl->st_full[s]), 1 + 32);  // the boxes, and every lane's scale words
+      mbar_init(smem_u32(&ctl->st_empty[s]), kHelpers);
+    }
+    mbar_init(smem_u32(&ctl->q_full), kHelpers);
     mbar_init(smem_u32(&ctl->q_empty), 1);
     for (int i = 0; i < kMeta; ++i) {
-      mbar_init(smem_u32(&ctl->k_meta[i]), kProducers);
-      mbar_init(smem_u32(&ctl->v_meta[i]), kProducers);
+      mbar_init(smem_u32(&ctl->k_meta[i]), 1);
+      mbar_init(smem_u32(&ctl->v_meta[i]), kHelpers);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
@@ -342,6 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
     ctl->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 12 && lane == 0 && a.box > 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)), "n"(kTmemCols) : "memory");
@@ -356,15 +378,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
   auto wait = [&](uint64_t& bar, uint32_t parity) { return wait_inline(smem_u32(&bar), parity & 1u, abort_flag, p.err); };
   // the same for a whole warp, with one answer for all of it
   auto wait_warp = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
-  // whether some row that sees keys at all does not see all of the tile's, and whether values there were not finite
+  // whether some row that sees keys at all does not see all of the tile's (none sees those past its ends), and whether
+  // values there were not finite
   auto partly_seen = [&](const Segment& s, int n) {
     const int first = s.key0 + n * kKeys;
-    return max(first, s.hull_lo) < s.max_lo || min(first + kKeys, s.hull_hi) > s.min_hi;
+    return first < s.max_lo || first + kKeys > s.min_hi;
   };
-  auto not_finite = [&](uint32_t kn) {
-    const volatile uint32_t* f = ctl->v_bad[kn % kMeta];
-    return (f[0] | f[1] | f[2] | f[3]) != 0;
+  auto bad_keys = [&](uint32_t kn, int w) {
+    uint32_t y = 0;
+#pragma unroll
+    for (int h = 0; h < kHelpers; ++h) y |= *(volatile uint32_t*)&ctl->v_bad[kn % kMeta][h][w];
+    return y;
   };
+  auto not_finite = [&](uint32_t kn) { return (bad_keys(kn, 0) | bad_keys(kn, 1) | bad_keys(kn, 2) | bad_keys(kn, 3)) != 0; };
   auto arrive = [&](uint64_t& bar) { mbar_arrive(smem_u32(&bar)); };
   uint32_t seg_n = 0;                                 // segments read so far
   auto next_segment = [&](bool whole_warp) {
@@ -494,8 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
                 }
                 for (int w = 0; w < 4; ++w) {
                   const uint32_t sees = w == 0 ? mask[0] : w == 1 ? mask[1] : w == 2 ? mask[2] : mask[3];
-                  for (uint32_t left = *(volatile uint32_t*)&ctl->v_bad[kn % kMeta][w]; left != 0; left &= left - 1) {
+                  for (uint32_t left = bad_keys(kn, w); left != 0; left &= left - 1) {
                     const int j = 32 * w + __ffs(left) - 1;
+                    if (!__any_sync(0xFFFFFFFFu, (sees >> (j & 31)) & 1u)) continue;   // (past the sequence, maybe: no page)
                     uint32_t pw = tmem_ld1(s_t + (j >> 1));
                     tmem_ld_wait();
                     asm volatile("" : "+r"(pw));
@@ -585,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
       if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);
       ++seg_n;
     }
-  } else if (warp < 12) {
+  } else {
     fewer_registers<72>();
     if (warp == 8) {
       // -------------------------------------------------------------- MMA
@@ -749,8 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
                 s.s0 = e.s0;
                 s.n = e.n;
                 s.len = e.len;
-                s.key0 = e.lo + (int)(from - run0) * kKeys;
-                s.hull_lo = e.lo;
+                s.key0 = e.key0 + (int)(from - run0) * kKeys;
                 s.hull_hi = e.hi;
                 s.max_lo = e.max_lo;
                 s.min_hi = e.min_hi;
@@ -772,27 +798,152 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
         if (ok) put(end);
       }
       __syncwarp();
-    }
-  } else {
-    // ---------------------------------------------------------------- rows of Q, K and V
-    fewer_registers<72>();
-    const int w = warp - 12;                          // rows 32 w .. 32 w + 31 of every tile
-    int slot = 0;
-    uint32_t phase = 0, kn = 0, q_n = 0;
-    // copies that are under way: what to do once they have landed, oldest first
-    constexpr uint32_t kHasQ = 1u << 8, kIsV = 1u << 9, kScan = 1u << 10, kLast = 1u << 11;   // | slot | tile of kMeta << 16
-    uint32_t queue[4] = {0, 0, 0, 0};
-    int queued = 0;
-    uint32_t bad = 0;                                 // rows of this warp in which this thread has found a value that is not finite
-    auto signal = [&](uint32_t what) {
-      const int at = what & 0xFF;
-      if (what & kScan) {
-        const int pieces = min(16, (D - ((what & kLast) && kWide ? 128 : 0)) / 8);
-        for (int k = lane; k < 32 * pieces; k += 32) {
-          // rows of this warp, all landed: each lane waited for its own copies before the __syncwarp of the caller
-          const uint32_t from = ring + (uint32_t)at * kSlotBytes + piece(32 * w + k / pieces, k % pieces);
-          uint32_t v[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(from) : "memory");
+    } else if (warp == 12) {
+      // -------------------------------------------------------------- pages, and boxes of K and V
+      int slot = 0, stage = 0;
+      uint32_t phase = 0, st_phase = 0, kn = 0;
+      bool ok = true;
+      while (ok && next_segment(true)) {
+        const Segment& s = ctl->seg[seg_n & 1];
+        // keys run `lead` tiles ahead of values
+        const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
+        // pages of keys 32 j + lane of the next values' tile and those behind it, requested ahead
+        int pg[3][4];
+        auto request = [&](int n, int (&to)[4]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int pos = s.key0 + n * kKeys + 32 * j + lane;
+            to[j] = -1;
+            if (n < T && pos < s.hull_hi) {
+              to[j] = p.table[(int64_t)s.b * p.table_stride + (int)fast_div((uint32_t)pos, p.cache.div_page)];
+              if (to[j] < 0 || to[j] >= p.cache.num_pages) {
+                to[j] = -1;
+                if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
+              }
+            }
+          }
+        };
+        request(0, pg[0]);
+        request(1, pg[1]);
+        request(2, pg[2]);
+        int next_k = 0, next_v = 0;
+        while (ok && next_v < T) {
+          const bool values = next_k == min(T, next_v + lead);
+          const int n = values ? next_v : next_k;
+          const int first = s.key0 + n * kKeys;
+          int page[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) page[j] = n == next_v ? pg[0][j] : pg[1][j];
+          if (!values) {
+            const int m = (kn + n) % kMeta;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t live = __ballot_sync(0xFFFFFFFFu, page[j] >= 0);
+              if (lane == j) ctl->live[m][j] = live;
+            }
+            __syncwarp();
+            if (lane == 0) arrive(ctl->k_meta[m]);
+          }
+          for (int part = 0; part < kSlotsPerTile; ++part) {
+            if (kFp8 && a.box > 0 ? !wait_warp(ctl->st_empty[stage], st_phase ^ 1u) : !wait_warp(ctl->empty[slot], phase ^ 1u)) { ok = false; break; }
+            if (a.box > 0) {
+              const int blocks = kFp8 ? 1 : (min(128, D - part * 128) + 63) / 64;
+              const uint32_t dst = kFp8 ? stages + (uint32_t)(stage * kStageBytes) : ring + (uint32_t)(slot * kSlotBytes);
+              const uint32_t bar = smem_u32(kFp8 ? &ctl->st_full[stage] : &ctl->full[slot]);
+              if (lane == 0) mbar_expect_tx(bar, (uint32_t)(blocks * kBlockBytes));
+              // a lane per box of `box` keys by 64 values (128 codes); a page that is not there reads as zeros
+              const int box = blocks == 2 ? lane >> 1 : lane, at = box * a.box;
+              int pb = -1;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int y = __shfl_sync(0xFFFFFFFFu, page[j], at & 31);
+                if (at >> 5 == j) pb = y;
+              }
+              __syncwarp();
+              if (at < kKeys) {
+                const int pos = first + at, place = pos - (int)fast_div((uint32_t)pos, p.cache.div_page) * p.cache.page_size;
+                const int block = blocks == 2 ? lane & 1 : 0;
+                tma_load_4d(dst + (uint32_t)(block * kBlockBytes + at * 128), values ? &tm_v : &tm_k, bar, part * 128 + block * 64, place, s.head, pb);
+              }
+              if (kFp8) {
+                const uint8_t* from = (values ? p.cache.vs : p.cache.ks) + s.head * p.cache.shead_b + 4 * part;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int pos = first + 32 * j + lane, place = pos - (int)fast_div((uint32_t)pos, p.cache.div_page) * p.cache.page_size;
+                  const bool live = page[j] >= 0;
+                  const int64_t off = live ? (int64_t)((uint64_t)(uint32_t)page[j] * p.cache.spage_u + (uint64_t)(uint32_t)place * p.cache.stok_u) << 2 : 0;
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + kBlockBytes + (uint32_t)(32 * j + lane) * 4), "l"(from + off),
+                               "r"(live ? 4 : 0) : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+              }
+            }
+            if (kFp8 && a.box > 0) {
+              if (++stage == kStages) { stage = 0; st_phase ^= 1u; }
+            } else if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+          if (values) {
+            ++next_v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              pg[0][j] = pg[1][j];
+              pg[1][j] = pg[2][j];
+            }
+            request(next_v + 2, pg[2]);
+          } else {
+            ++next_k;
+          }
+        }
+        if (!ok) break;
+        kn += T;
+        __syncwarp();
+        if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);
+        ++seg_n;
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+    } else {
+      // -------------------------------------------------------------- Q; rows to convert, to fetch or to look through
+      const int w = warp < 12 ? warp - 10 : warp - 11;
+      const bool rows_here = kFp8 || a.box == 0;      // the slots are filled here
+      uint32_t kn = 0, q_n = 0, seq = 0;              // key tiles, segments, slots so far
+      bool ok = true;
+      while (ok && next_segment(true)) {
+        const Segment& s = ctl->seg[seg_n & 1];
+        const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
+        // ---- Q, 32 rows at a time
+        if (q_n > 0 && !wait_warp(ctl->q_empty, q_n - 1)) break;
+        {
+          const int pieces = D / 8;
+          for (int g = w; g < s.nt * 4; g += kHelpers) {
+            const int r = s.row0 + g * 32 + lane;
+            int64_t off = -1;
+            if (r < s.rows) {
+              const int i = (int)fast_div((uint32_t)r, a.div_g);
+              off = ((int64_t)s.s0 + i) * p.q.ts + (int64_t)(s.head * G + (r - i * G)) * p.q.hs;
+            }
+            constexpr int kLanes = kWide ? 32 : 16;   // of a row
+            const int c = lane % kLanes, sub = lane / kLanes;
+            const uint32_t to = q_smem + (uint32_t)((g >> 2) * 2) * kBlockBytes;
+#pragma unroll 4
+            for (int k = 0; k < kLanes; ++k) {
+              const int row = k * (32 / kLanes) + sub;
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+              if (c < pieces) copy16_or_zero(to + piece((g & 3) * 32 + row, c), static_cast<const uint16_t*>(p.q.data) + (o < 0 ? 0 : o) + c * 8, o >= 0);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) arrive(ctl->q_full);
+        }
+        uint32_t bad[4] = {0, 0, 0, 0};               // keys of the tile in which this thread has found a value that is not finite
+        // eight bf16 of key `row`: what is not finite becomes zero, and is noted
+        auto clean = [&](uint32_t (&v)[4], int row) {
           bool found = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -801,186 +952,162 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
             v[e] &= ~(lo | hi);
           }
           if (found) {
-            bad |= 1u << (k / pieces);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(from), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-          }
-        }
-      }
-      if ((what & kIsV) && (what & kLast)) {
-        const int m = what >> 16;
-        const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, bad);
-        bad = 0;
-        if (lane == 0) {
-          ctl->v_bad[m][w] = any;
-          arrive(ctl->v_meta[m]);
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        if (what & kHasQ) arrive(ctl->q_full);
-        arrive(ctl->full[at]);
-      }
-    };
-    auto signal_oldest = [&] {
-      __syncwarp();
-      signal(queue[0]);
-      queue[0] = queue[1];
-      queue[1] = queue[2];
-      queue[2] = queue[3];
-      --queued;
-    };
-    auto signal_all = [&] {
-      cp_async_wait<0>();
-      while (queued > 0) signal_oldest();
-    };
-    auto push = [&](uint32_t what) {
-      cp_async_commit();
-      if (queued == 0) queue[0] = what;
-      else if (queued == 1) queue[1] = what;
-      else if (queued == 2) queue[2] = what;
-      else queue[3] = what;
-      if (++queued == 4) {
-        cp_async_wait<3>();
-        signal_oldest();
-      }
-    };
-    // waits for a barrier; while it is not there, what has been copied is handed on
-    auto wait_or_signal = [&](uint64_t& bar, uint32_t parity) {
-      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&bar), parity & 1u))) return true;
-      signal_all();
-      return wait_warp(bar, parity);
-    };
-    bool ok = true;
-    while (ok && next_segment(true)) {
-      const Segment& s = ctl->seg[seg_n & 1];
-      const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
-      const int64_t head_b = s.head * p.cache.head_b, shead_b = s.head * p.cache.shead_b;
-      // ---- Q
-      if (q_n > 0 && !wait_or_signal(ctl->q_empty, q_n - 1)) break;
-      {
-        const int pieces = D / 8;
-        for (int t = 0; t < s.nt; ++t) {
-          const int r = s.row0 + t * 128 + 32 * w + lane;
-          int64_t off = -1;
-          if (r < s.rows) {
-            const int i = (int)fast_div((uint32_t)r, a.div_g);
-            off = ((int64_t)s.s0 + i) * p.q.ts + (int64_t)(s.head * G + (r - i * G)) * p.q.hs;
-          }
-          for (int k = 0; k < 32; ++k) {
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, k);
-            if (lane < pieces)
-              copy16_or_zero(q_smem + (uint32_t)(t * 2) * kBlockBytes + piece(32 * w + k, lane),
-                             static_cast<const uint16_t*>(p.q.data) + (o < 0 ? 0 : o) + lane * 8, o >= 0);
-          }
-        }
-      }
-      bool has_q = true;
-      // ---- K and V in the order in which they are used: keys run `lead` tiles ahead of values
-      int pg[3], at[3];                               // page and place of this lane's row in the next values' tile and those behind it
-      auto request = [&](int n, int& page, int& place) {
-        const int pos = s.key0 + n * kKeys + 32 * w + lane;
-        page = -1;
-        place = 0;
-        if (n < T && pos < s.hull_hi) {
-          const int i = (int)fast_div((uint32_t)pos, p.cache.div_page);
-          place = pos - i * p.cache.page_size;
-          page = p.table[(int64_t)s.b * p.table_stride + i];
-          if ((page < 0 || page >= p.cache.num_pages) && p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
-        }
-      };
-      request(0, pg[0], at[0]);
-      request(1, pg[1], at[1]);
-      request(2, pg[2], at[2]);
-      int next_k = 0, next_v = 0;
-      while (ok && next_v < T) {
-        const bool values = next_k == min(T, next_v + lead);
-        const int n = values ? next_v : next_k;
-        const int page = n == next_v ? pg[0] : pg[1], place = n == next_v ? at[0] : at[1];
-        const bool live = page >= 0 && page < p.cache.num_pages;
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
-        const int m = (kn + n) % kMeta;
-        if (!values && lane == 0) {
-          ctl->live[m][w] = mask;
-          arrive(ctl->k_meta[m]);
-        }
-        const bool partly = values && partly_seen(s, n);
-        const int64_t off = live ? ((int64_t)((uint64_t)(uint32_t)page * p.cache.page_u + (uint64_t)(uint32_t)place * p.cache.tok_u) << 4) + head_b : -1;
-        const uint8_t* from = values ? p.cache.v : p.cache.k;
-        for (int part = 0; part < kSlotsPerTile; ++part) {
-          const int pieces = min(16, (D - part * 128) / 8);
-          if (!wait_or_signal(ctl->empty[slot], phase ^ 1u)) { ok = false; break; }
-          const uint32_t dst = ring + (uint32_t)slot * kSlotBytes;
-          if (!kFp8) {
-            const int c = lane & 15, sub = lane >> 4;
-#pragma unroll 4
-            for (int k = 0; k < 16; ++k) {
-              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 2 * k + sub);
-              if (c < pieces) copy16_or_zero(dst + piece(32 * w + 2 * k + sub, c), from + (o < 0 ? 0 : o) + part * 256 + c * 16, o >= 0);
-            }
-          } else {
-            uint32_t word = 0;
-            if (live) {
-              const int64_t so = ((int64_t)((uint64_t)(uint32_t)page * p.cache.spage_u + (uint64_t)(uint32_t)place * p.cache.stok_u) << 2) + shead_b;
-              word = *reinterpret_cast<const uint32_t*>((values ? p.cache.vs : p.cache.ks) + so + 4 * part);
-            }
-            const int c = lane & 7, sub = lane >> 3;  // 16 codes of a row, row of four
-            uint4 x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 4 * k + sub);
-              x[k] = make_uint4(0, 0, 0, 0);
-              if (o >= 0 && 2 * c < pieces) x[k] = *reinterpret_cast<const uint4*>(from + o + part * 128 + c * 16);
+            for (int x = 0; x < 4; ++x)
+              if (row >> 5 == x) bad[x] |= 1u << (row & 31);
+          }
+          return found;
+        };
+        auto note = [&](int m, bool partly) {         // a value tile is through
+          if (partly) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, bad[x]);
+              if (lane == x) ctl->v_bad[m][w][x] = any;
+              bad[x] = 0;
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t sw = __shfl_sync(0xFFFFFFFFu, word, 4 * k + sub);
-              const float scale = (mask >> (4 * k + sub)) & 1u ? __uint_as_float(((sw >> (8 * (c >> 1))) & 0xFFu) << 23) : 0.f;
-              const uint32_t codes[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t f0, f1;
-                e4m3x4_to_f16x2(codes[e], f0, f1);
-                const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&f0)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
-                y[2 * e] = pack_bf16(g0.x * scale, g0.y * scale);
-                y[2 * e + 1] = pack_bf16(g1.x * scale, g1.y * scale);
+            __syncwarp();
+          }
+          if (lane == 0) arrive(ctl->v_meta[m]);
+        };
+        if (!rows_here) {
+          // value tiles that some row sees partly, once they have landed
+          for (int n = 0; ok && n < T; ++n) {
+            const int m = (kn + n) % kMeta;
+            if (!wait_warp(ctl->k_meta[m], (kn + n) / kMeta)) { ok = false; break; }   // (not further ahead than the ring)
+            const bool partly = partly_seen(s, n);
+            if (partly) {
+              for (int part = 0; part < kSlotsPerTile; ++part) {
+                const uint32_t at = seq + (uint32_t)((min(T, n + lead) + n) * kSlotsPerTile + part);
+                if (!wait_warp(ctl->full[at % kSlots], at / kSlots)) { ok = false; break; }
+                const uint32_t from = ring + (at % kSlots) * kSlotBytes;
+                const int pieces = min(16, (D - part * 128) / 8);
+                for (int k = w * 32 + lane; k < kKeys * pieces; k += kHelpers * 32) {
+                  const int row = k / pieces;
+                  const uint32_t addr = from + piece(row, k % pieces);
+                  uint32_t v[4];
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+                  if (clean(v, row))
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+                }
               }
-              if (2 * c < pieces) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(32 * w + 4 * k + sub, 2 * c + e)), "r"(y[4 * e]),
-                               "r"(y[4 * e + 1]), "r"(y[4 * e + 2]), "r"(y[4 * e + 3])
-                               : "memory");
-              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
             }
+            if (ok) note(m, partly);
           }
-          push((uint32_t)slot | (has_q ? kHasQ : 0u) | (values ? kIsV : 0u) | (partly ? kScan : 0u) |
-               (part + 1 == kSlotsPerTile ? kLast : 0u) | ((uint32_t)m << 16));
-          if (kFp8) signal_all();
-          has_q = false;
-          if (++slot == kSlots) { slot = 0; phase ^= 1u; }
-        }
-        if (values) {
-          ++next_v;
-          pg[0] = pg[1];
-          at[0] = at[1];
-          pg[1] = pg[2];
-          at[1] = at[2];
-          request(next_v + 2, pg[2], at[2]);
+          seq += (uint32_t)(2 * T * kSlotsPerTile);
         } else {
-          ++next_k;
+          int next_k = 0, next_v = 0;
+          while (ok && next_v < T) {
+            const bool values = next_k == min(T, next_v + lead);
+            const int n = values ? next_v++ : next_k++;
+            const int m = (kn + n) % kMeta;
+            const bool partly = values && partly_seen(s, n);
+            for (int part = 0; part < kSlotsPerTile; ++part, ++seq) {
+              const uint32_t dst = ring + (seq % kSlots) * kSlotBytes;
+              const int pieces = min(16, (D - part * 128) / 8);
+              // codes (16 of a row) to bf16
+              auto convert = [&](const uint4& x, float scale, int row, int c) {
+                const uint32_t codes[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e0 = 0; e0 < 2; ++e0) {
+                  const int e = e0 ^ ((c >> 2) & 1);  // (eight lanes of a row, eight different bank groups)
+                  uint32_t y[4];
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    uint32_t f0, f1;
+                    e4m3x4_to_f16x2(e == 0 ? codes[z] : codes[2 + z], f0, f1);
+                    const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&f0)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+                    y[2 * z] = pack_bf16(g0.x * scale, g0.y * scale);
+                    y[2 * z + 1] = pack_bf16(g1.x * scale, g1.y * scale);
+                  }
+                  if (partly) clean(y, row);
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(row, 2 * c + e)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+                }
+              };
+              if (kFp8 && a.box > 0) {
+                const uint32_t st = seq % kStages, from = stages + st * kStageBytes;
+                if (!wait_warp(ctl->st_full[st], seq / kStages) || (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1))) { ok = false; break; }
+                const int per_row = pieces / 2;
+#pragma unroll 2
+                for (int k = w * 32 + lane; k < kKeys * per_row; k += kHelpers * 32) {
+                  const int row = per_row == 8 ? k >> 3 : k / per_row, c = k - row * per_row;
+                  uint4 x;
+                  uint32_t word;
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(from + row * 128 + c * 16) : "memory");
+                  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(word) : "r"(from + kBlockBytes + row * 4) : "memory");
+                  convert(x, __uint_as_float(((word >> (8 * (c >> 1))) & 0xFFu) << 23), row, c);
+                }
+                __syncwarp();
+                if (lane == 0) arrive(ctl->st_empty[st]);
+              } else {
+                // 26 rows of each warp; a lane looks one up
+                if (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1)) { ok = false; break; }
+                const int row0 = w * 26, rows = min(26, kKeys - row0);
+                const int pos = s.key0 + n * kKeys + row0 + lane;
+                int64_t off = -1, soff = 0;
+                if (lane < rows && pos < s.hull_hi) {
+                  const int i = (int)fast_div((uint32_t)pos, p.cache.div_page), place = pos - i * p.cache.page_size;
+                  const int64_t page = p.table[(int64_t)s.b * p.table_stride + i];
+                  if (page >= 0 && page < p.cache.num_pages) {
+                    off = page * p.cache.page_b + s.head * p.cache.head_b + place * p.cache.tok_b;
+                    soff = page * p.cache.spage_b + s.head * p.cache.shead_b + place * p.cache.stok_b;
+                  }
+                }
+                const uint8_t* from = values ? p.cache.v : p.cache.k;
+                if (!kFp8) {
+                  const int c = lane & 15, sub = lane >> 4;
+                  for (int k = 0; k < 13; ++k) {
+                    const int row = 2 * k + sub;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+                    if (row < rows && c < pieces) copy16_or_zero(dst + piece(row0 + row, c), from + (o < 0 ? 0 : o) + part * 256 + c * 16, o >= 0);
+                  }
+                  cp_async_commit();
+                  cp_async_wait<0>();
+                  __syncwarp();
+                  if (partly) {
+                    for (int k = lane; k < rows * pieces; k += 32) {
+                      const int row = row0 + k / pieces;
+                      const uint32_t addr = dst + piece(row, k % pieces);
+                      uint32_t v[4];
+                      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+                      if (clean(v, row))
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+                    }
+                  }
+                } else {
+                  uint32_t word = 0;
+                  if (off >= 0) word = *reinterpret_cast<const uint32_t*>((values ? p.cache.vs : p.cache.ks) + soff + 4 * part);
+                  const int c = lane & 7, sub = lane >> 3;
+                  for (int k = 0; k < 7; ++k) {
+                    const int row = 4 * k + sub;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+                    const uint32_t sw = __shfl_sync(0xFFFFFFFFu, word, row);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (row < rows && 2 * c < pieces) {
+                      if (o >= 0) x = *reinterpret_cast<const uint4*>(from + o + part * 128 + c * 16);
+                      convert(x, o >= 0 ? __uint_as_float(((sw >> (8 * (c >> 1))) & 0xFFu) << 23) : 0.f, row0 + row, c);
+                    }
+                  }
+                }
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) arrive(ctl->full[seq % kSlots]);
+            }
+            if (ok && values) note(m, partly);
+          }
         }
+        if (!ok) break;
+        kn += T;
+        ++q_n;
+        __syncwarp();
+        if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);
+        ++seg_n;
       }
-      if (!ok) break;
-      kn += T;
-      ++q_n;
-      // nothing of this segment may wait for the next one's rows
-      signal_all();
-      if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);
-      ++seg_n;
+      cp_async_wait<0>();
     }
-    cp_async_wait<0>();
   }
 
   // ---- rows that see nothing, and (a shared prefix) rows of no group
@@ -1030,24 +1157,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Args a) {
 }
 
 template <bool kWide, bool kFp8, bool kForm>
-cudaError_t launch(const Args& a, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream) {
   static PerContextOnce once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(prompt_kernel<kWide, kFp8, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return cudaFuncSetAttribute(prompt_kernel<kWide, kFp8, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kFp8));
   });
   if (e != cudaSuccess) return e;
-  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(kThreads), kSmemBytes, stream, true, a);
+  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(kThreads), smem_bytes(kFp8), stream, true, tm_k, tm_v, a);
 }
 
 template <bool kFp8>
-cudaError_t launch_any(const Args& a, cudaStream_t stream) {
+cudaError_t launch_any(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream) {
   const bool form = a.p.form.cap2 > 0.f || a.p.form.slopes != nullptr || !(a.p.scale_log2 > 0.f);
-  if (a.p.D > 128) return form ? launch<true, kFp8, true>(a, stream) : launch<true, kFp8, false>(a, stream);
-  return form ? launch<false, kFp8, true>(a, stream) : launch<false, kFp8, false>(a, stream);
+  if (a.p.D > 128) return form ? launch<true, kFp8, true>(tm_k, tm_v, a, stream) : launch<true, kFp8, false>(tm_k, tm_v, a, stream);
+  return form ? launch<false, kFp8, true>(tm_k, tm_v, a, stream) : launch<false, kFp8, false>(tm_k, tm_v, a, stream);
 }
 
-cudaError_t launch_bf16(const Args& a, cudaStream_t stream);
-cudaError_t launch_fp8(const Args& a, cudaStream_t stream);
+cudaError_t launch_bf16(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream);
+cudaError_t launch_fp8(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream);
 
 }  // namespace prompt
 }  // namespace engram

@@ -4,7 +4,9 @@
 namespace engram {
 namespace prompt {
 
-cudaError_t launch_bf16(const Args& a, cudaStream_t stream) { return launch_any<false>(a, stream); }
+cudaError_t launch_bf16(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream) {
+  return launch_any<false>(tm_k, tm_v, a, stream);
+}
 
 }  // namespace prompt
 }  // namespace engram
