@@ -251,6 +251,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(is));
   return is != 0;
 }
+// (the four warpgroups' shares come to what the block is launched with: 2 * 168 + 2 * 88 = 4 * 128 a thread)
 template <int kRegs>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
@@ -265,7 +266,7 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
                "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
                : "memory");
 }
-// mbar_wait without a call: a function call's registers do not go together with setmaxnreg
+// mbar_wait without a call, which would cost the softmax warps their registers
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = clock64();
@@ -302,7 +303,7 @@ struct Ctl {
   uint64_t seg_full[2], seg_empty[2];
   uint64_t drained;
   Segment seg[2];
-  uint32_t live[kMeta][4];                            // which keys of a tile are there
+  alignas(16) uint32_t live[kMeta][4];                // which keys of a tile are there
   uint32_t v_bad[kMeta][kHelpers][4];                 // keys whose values are not all finite (in tiles that some row sees partly)
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -312,6 +313,24 @@ static_assert(smem_bytes(false) <= kSmemBudget && smem_bytes(true) <= kSmemBudge
 constexpr int kSegReaders = 8 + 1 + 1 + kHelpers;
 
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+// ---- two values at once; the largest of three ------------------------------------------------------------------
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // 16-byte piece c of row r in blocks of 128-byte rows, 128B swizzle
 __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)((c >> 3) * kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
 
@@ -401,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    more_registers<184>();
+    more_registers<168>();
     const int tile = warp >> 2, wl = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     const uint32_t o_t = lanes + kOCol + (uint32_t)(tile * 128);
@@ -423,90 +442,130 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         const float slope = kForm && p.form.slopes != nullptr && valid ? p.form.slopes[s.head * G + g] * 1.44269504f : 0.f;
         float m = -INFINITY, l = 0.f;
-        for (int n = 0; n < s.tiles; ++n) {
-          const int buf = s.nt == 2 ? tile : n & 1;
-          const uint32_t nth = used[buf] + (s.nt == 2 ? n : n >> 1);
+        // Tiles [whole_from, whole_to) are seen whole by every row of the warp, tiles [plain_from, plain_to) by every row of
+        // the pair that sees any
+        const int T = s.tiles, nt = s.nt, first_key = s.key0;
+        const int whole_from = __reduce_max_sync(0xFFFFFFFFu, lo > first_key ? (lo - first_key + kKeys - 1) / kKeys : 0);
+        const int whole_to = __reduce_min_sync(0xFFFFFFFFu, hi > first_key ? (hi - first_key) / kKeys : 0);
+        const int plain_from = s.max_lo > first_key ? (s.max_lo - first_key + kKeys - 1) / kKeys : 0;
+        const int plain_to = s.min_hi > first_key ? (s.min_hi - first_key) / kKeys : 0;
+        uint32_t nth = used[nt == 2 ? tile : 0], other = used[1];
+        for (int n = 0; n < T; ++n) {
+          const int buf = nt == 2 ? tile : n & 1;
           const uint32_t s_t = lanes + (uint32_t)(buf * 128);
           const uint32_t kn = keys_n + n;
-          const int key0 = s.key0 + n * kKeys;
-          if (!wait_warp(ctl->k_meta[kn % kMeta], kn / kMeta) || !wait_warp(ctl->s_full[buf], nth)) { ok = false; break; }
+          const int key0 = first_key + n * kKeys;
+          // what can be done before the scores are there: the softmax's latency is what the tensor cores wait for
+          if (!wait_warp(ctl->k_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
+          const uint4 live = *reinterpret_cast<const uint4*>(ctl->live[kn % kMeta]);
+          const bool full = n >= whole_from && n < whole_to && (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu;
+          if (nt == 2 || buf == 0 ? !wait_warp(ctl->s_full[buf], nth++) : !wait_warp(ctl->s_full[1], other++)) { ok = false; break; }
           tc_fence_after();
-          float x[128];
+          // Chunks of 32 keys, each requested while the one before is computed. Their exponentials are formed with the
+          // maximum so far: o, the sum and P are in units of 2^m, m a whole number that follows the true maximum only when
+          // that is 2^8 beyond it, which hardly ever happens after the first tile. (A loop of two chunks: unrolled over a
+          // whole tile, the code alone cost a third of the time, in instruction fetches.)
+          float xa[32], xb[32];
+          auto chunk = [&](float (&x)[32], int c) {
+            if (kForm) {
+              const float back = (float)(pos - key0 - 32 * c);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, x + 32 * c);
-          uint32_t mask[4];
-          uint32_t all = 0xFFFFFFFFu;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            mask[w] = *(volatile uint32_t*)&ctl->live[kn % kMeta][w] & bits_below(hi - key0 - 32 * w) & ~bits_below(lo - key0 - 32 * w);
-            all &= mask[w];
-          }
-          const bool full = __all_sync(0xFFFFFFFFu, all == 0xFFFFFFFFu);
-          tmem_ld_wait();
-          hold(x);
-          if (kForm) {
-            const float back = (float)(pos - key0);
-#pragma unroll
-            for (int j = 0; j < 128; ++j) {
-              float y = x[j] * p.scale_log2;
-              if (p.form.cap2 > 0.f) y = capped(y, p.form.cap2, p.form.cap_inv);
-              x[j] = fmaf(-slope, fabsf(back - (float)j), y);
-            }
-          }
-          if (!full) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (!((mask[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (!kForm) top *= p.scale_log2;
-          // o stays in units of 2^m until the maximum has grown by 8: weights up to 2^8, and hardly ever a pass over o
-          const bool grown = top > m + 8.f;
-          if (__any_sync(0xFFFFFFFFu, grown)) {
-            const float to = grown ? top : m;
-            const float alpha = grown ? ex2(m - to) : 1.f;
-            m = to;
-            l *= alpha;
-            if (n > 0) {
-              if (s.nt == 1 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
-              tc_fence_after();
-              for (int d = 0; d < D; d += 16) {
-                float y[16];
-                tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
-                tmem_ld_wait();
-                hold(y);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] *= alpha;
-                tmem_st16(o_t + d, reinterpret_cast<const uint32_t*>(y));
+              for (int j = 0; j < 32; ++j) {
+                float y = x[j] * p.scale_log2;
+                if (p.form.cap2 > 0.f) y = capped(y, p.form.cap2, p.form.cap_inv);
+                x[j] = fmaf(-slope, fabsf(back - (float)j), y);
               }
             }
-          }
-          const float base = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            if (!full) {
+              const uint32_t word = c == 0 ? live.x : c == 1 ? live.y : c == 2 ? live.z : live.w;
+              const uint32_t sees = word & bits_below(hi - key0 - 32 * c) & ~bits_below(lo - key0 - 32 * c);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float x0 = x[32 * c + 2 * j], x1 = x[32 * c + 2 * j + 1];
-              const float p0 = ex2(kForm ? x0 - base : fmaf(x0, p.scale_log2, -base));
-              const float p1 = ex2(kForm ? x1 - base : fmaf(x1, p.scale_log2, -base));
-              sum[j & 1] += p0;
-              sum[2 + (j & 1)] += p1;
-              w[j] = pack_bf16(p0, p1);
+              for (int j = 0; j < 32; ++j)
+                if (!((sees >> j) & 1u)) x[j] = -INFINITY;
             }
-            tmem_st16(s_t + 16 * c, w);
+            float mx[2] = {max3(x[0], x[2], x[4]), max3(x[1], x[3], x[5])};
+#pragma unroll
+            for (int j = 6; j < 30; j += 4) {
+              mx[0] = max3(mx[0], x[j], x[j + 2]);
+              mx[1] = max3(mx[1], x[j + 1], x[j + 3]);
+            }
+            float top = fmaxf(max3(mx[0], mx[1], x[30]), x[31]);
+            if (!kForm) top *= p.scale_log2;
+            uint32_t w[16];
+            float2 sum[2];
+            while (true) {
+              const float base = m == -INFINITY ? 0.f : m;
+              const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
+              sum[0] = sum[1] = {0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 xx = {x[2 * j], x[2 * j + 1]};
+                const float2 y = kForm ? add2(xx, base2) : fma2(xx, scale2, base2);
+                const float2 e = {ex2(y.x), ex2(y.y)};
+                sum[j & 1] = add2(sum[j & 1], e);
+                w[j] = pack_bf16(e.x, e.y);
+              }
+              const bool grown = top > m + 8.f;
+              if (!__any_sync(0xFFFFFFFFu, grown)) break;
+              const float to = grown ? ceilf(top) : m;
+              const float alpha = grown ? ex2(m - to) : 1.f;   // a power of two: exact, also for P
+              m = to;
+              l *= alpha;
+              if (n > 0) {
+                if (nt == 1 && !wait_warp(ctl->o_done, dones + n - 1)) return false;
+                tc_fence_after();
+                for (int d = 0; d < D; d += 16) {
+                  float y[16];
+                  tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+                  tmem_ld_wait();
+                  hold(y);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) y[e] *= alpha;
+                  tmem_st16(o_t + d, reinterpret_cast<const uint32_t*>(y));
+                }
+              }
+              if (c > 0) {
+                tmem_st_wait();                       // this tile's P so far
+                const __nv_bfloat162 by = __float2bfloat162_rn(alpha);
+                for (int d = 0; d < 16 * c; d += 16) {
+                  float y[16];
+                  tmem_ld16(s_t + d, reinterpret_cast<uint32_t*>(y));
+                  tmem_ld_wait();
+                  hold(y);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    __nv_bfloat162 z = *reinterpret_cast<__nv_bfloat162*>(&y[e]);
+                    z = __hmul2(z, by);
+                    y[e] = *reinterpret_cast<float*>(&z);
+                  }
+                  tmem_st16(s_t + d, reinterpret_cast<const uint32_t*>(y));
+                }
+              }
+            }
+            tmem_st16(s_t + 16 * c, w);               // over scores that have been read
+            const float2 sums = add2(sum[0], sum[1]);
+            l += sums.x + sums.y;
+            return true;
+          };
+          tmem_ld32(s_t, xa);
+#pragma unroll 1
+          for (int c = 0; ok && c < 4; c += 2) {
+            tmem_ld_wait();
+            hold(xa);
+            tmem_ld32(s_t + 32 * (c + 1), xb);
+            ok = chunk(xa, c);
+            tmem_ld_wait();
+            hold(xb);
+            if (c == 0) tmem_ld32(s_t + 64, xa);
+            ok = ok && chunk(xb, c + 1);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          if (!ok) break;
           tmem_st_wait();
-          if (partly_seen(s, n)) {
+          if (n < plain_from || n >= plain_to) {
             // some row does not see all of the tile's keys: values that are not finite must not reach it
             if (!wait_warp(ctl->v_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
             if (not_finite(kn)) {
-              if (s.nt == 1 && n > 0 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
+              if (nt == 1 && n > 0 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
               tc_fence_after();
               for (int d = 0; d < D; d += 16) {
                 float y[16];
@@ -519,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                   for (int e = 0; e < 16; ++e) y[e] = 0.f;
                 }
                 for (int w = 0; w < 4; ++w) {
-                  const uint32_t sees = w == 0 ? mask[0] : w == 1 ? mask[1] : w == 2 ? mask[2] : mask[3];
+                  const uint32_t sees = ctl->live[kn % kMeta][w] & bits_below(hi - key0 - 32 * w) & ~bits_below(lo - key0 - 32 * w);
                   for (uint32_t left = bad_keys(kn, w); left != 0; left &= left - 1) {
                     const int j = 32 * w + __ffs(left) - 1;
                     if (!__any_sync(0xFFFFFFFFu, (sees >> (j & 31)) & 1u)) continue;   // (past the sequence, maybe: no page)
@@ -613,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       ++seg_n;
     }
   } else {
-    fewer_registers<72>();
+    fewer_registers<88>();
     if (warp == 8) {
       // -------------------------------------------------------------- MMA
       // The warp stays together: every lane waits, one issues. (Uniform registers hold the descriptors.)
@@ -807,40 +866,65 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const Segment& s = ctl->seg[seg_n & 1];
         // keys run `lead` tiles ahead of values
         const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
-        // pages of keys 32 j + lane of the next values' tile and those behind it, requested ahead
-        int pg[3][4];
-        auto request = [&](int n, int (&to)[4]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int pos = s.key0 + n * kKeys + 32 * j + lane;
-            to[j] = -1;
-            if (n < T && pos < s.hull_hi) {
-              to[j] = p.table[(int64_t)s.b * p.table_stride + (int)fast_div((uint32_t)pos, p.cache.div_page)];
-              if (to[j] < 0 || to[j] >= p.cache.num_pages) {
-                to[j] = -1;
-                if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
-              }
-            }
+        // A lane has a box (of 64 or more lanes have the same): lane / 2, and its first or second block of 64 values. Its
+        // page and its first place there, for the next values' tile and those behind it, looked up ahead. (Rows one by
+        // one: the pages are only looked at, four keys to a lane.)
+        const int per_box = a.box > 0 ? a.box : 4, at = (lane >> (a.box > 0 ? 1 : 0)) * per_box;
+        int pg[3], pl[3];
+        auto request = [&](int n, int& page, int& place) {   // (what the load brings is looked at when the tile's turn comes)
+          const int first = s.key0 + n * kKeys + at;
+          const int i = (int)fast_div((uint32_t)first, p.cache.div_page);
+          place = first - i * p.cache.page_size;
+          page = -1;
+          if (a.box > 0 && n < T && at < kKeys && first < s.hull_hi) {
+            page = p.table[(int64_t)s.b * p.table_stride + i];
+            if (page < 0) page = 0x7FFFFFFF;
           }
         };
-        request(0, pg[0]);
-        request(1, pg[1]);
-        request(2, pg[2]);
+        // word `lane` (0..3) of which keys of tile n are there, and the page made -1 if it is not in the cache
+        auto look = [&](int n, int& page) {
+          uint32_t live = 0;
+          if (a.box > 0) {
+            if (page >= p.cache.num_pages) {
+              page = -1;
+              if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
+            }
+            const uint32_t boxes = __ballot_sync(0xFFFFFFFFu, page >= 0);   // box by box, two lanes apart
+            for (int k = 0; k < 32; k += per_box) {
+              const int box = (32 * (lane & 3) + k) / per_box;
+              if ((boxes >> (2 * box)) & 1u) live |= (per_box >= 32 ? 0xFFFFFFFFu : (1u << per_box) - 1u) << k;
+            }
+          } else {
+            uint32_t there = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int pos = s.key0 + n * kKeys + at + k;
+              if (pos < s.hull_hi) {
+                const int y = p.table[(int64_t)s.b * p.table_stride + (int)fast_div((uint32_t)pos, p.cache.div_page)];
+                if (y >= 0 && y < p.cache.num_pages)
+                  there |= 1u << k;
+                else if (p.err != nullptr)
+                  atomicOr(p.err, ENGRAM_ERR_PAGE);
+              }
+            }
+            for (int k = 0; k < 8; ++k) live |= __shfl_sync(0xFFFFFFFFu, there, (lane & 3) * 8 + k) << (4 * k);
+          }
+          return live;
+        };
+        request(0, pg[0], pl[0]);
+        request(1, pg[1], pl[1]);
+        request(2, pg[2], pl[2]);
         int next_k = 0, next_v = 0;
         while (ok && next_v < T) {
           const bool values = next_k == min(T, next_v + lead);
-          const int n = values ? next_v : next_k;
-          const int first = s.key0 + n * kKeys;
-          int page[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) page[j] = n == next_v ? pg[0][j] : pg[1][j];
+          const bool now = values || next_k == next_v;
+          int page = now ? pg[0] : pg[1];
+          const int place = now ? pl[0] : pl[1];
           if (!values) {
-            const int m = (kn + n) % kMeta;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t live = __ballot_sync(0xFFFFFFFFu, page[j] >= 0);
-              if (lane == j) ctl->live[m][j] = live;
-            }
+            const int m = (kn + next_k) % kMeta;
+            const uint32_t live = look(next_k, page);
+            (now ? pg[0] : pg[1]) = page;
+            if (lane < 4) ctl->live[m][lane] = live;
             __syncwarp();
             if (lane == 0) arrive(ctl->k_meta[m]);
           }
@@ -851,30 +935,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               const uint32_t dst = kFp8 ? stages + (uint32_t)(stage * kStageBytes) : ring + (uint32_t)(slot * kSlotBytes);
               const uint32_t bar = smem_u32(kFp8 ? &ctl->st_full[stage] : &ctl->full[slot]);
               if (lane == 0) mbar_expect_tx(bar, (uint32_t)(blocks * kBlockBytes));
-              // a lane per box of `box` keys by 64 values (128 codes); a page that is not there reads as zeros
-              const int box = blocks == 2 ? lane >> 1 : lane, at = box * a.box;
-              int pb = -1;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int y = __shfl_sync(0xFFFFFFFFu, page[j], at & 31);
-                if (at >> 5 == j) pb = y;
-              }
               __syncwarp();
-              if (at < kKeys) {
-                const int pos = first + at, place = pos - (int)fast_div((uint32_t)pos, p.cache.div_page) * p.cache.page_size;
-                const int block = blocks == 2 ? lane & 1 : 0;
-                tma_load_4d(dst + (uint32_t)(block * kBlockBytes + at * 128), values ? &tm_v : &tm_k, bar, part * 128 + block * 64, place, s.head, pb);
-              }
+              // a page that is not there reads as zeros
+              if (at < kKeys && (lane & 1) < blocks)
+                tma_load_4d(dst + (uint32_t)((lane & 1) * kBlockBytes + at * 128), values ? &tm_v : &tm_k, bar, part * 128 + (lane & 1) * 64, place, s.head, page);
               if (kFp8) {
-                const uint8_t* from = (values ? p.cache.vs : p.cache.ks) + s.head * p.cache.shead_b + 4 * part;
+                // scale words: keys 4 * lane .. + 3, all in one box
+                const int key = 4 * lane, from_lane = 2 * (key / per_box);
+                const int pb = __shfl_sync(0xFFFFFFFFu, page, from_lane), first_place = __shfl_sync(0xFFFFFFFFu, place, from_lane) + key % per_box;
+                const uint8_t* from = (values ? p.cache.vs : p.cache.ks) + s.head * p.cache.shead_b + 4 * part +
+                    (pb >= 0 ? (int64_t)((uint64_t)(uint32_t)pb * p.cache.spage_u + (uint64_t)(uint32_t)first_place * p.cache.stok_u) << 2 : 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int pos = first + 32 * j + lane, place = pos - (int)fast_div((uint32_t)pos, p.cache.div_page) * p.cache.page_size;
-                  const bool live = page[j] >= 0;
-                  const int64_t off = live ? (int64_t)((uint64_t)(uint32_t)page[j] * p.cache.spage_u + (uint64_t)(uint32_t)place * p.cache.stok_u) << 2 : 0;
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + kBlockBytes + (uint32_t)(32 * j + lane) * 4), "l"(from + off),
-                               "r"(live ? 4 : 0) : "memory");
-                }
+                for (int k = 0; k < 4; ++k)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + kBlockBytes + (uint32_t)(key + k) * 4),
+                               "l"(from + (pb >= 0 ? k * p.cache.stok_b : 0)), "r"(pb >= 0 ? 4 : 0) : "memory");
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
               }
             }
@@ -887,12 +961,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           if (values) {
             ++next_v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              pg[0][j] = pg[1][j];
-              pg[1][j] = pg[2][j];
-            }
-            request(next_v + 2, pg[2]);
+            pg[0] = pg[1];
+            pl[0] = pl[1];
+            pg[1] = pg[2];
+            pl[1] = pl[2];
+            request(next_v + 2, pg[2], pl[2]);
           } else {
             ++next_k;
           }
