@@ -458,62 +458,72 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           // what can be done before the scores are there: the softmax's latency is what the tensor cores wait for
           if (!wait_warp(ctl->k_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
           const uint4 live = *reinterpret_cast<const uint4*>(ctl->live[kn % kMeta]);
-          const bool full = n >= whole_from && n < whole_to && (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu;
+          const bool full = __all_sync(0xFFFFFFFFu, n >= whole_from && n < whole_to && (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu);
           if (nt == 2 || buf == 0 ? !wait_warp(ctl->s_full[buf], nth++) : !wait_warp(ctl->s_full[1], other++)) { ok = false; break; }
           tc_fence_after();
-          // Chunks of 32 keys, each requested while the one before is computed. Their exponentials are formed with the
-          // maximum so far: o, the sum and P are in units of 2^m, m a whole number that follows the true maximum only when
-          // that is 2^8 beyond it, which hardly ever happens after the first tile. (A loop of two chunks: unrolled over a
-          // whole tile, the code alone cost a third of the time, in instruction fetches.)
-          float xa[32], xb[32];
-          auto chunk = [&](float (&x)[32], int c) {
-            if (kForm) {
-              const float back = (float)(pos - key0 - 32 * c);
+          if (!kForm && !full) {
+            // masked before: hardly any tile is, and the loop below stays small
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 16) {
+              float y[16];
+              tmem_ld16(s_t + c, reinterpret_cast<uint32_t*>(y));
+              const uint32_t sees = (ctl->live[kn % kMeta][c >> 5] >> (c & 16)) & bits_below(hi - key0 - c) & ~bits_below(lo - key0 - c);
+              tmem_ld_wait();
+              hold(y);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              for (int e = 0; e < 16; ++e)
+                if (!((sees >> e) & 1u)) y[e] = -INFINITY;
+              tmem_st16(s_t + c, reinterpret_cast<const uint32_t*>(y));
+            }
+            tmem_st_wait();
+          }
+          // Half a tile at a time, in a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
+          // exponentials are formed with the maximum so far: o, the sum and P are in units of 2^m, m a whole number that
+          // follows the true maximum only when that is 2^8 beyond it, which hardly ever happens after the first tile.
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 64) {
+            float x[64];
+            tmem_ld32(s_t + c, x);
+            tmem_ld32(s_t + c + 32, x + 32);
+            tmem_ld_wait();
+            hold(x);
+            if (kForm) {
+              const float back = (float)(pos - key0 - c);
+#pragma unroll
+              for (int j = 0; j < 64; ++j) {
                 float y = x[j] * p.scale_log2;
                 if (p.form.cap2 > 0.f) y = capped(y, p.form.cap2, p.form.cap_inv);
                 x[j] = fmaf(-slope, fabsf(back - (float)j), y);
               }
-            }
-            if (!full) {
-              const uint32_t word = c == 0 ? live.x : c == 1 ? live.y : c == 2 ? live.z : live.w;
-              const uint32_t sees = word & bits_below(hi - key0 - 32 * c) & ~bits_below(lo - key0 - 32 * c);
+              if (!full) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((sees >> j) & 1u)) x[j] = -INFINITY;
-            }
-            float mx[2] = {max3(x[0], x[2], x[4]), max3(x[1], x[3], x[5])};
+                for (int w = 0; w < 2; ++w) {
+                  const uint32_t sees = ctl->live[kn % kMeta][c / 32 + w] & bits_below(hi - key0 - c - 32 * w) & ~bits_below(lo - key0 - c - 32 * w);
 #pragma unroll
-            for (int j = 6; j < 30; j += 4) {
-              mx[0] = max3(mx[0], x[j], x[j + 2]);
-              mx[1] = max3(mx[1], x[j + 1], x[j + 3]);
-            }
-            float top = fmaxf(max3(mx[0], mx[1], x[30]), x[31]);
-            if (!kForm) top *= p.scale_log2;
-            uint32_t w[16];
-            float2 sum[2];
-            while (true) {
-              const float base = m == -INFINITY ? 0.f : m;
-              const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
-              sum[0] = sum[1] = {0.f, 0.f};
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 xx = {x[2 * j], x[2 * j + 1]};
-                const float2 y = kForm ? add2(xx, base2) : fma2(xx, scale2, base2);
-                const float2 e = {ex2(y.x), ex2(y.y)};
-                sum[j & 1] = add2(sum[j & 1], e);
-                w[j] = pack_bf16(e.x, e.y);
+                  for (int j = 0; j < 32; ++j)
+                    if (!((sees >> j) & 1u)) x[32 * w + j] = -INFINITY;
+                }
               }
-              const bool grown = top > m + 8.f;
-              if (!__any_sync(0xFFFFFFFFu, grown)) break;
+            }
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(x[e], x[4 + e], x[8 + e]);
+#pragma unroll
+            for (int j = 12; j < 60; j += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+            float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[60], max3(x[61], x[62], x[63])));
+            if (!kForm) top *= p.scale_log2;
+            const bool grown = top > m + 8.f;
+            if (__any_sync(0xFFFFFFFFu, grown)) {
               const float to = grown ? ceilf(top) : m;
-              const float alpha = grown ? ex2(m - to) : 1.f;   // a power of two: exact, also for P
+              const float alpha = grown ? ex2(m - to) : 1.f;  // a power of two: exact, also for P
               m = to;
               l *= alpha;
               if (n > 0) {
-                if (nt == 1 && !wait_warp(ctl->o_done, dones + n - 1)) return false;
+                if (nt == 1 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
                 tc_fence_after();
+#pragma unroll 1
                 for (int d = 0; d < D; d += 16) {
                   float y[16];
                   tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
@@ -527,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               if (c > 0) {
                 tmem_st_wait();                       // this tile's P so far
                 const __nv_bfloat162 by = __float2bfloat162_rn(alpha);
-                for (int d = 0; d < 16 * c; d += 16) {
+#pragma unroll 1
+                for (int d = 0; d < 32; d += 16) {
                   float y[16];
                   tmem_ld16(s_t + d, reinterpret_cast<uint32_t*>(y));
                   tmem_ld_wait();
@@ -542,22 +553,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
               }
             }
-            tmem_st16(s_t + 16 * c, w);               // over scores that have been read
+            const float base = m == -INFINITY ? 0.f : m;
+            const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 xx = {x[32 * h + 2 * j], x[32 * h + 2 * j + 1]};
+                const float2 y = kForm ? add2(xx, base2) : fma2(xx, scale2, base2);
+                const float2 e = {ex2(y.x), ex2(y.y)};
+                sum[j & 1] = add2(sum[j & 1], e);
+                w[j] = pack_bf16(e.x, e.y);
+              }
+              tmem_st16(s_t + c / 2 + 16 * h, w);     // over scores that have been read
+            }
             const float2 sums = add2(sum[0], sum[1]);
             l += sums.x + sums.y;
-            return true;
-          };
-          tmem_ld32(s_t, xa);
-#pragma unroll 1
-          for (int c = 0; ok && c < 4; c += 2) {
-            tmem_ld_wait();
-            hold(xa);
-            tmem_ld32(s_t + 32 * (c + 1), xb);
-            ok = chunk(xa, c);
-            tmem_ld_wait();
-            hold(xb);
-            if (c == 0) tmem_ld32(s_t + 64, xa);
-            ok = ok && chunk(xb, c + 1);
           }
           if (!ok) break;
           tmem_st_wait();
@@ -859,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       __syncwarp();
     } else if (warp == 12) {
       // -------------------------------------------------------------- pages, and boxes of K and V
+      const bool leader = elect_one();
       int slot = 0, stage = 0;
       uint32_t phase = 0, st_phase = 0, kn = 0;
       bool ok = true;
@@ -866,84 +880,87 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const Segment& s = ctl->seg[seg_n & 1];
         // keys run `lead` tiles ahead of values
         const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
-        // A lane has a box (of 64 or more lanes have the same): lane / 2, and its first or second block of 64 values. Its
-        // page and its first place there, for the next values' tile and those behind it, looked up ahead. (Rows one by
-        // one: the pages are only looked at, four keys to a lane.)
-        const int per_box = a.box > 0 ? a.box : 4, at = (lane >> (a.box > 0 ? 1 : 0)) * per_box;
-        int pg[3], pl[3];
-        auto request = [&](int n, int& page, int& place) {   // (what the load brings is looked at when the tile's turn comes)
-          const int first = s.key0 + n * kKeys + at;
-          const int i = (int)fast_div((uint32_t)first, p.cache.div_page);
-          place = first - i * p.cache.page_size;
+        const int head = s.head, b = s.b, first_key = s.key0, hull_hi = s.hull_hi;
+        // Pages and places of 32 boxes at a time, a lane each: this loop feeds the tensor cores, so looking up and dividing
+        // is done once for many tiles. Values are in the older batch, keys in that or the next (a batch is two tiles or more).
+        // Rows one by one: the pages are only looked at, key by key; a "box" is a key then, a batch a quarter of a tile.
+        const int box_log = a.box > 0 ? 31 - __clz(a.box) : 0, batch_log = 5 + box_log - 7;   // tiles in a batch, log 2
+        int pg[2] = {-1, -1}, pl[2] = {0, 0};
+        uint32_t there[2] = {0, 0};
+        auto request = [&](int batch, int& page, int& place) {
+          const int pos = first_key + (((batch << 5) + lane) << box_log);
+          const int i = (int)fast_div((uint32_t)pos, p.cache.div_page);
           page = -1;
-          if (a.box > 0 && n < T && at < kKeys && first < s.hull_hi) {
-            page = p.table[(int64_t)s.b * p.table_stride + i];
-            if (page < 0) page = 0x7FFFFFFF;
-          }
-        };
-        // word `lane` (0..3) of which keys of tile n are there, and the page made -1 if it is not in the cache
-        auto look = [&](int n, int& page) {
-          uint32_t live = 0;
-          if (a.box > 0) {
-            if (page >= p.cache.num_pages) {
+          place = pos - i * p.cache.page_size;
+          if (pos < hull_hi && pos >= first_key) {     // (past 2^31 it would be negative)
+            page = p.table[(int64_t)b * p.table_stride + i];
+            if (page < 0 || page >= p.cache.num_pages) {
               page = -1;
               if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
             }
-            const uint32_t boxes = __ballot_sync(0xFFFFFFFFu, page >= 0);   // box by box, two lanes apart
-            for (int k = 0; k < 32; k += per_box) {
-              const int box = (32 * (lane & 3) + k) / per_box;
-              if ((boxes >> (2 * box)) & 1u) live |= (per_box >= 32 ? 0xFFFFFFFFu : (1u << per_box) - 1u) << k;
-            }
-          } else {
-            uint32_t there = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int pos = s.key0 + n * kKeys + at + k;
-              if (pos < s.hull_hi) {
-                const int y = p.table[(int64_t)s.b * p.table_stride + (int)fast_div((uint32_t)pos, p.cache.div_page)];
-                if (y >= 0 && y < p.cache.num_pages)
-                  there |= 1u << k;
-                else if (p.err != nullptr)
-                  atomicOr(p.err, ENGRAM_ERR_PAGE);
-              }
-            }
-            for (int k = 0; k < 8; ++k) live |= __shfl_sync(0xFFFFFFFFu, there, (lane & 3) * 8 + k) << (4 * k);
           }
-          return live;
         };
-        request(0, pg[0], pl[0]);
-        request(1, pg[1], pl[1]);
-        request(2, pg[2], pl[2]);
+        int batch = 0;                                // of the values
+        if (a.box > 0) {
+          request(0, pg[0], pl[0]);
+          request(1, pg[1], pl[1]);
+          there[0] = __ballot_sync(0xFFFFFFFFu, pg[0] >= 0);
+          there[1] = __ballot_sync(0xFFFFFFFFu, pg[1] >= 0);
+        }
+        const int boxes = kKeys >> box_log;           // of a tile
         int next_k = 0, next_v = 0;
         while (ok && next_v < T) {
           const bool values = next_k == min(T, next_v + lead);
-          const bool now = values || next_k == next_v;
-          int page = now ? pg[0] : pg[1];
-          const int place = now ? pl[0] : pl[1];
+          const int n = values ? next_v : next_k;
+          const bool next_batch = a.box > 0 && (n >> batch_log) != batch;
+          const int page = next_batch ? pg[1] : pg[0], place = next_batch ? pl[1] : pl[0];
+          const int at = (n * boxes) & 31;            // the tile's first box in its batch
           if (!values) {
-            const int m = (kn + next_k) % kMeta;
-            const uint32_t live = look(next_k, page);
-            (now ? pg[0] : pg[1]) = page;
-            if (lane < 4) ctl->live[m][lane] = live;
+            const int m = (kn + n) % kMeta;
+            if (a.box > 0) {
+              const uint32_t all = boxes == 16 ? 0xFFFFu : (1u << boxes) - 1u, has = ((next_batch ? there[1] : there[0]) >> at) & all;
+              if (lane < 4) {
+                uint32_t live = has == all ? 0xFFFFFFFFu : 0u;
+                if (has != all)
+                  for (int k = 0; k < 32; k += 1 << min(box_log, 5))
+                    if ((has >> ((32 * lane + k) >> box_log)) & 1u) live |= (box_log >= 5 ? 0xFFFFFFFFu : (1u << (1 << box_log)) - 1u) << k;
+                ctl->live[m][lane] = live;
+              }
+            } else {
+              for (int w = 0; w < 4; ++w) {
+                int y, z;
+                request(n * 4 + w, y, z);
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, y >= 0);
+                if (lane == w) ctl->live[m][w] = live;
+              }
+            }
             __syncwarp();
             if (lane == 0) arrive(ctl->k_meta[m]);
           }
           for (int part = 0; part < kSlotsPerTile; ++part) {
             if (kFp8 && a.box > 0 ? !wait_warp(ctl->st_empty[stage], st_phase ^ 1u) : !wait_warp(ctl->empty[slot], phase ^ 1u)) { ok = false; break; }
             if (a.box > 0) {
-              const int blocks = kFp8 ? 1 : (min(128, D - part * 128) + 63) / 64;
+              const bool two = !kFp8 && D - part * 128 > 64;   // blocks of 64 values
               const uint32_t dst = kFp8 ? stages + (uint32_t)(stage * kStageBytes) : ring + (uint32_t)(slot * kSlotBytes);
               const uint32_t bar = smem_u32(kFp8 ? &ctl->st_full[stage] : &ctl->full[slot]);
-              if (lane == 0) mbar_expect_tx(bar, (uint32_t)(blocks * kBlockBytes));
-              __syncwarp();
-              // a page that is not there reads as zeros
-              if (at < kKeys && (lane & 1) < blocks)
-                tma_load_4d(dst + (uint32_t)((lane & 1) * kBlockBytes + at * 128), values ? &tm_v : &tm_k, bar, part * 128 + (lane & 1) * 64, place, s.head, page);
+              if (leader) mbar_expect_tx(bar, two ? 2 * kBlockBytes : kBlockBytes);
+              // One lane requests all boxes (lanes of their own would take turns all the same, at a higher price). A page that
+              // is not there reads as zeros.
+              const CUtensorMap* map = values ? &tm_v : &tm_k;
+              for (int k = 0; k < boxes; ++k) {
+                const int y = __shfl_sync(0xFFFFFFFFu, place, at + k), z = __shfl_sync(0xFFFFFFFFu, page, at + k);
+                const uint32_t to = dst + (uint32_t)((k << box_log) * 128);
+                if (leader) {
+                  tma_load_4d(to, map, bar, part * 128, y, head, z);
+                  if (two) tma_load_4d(to + kBlockBytes, map, bar, part * 128 + 64, y, head, z);
+                }
+              }
               if (kFp8) {
                 // scale words: keys 4 * lane .. + 3, all in one box
-                const int key = 4 * lane, from_lane = 2 * (key / per_box);
-                const int pb = __shfl_sync(0xFFFFFFFFu, page, from_lane), first_place = __shfl_sync(0xFFFFFFFFu, place, from_lane) + key % per_box;
-                const uint8_t* from = (values ? p.cache.vs : p.cache.ks) + s.head * p.cache.shead_b + 4 * part +
+                const int key = 4 * lane, from_lane = at + (key >> box_log);
+                const int pb = __shfl_sync(0xFFFFFFFFu, page, from_lane);
+                const int first_place = __shfl_sync(0xFFFFFFFFu, place, from_lane) + (key & ((1 << box_log) - 1));
+                const uint8_t* from = (values ? p.cache.vs : p.cache.ks) + head * p.cache.shead_b + 4 * part +
                     (pb >= 0 ? (int64_t)((uint64_t)(uint32_t)pb * p.cache.spage_u + (uint64_t)(uint32_t)first_place * p.cache.stok_u) << 2 : 0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -961,11 +978,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           if (values) {
             ++next_v;
-            pg[0] = pg[1];
-            pl[0] = pl[1];
-            pg[1] = pg[2];
-            pl[1] = pl[2];
-            request(next_v + 2, pg[2], pl[2]);
+            if (a.box > 0 && (next_v >> batch_log) != batch && next_v < T) {
+              ++batch;
+              pg[0] = pg[1];
+              pl[0] = pl[1];
+              there[0] = there[1];
+              request(batch + 1, pg[1], pl[1]);
+              there[1] = __ballot_sync(0xFFFFFFFFu, pg[1] >= 0);
+            }
           } else {
             ++next_k;
           }
