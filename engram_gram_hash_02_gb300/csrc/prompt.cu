@@ -167,9 +167,10 @@ int box_of(const CacheRef& c) {
   return box >= 8 && c.num_pages > 0 ? box : 0;
 }
 
-// The cache's keys or values as [page][head][place][value], boxes of `box` tokens by 128 bytes: bf16 in the MMAs' swizzle,
-// codes as they are. False if the strides do not fit a tensor map.
-bool make_map_pages(CUtensorMap* m, const void* base, const PromptParams& p, int box) {
+// A tensor map with the values of a row innermost; an axis of one entry is never stepped along, whatever its stride says.
+// False if the strides do not fit one.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const int64_t* dims, const int64_t* strides_b,
+              const uint32_t* box, bool swizzle, int64_t row_b) {
   typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   static Encode fn = nullptr;
@@ -182,19 +183,36 @@ bool make_map_pages(CUtensorMap* m, const void* base, const PromptParams& p, int
       fn = reinterpret_cast<Encode>(f);
   });
   if (fn == nullptr) return false;
-  const CacheRef& c = p.cache;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)c.page_size, (cuuint64_t)p.Hk, (cuuint64_t)c.num_pages};
-  const int64_t row = (int64_t)p.D * (c.fp8 ? 1 : 2);
-  // an axis of one entry is never stepped along: any stride that a map takes
-  cuuint64_t strides[3] = {(cuuint64_t)c.tok_b, (cuuint64_t)c.head_b, (cuuint64_t)c.page_b};
-  for (int i = 0; i < 3; ++i) {
-    if (dims[i + 1] == 1) strides[i] = (cuuint64_t)row;
-    if (strides[i] == 0 || strides[i] >= (cuuint64_t)1 << 40) return false;
+  cuuint64_t n[4], step[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    n[i] = (cuuint64_t)dims[i];
+    b[i] = box[i];
+    if (i == 0) continue;
+    step[i - 1] = (cuuint64_t)(dims[i] == 1 ? row_b : strides_b[i - 1]);
+    if (step[i - 1] == 0 || step[i - 1] >= (cuuint64_t)1 << 40) return false;
   }
-  const cuuint32_t boxes[4] = {c.fp8 ? 128u : 64u, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
-  return fn(m, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes,
-            steps, CU_TENSOR_MAP_INTERLEAVE_NONE, c.fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), n, step, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// the cache's keys or values as [page][head][place][value], boxes of `box` tokens by 128 bytes: bf16 in the MMAs' swizzle,
+// codes as they are
+bool map_pages(CUtensorMap* m, const void* base, const PromptParams& p, int box) {
+  const CacheRef& c = p.cache;
+  const int64_t dims[4] = {p.D, c.page_size, p.Hk, c.num_pages}, strides[3] = {c.tok_b, c.head_b, c.page_b};
+  const uint32_t boxes[4] = {c.fp8 ? 128u : 64u, (uint32_t)box, 1, 1};
+  return make_map(m, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes, !c.fp8,
+                  (int64_t)p.D * (c.fp8 ? 1 : 2));
+}
+
+// queries as [token][head][value], a tile's worth of whole tokens to a box
+bool map_queries(CUtensorMap* m, const PromptParams& p) {
+  if (128 % p.G != 0) return false;
+  const int64_t dims[3] = {p.D, (int64_t)p.Hk * p.G, p.T}, strides[2] = {p.q.hs * 2, p.q.ts * 2};
+  const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)(128 / p.G)};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.q.data, dims, strides, box, true, (int64_t)p.D * 2);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -240,11 +258,12 @@ cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   // cut once or twice, and the last to arrive joins it.
   const int R = pair_rows(p.D);
   a.join = (p.T * p.G + R - 1) / R * p.Hk >= a.ctas;
-  CUtensorMap tm_k{}, tm_v{};
+  CUtensorMap tm_k{}, tm_v{}, tm_q{};
   a.box = box_of(p.cache);
-  if (a.box > 0 && !(make_map_pages(&tm_k, p.cache.k, p, a.box) && make_map_pages(&tm_v, p.cache.v, p, a.box))) a.box = 0;
+  if (a.box > 0 && !(map_pages(&tm_k, p.cache.k, p, a.box) && map_pages(&tm_v, p.cache.v, p, a.box))) a.box = 0;
+  a.q_box = map_queries(&tm_q, p);
   cudaError_t e = launch_k(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
-  if (e == cudaSuccess) e = p.cache.fp8 ? launch_fp8(tm_k, tm_v, a, stream) : launch_bf16(tm_k, tm_v, a, stream);
+  if (e == cudaSuccess) e = p.cache.fp8 ? launch_fp8(tm_k, tm_v, tm_q, a, stream) : launch_bf16(tm_k, tm_v, tm_q, a, stream);
   if (e == cudaSuccess && !a.join) e = launch_k(join_kernel, dim3((unsigned)a.ctas * 2), dim3(256), 0, stream, true, a);
   return e;
 }

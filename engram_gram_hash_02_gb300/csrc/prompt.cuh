@@ -39,7 +39,10 @@ namespace prompt {
 constexpr int kKeys = 128;                            // of a tile
 constexpr int kSlotBytes = 32768;                     // 128 keys of up to 128 values, as two blocks of 128-byte rows
 constexpr int kBlockBytes = 16384;
-__host__ __device__ constexpr int slots_of(bool fp8) { return fp8 ? 3 : 5; }
+__host__ __device__ constexpr int slots_of(bool fp8) { return fp8 ? 3 : 4; }
+// of a softmax warp: 32 rows of 32 values (FP8: 16, its stages leave no room for more) on their way out, in pieces of 16 bytes
+__host__ __device__ constexpr int staging_pieces(bool fp8) { return fp8 ? 2 : 4; }
+__host__ __device__ constexpr int staging_bytes(bool fp8) { return 32 * 16 * staging_pieces(fp8); }
 constexpr int kStages = 3;                            // FP8: of 128 codes and their scale word for each of 128 keys
 constexpr int kStageBytes = kBlockBytes + 512;
 constexpr int kQBytes = 65536;
@@ -86,6 +89,7 @@ struct Args {
   int32_t join;                                       // 1: the last warp to arrive joins a cut pair's rows
   int32_t ctas;
   int32_t box;                                        // tokens per TMA box, a power of two that divides a page (0: rows one by one)
+  int32_t q_box;                                      // 1: a tile is whole tokens, and Q comes as TMA boxes
   FastDiv div_g;
 };
 
@@ -261,6 +265,11 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
   asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
@@ -295,7 +304,7 @@ struct Segment {
   int32_t c_first, c_last;                            // CTAs of a cut pair
 };
 struct Ctl {
-  uint64_t full[5], empty[5];
+  uint64_t full[4], empty[4];
   uint64_t st_full[kStages], st_empty[kStages];
   uint64_t q_full, q_empty;
   uint64_t k_meta[kMeta], v_meta[kMeta];
@@ -308,7 +317,7 @@ struct Ctl {
   uint32_t tmem_base;
   int32_t abort_flag;
 };
-constexpr int smem_bytes(bool fp8) { return 1024 + kQBytes + slots_of(fp8) * kSlotBytes + (fp8 ? kStages * kStageBytes : 0) + (int)sizeof(Ctl); }
+constexpr int smem_bytes(bool fp8) { return 1024 + kQBytes + slots_of(fp8) * kSlotBytes + (fp8 ? kStages * kStageBytes : 0) + 8 * staging_bytes(fp8) + (int)sizeof(Ctl); }
 static_assert(smem_bytes(false) <= kSmemBudget && smem_bytes(true) <= kSmemBudget, "one CTA's shared memory");
 constexpr int kSegReaders = 8 + 1 + 1 + kHelpers;
 
@@ -338,7 +347,7 @@ __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)((c >
 // scale that is not positive
 template <bool kWide, bool kFp8, bool kForm>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                                                             const __grid_constant__ Args a) {
+                                                             const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
   const PromptParams& p = a.p;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -346,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t ring = q_smem + kQBytes;
   constexpr int kSlots = slots_of(kFp8);
   const uint32_t stages = ring + kSlots * kSlotBytes;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (stages + (kFp8 ? kStages * kStageBytes : 0) - raw));
+  const uint32_t staging = stages + (kFp8 ? kStages * kStageBytes : 0);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (staging + 8 * staging_bytes(kFp8) - raw));
   volatile int32_t* abort_flag = &ctl->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = p.D, G = p.G;
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(smem_u32(&ctl->st_full[s]), 1 + 32);  // the boxes, and every lane's scale words
       mbar_init(smem_u32(&ctl->st_empty[s]), kHelpers);
     }
-    mbar_init(smem_u32(&ctl->q_full), kHelpers);
+    mbar_init(smem_u32(&ctl->q_full), a.q_box ? 1 : kHelpers);
     mbar_init(smem_u32(&ctl->q_empty), 1);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(smem_u32(&ctl->k_meta[i]), 1);
@@ -478,8 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             tmem_st_wait();
           }
           // Half a tile at a time, in a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
-          // exponentials are formed with the maximum so far: o, the sum and P are in units of 2^m, m a whole number that
-          // follows the true maximum only when that is 2^8 beyond it, which hardly ever happens after the first tile.
+          // exponentials are formed with the maximum so far, while the half's own is found: o, the sum and P are in units of
+          // 2^m, m a whole number that follows the true maximum only when that is 2^8 beyond it, which hardly ever happens
+          // after the first tile; then the half is done again.
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 64) {
             float x[64];
@@ -515,6 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[60], max3(x[61], x[62], x[63])));
             if (!kForm) top *= p.scale_log2;
             const bool grown = top > m + 8.f;
+            const float base = m == -INFINITY ? 0.f : m;
+            const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 xx = {x[2 * j], x[2 * j + 1]};
+              const float2 y = kForm ? add2(xx, base2) : fma2(xx, scale2, base2);
+              const float2 e = {ex2(y.x), ex2(y.y)};
+              sum[j & 1] = add2(sum[j & 1], e);
+              w[j] = pack_bf16(e.x, e.y);
+            }
             if (__any_sync(0xFFFFFFFFu, grown)) {
               const float to = grown ? ceilf(top) : m;
               const float alpha = grown ? ex2(m - to) : 1.f;  // a power of two: exact, also for P
@@ -552,23 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                   tmem_st16(s_t + d, reinterpret_cast<const uint32_t*>(y));
                 }
               }
+              c -= 64;
+              continue;
             }
-            const float base = m == -INFINITY ? 0.f : m;
-            const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
-            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 xx = {x[32 * h + 2 * j], x[32 * h + 2 * j + 1]};
-                const float2 y = kForm ? add2(xx, base2) : fma2(xx, scale2, base2);
-                const float2 e = {ex2(y.x), ex2(y.y)};
-                sum[j & 1] = add2(sum[j & 1], e);
-                w[j] = pack_bf16(e.x, e.y);
-              }
-              tmem_st16(s_t + c / 2 + 16 * h, w);     // over scores that have been read
-            }
+            tmem_st16(s_t + c / 2, w);                // over scores that have been read
+            tmem_st16(s_t + c / 2 + 16, w + 16);
             const float2 sums = add2(sum[0], sum[1]);
             l += sums.x + sums.y;
           }
@@ -580,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (not_finite(kn)) {
               if (nt == 1 && n > 0 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
               tc_fence_after();
+#pragma unroll 1
               for (int d = 0; d < D; d += 16) {
                 float y[16];
                 if (n > 0) {
@@ -632,7 +644,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tc_fence_after();
         const int64_t token = (int64_t)s.s0 + (valid ? (int)fast_div((uint32_t)r, a.div_g) : 0);
         const int h = s.head * G + g;
-        if (s.whole) {
+        if (s.whole && p.out != nullptr) {
+          // through shared memory, so that rows leave in longer pieces than a thread's 16 bytes
+          constexpr int kPieces = staging_pieces(kFp8), kCols = 8 * kPieces;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int64_t row = token * p.out_ts + (int64_t)h * p.out_hs;
+          const uint32_t stage = staging + (uint32_t)(warp * staging_bytes(kFp8));
+          auto place = [&](int r, int c) { return stage + (uint32_t)(r * 16 * kPieces + ((c ^ ((r * kPieces >> 3) & (kPieces - 1))) << 4)); };
+#pragma unroll 1
+          for (int d = 0; d < D; d += kCols) {
+            float y[kCols];
+            if (kCols == 32) tmem_ld32(o_t + d, y); else tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+            tmem_ld_wait();
+            hold(y);
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = pack_bf16(y[8 * c + 2 * e] * inv, y[8 * c + 2 * e + 1] * inv);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(lane, c)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              const int from = 32 / kPieces * k + lane / kPieces, c = lane % kPieces;
+              const int64_t to = __shfl_sync(0xFFFFFFFFu, row, from);
+              uint4 v;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(from, c)) : "memory");
+              if (s.row0 + tile * 128 + wl * 32 + from < s.rows && d + 8 * c < D) *reinterpret_cast<uint4*>(p.out + to + d + 8 * c) = v;
+            }
+            __syncwarp();
+          }
+          if (valid && p.lse != nullptr) p.lse[token * (p.Hk * G) + h] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+        } else if (s.whole) {
+#pragma unroll 1
           for (int d = 0; d < D; d += 16) {
             float y[16];
             tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
@@ -642,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
         } else {
           float* slot = a.parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == s.c_first ? 1 : 0)) * a.slot_floats;
+#pragma unroll 1
           for (int d = 0; d < D; d += 16) {
             float y[16];
             tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
@@ -665,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               __threadfence();
             }
             if (__shfl_sync(0xFFFFFFFFu, last, 0) && valid)
+#pragma unroll 1
               for (int d = 0; d < D; d += 16) join16(a, s.c_first, s.c_last, kPair, r_in, token, h, d);
           }
         }
@@ -1007,9 +1054,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       while (ok && next_segment(true)) {
         const Segment& s = ctl->seg[seg_n & 1];
         const int T = s.tiles, lead = min(T, !kWide && s.nt == 2 ? 1 : 2);
-        // ---- Q, 32 rows at a time
-        if (q_n > 0 && !wait_warp(ctl->q_empty, q_n - 1)) break;
-        {
+        // ---- Q: boxes of whole tokens where a tile has whole tokens, else 32 rows at a time
+        if ((!a.q_box || w == 0) && q_n > 0 && !wait_warp(ctl->q_empty, q_n - 1)) break;
+        if (a.q_box) {
+          if (w == 0 && elect_one()) {
+            const int blocks = (D + 63) / 64;
+            const uint32_t bar = smem_u32(&ctl->q_full);
+            mbar_expect_tx(bar, (uint32_t)(s.nt * blocks * kBlockBytes));
+            for (int t = 0; t < s.nt; ++t)
+              for (int k = 0; k < blocks; ++k)
+                tma_load_3d(q_smem + (uint32_t)((t * 2 + k) * kBlockBytes), &tm_q, bar, k * 64, s.head * G,
+                            s.s0 + (int)fast_div((uint32_t)(s.row0 + t * 128), a.div_g));
+          }
+          __syncwarp();
+        } else {
           const int pieces = D / 8;
           for (int g = w; g < s.nt * 4; g += kHelpers) {
             const int r = s.row0 + g * 32 + lane;
@@ -1250,24 +1308,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 }
 
 template <bool kWide, bool kFp8, bool kForm>
-cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q, const Args& a, cudaStream_t stream) {
   static PerContextOnce once;
   const cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(prompt_kernel<kWide, kFp8, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kFp8));
   });
   if (e != cudaSuccess) return e;
-  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(kThreads), smem_bytes(kFp8), stream, true, tm_k, tm_v, a);
+  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(kThreads), smem_bytes(kFp8), stream, true, tm_k, tm_v, tm_q, a);
 }
 
 template <bool kFp8>
-cudaError_t launch_any(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream) {
+cudaError_t launch_any(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q, const Args& a, cudaStream_t stream) {
   const bool form = a.p.form.cap2 > 0.f || a.p.form.slopes != nullptr || !(a.p.scale_log2 > 0.f);
-  if (a.p.D > 128) return form ? launch<true, kFp8, true>(tm_k, tm_v, a, stream) : launch<true, kFp8, false>(tm_k, tm_v, a, stream);
-  return form ? launch<false, kFp8, true>(tm_k, tm_v, a, stream) : launch<false, kFp8, false>(tm_k, tm_v, a, stream);
+  if (a.p.D > 128) return form ? launch<true, kFp8, true>(tm_k, tm_v, tm_q, a, stream) : launch<true, kFp8, false>(tm_k, tm_v, tm_q, a, stream);
+  return form ? launch<false, kFp8, true>(tm_k, tm_v, tm_q, a, stream) : launch<false, kFp8, false>(tm_k, tm_v, tm_q, a, stream);
 }
 
-cudaError_t launch_bf16(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream);
-cudaError_t launch_fp8(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a, cudaStream_t stream);
+cudaError_t launch_bf16(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q, const Args& a, cudaStream_t stream);
+cudaError_t launch_fp8(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q, const Args& a, cudaStream_t stream);
 
 }  // namespace prompt
 }  // namespace engram
