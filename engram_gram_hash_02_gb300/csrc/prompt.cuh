@@ -718,6 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tc_fence_before();
         ++finals;
       }
+      // The second tile's warps stay with a segment of one tile: a barrier's phases are told apart by their parity alone
+      if (!kWide && !mine) {
+        for (int n = 1; ok && n < s.tiles; n += 2) ok = wait_warp(ctl->s_full[1], used[1] + (n >> 1));
+      }
       if (s.nt == 2) {
         used[0] += s.tiles;
         used[1] += s.tiles;
@@ -1094,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         uint32_t bad[4] = {0, 0, 0, 0};               // keys of the tile in which this thread has found a value that is not finite
         // eight bf16 of key `row`: what is not finite becomes zero, and is noted
-        auto clean = [&](uint32_t (&v)[4], int row) {
+        auto clean = [&](uint32_t (&v)[4], int row, int first) {
           bool found = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1102,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             found |= (lo | hi) != 0;
             v[e] &= ~(lo | hi);
           }
-          if (found) {
+          if (found && first + row < s.hull_hi) {     // (what lies behind the sequence is nobody's)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               if (row >> 5 == x) bad[x] |= 1u << (row & 31);
@@ -1138,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                   const uint32_t addr = from + piece(row, k % pieces);
                   uint32_t v[4];
                   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-                  if (clean(v, row))
+                  if (clean(v, row, s.key0 + n * kKeys))
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
                 }
               }
@@ -1173,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     y[2 * z] = pack_bf16(g0.x * scale, g0.y * scale);
                     y[2 * z + 1] = pack_bf16(g1.x * scale, g1.y * scale);
                   }
-                  if (partly) clean(y, row);
+                  if (partly) clean(y, row, s.key0 + n * kKeys);
                   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(row, 2 * c + e)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
                 }
               };
@@ -1223,7 +1227,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                       const uint32_t addr = dst + piece(row, k % pieces);
                       uint32_t v[4];
                       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-                      if (clean(v, row))
+                      if (clean(v, row, s.key0 + n * kKeys))
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
                     }
                   }

@@ -386,3 +386,21 @@ def test_many_sequences_and_long_ones():
     P.check_prompt(cache, table, new, lens, q, out, lse, 64 ** -0.5)
 
 
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_pairs_of_tiles_and_single_ones_in_turn(slopes):
+    """Sequences of many lengths in one batch: a block goes from two tiles of rows to one and back, with key tiles of any
+    number in between, and several times over."""
+    E = H.pkg()
+    new = [113, 2011, 60, 700, 1, 333, 1290, 129, 97, 512, 40, 257] * 2
+    cache, table = H.filled(new, 24, 4, 64, "bf16", 40)
+    T = sum(new)
+    q = randn(41, (T, 4, 64))
+    sl = P.alibi(4) if slopes else None
+    err = word()
+    for _ in range(3):
+        out, lse = E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(new), lse=True, err=err,
+                                             slopes=None if sl is None else P.dev(sl, torch.float32))
+    assert int(err) == 0
+    P.check_prompt(cache, table, new, new, q, out, lse, 64 ** -0.5, slopes=sl)
