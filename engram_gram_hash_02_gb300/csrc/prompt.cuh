@@ -50,6 +50,11 @@ constexpr int kThreads = 512;
 constexpr int kHelpers = 5;                           // warps
 constexpr int kMeta = 8;                              // key tiles whose masks are kept
 constexpr int kRunCost = 1;                           // a pair's fixed cost in key tiles, when work is divided
+// How far a row's maximum may run ahead of the one its sums are in units of, log 2. fp32 and bf16 keep their bits there;
+// what it takes is range: sums come to 2^30 times what they stand for at most, so values may be as large as 2^85 or so over
+// a few thousand keys. (With 8, rows whose scores spread by 2^14 had o multiplied in most of their tiles: 8192 tokens of 32 / 8
+// heads of 128, scores capped at 30, took three times as long.)
+constexpr float kLag = 30.f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;                       // S of buffer b at column 128 b, O of tile t at 256 + 128 t
 
@@ -335,6 +340,27 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// cap tanh(x y1) for two scores, as `capped` forms it
+__device__ __forceinline__ float2 capped2(float2 x, float y1, float cap) {
+  const float2 y = mul2(x, {y1, y1}), t = mul2(y, y), z = mul2(y, {2.88539008f, 2.88539008f});
+  float2 near = fma2(t, {-17.f / 315.f, -17.f / 315.f}, {2.f / 15.f, 2.f / 15.f});
+  near = fma2(t, near, {-1.f / 3.f, -1.f / 3.f});
+  near = mul2(y, fma2(t, near, {1.f, 1.f}));
+  const float2 e = add2({ex2(z.x), ex2(z.y)}, {1.f, 1.f});
+  const float2 far = fma2({rcp(e.x), rcp(e.y)}, {-2.f, -2.f}, {1.f, 1.f});
+  return mul2({fabsf(y.x) < 0.25f ? near.x : far.x, fabsf(y.y) < 0.25f ? near.y : far.y}, {cap, cap});
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -407,10 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto wait = [&](uint64_t& bar, uint32_t parity) { return wait_inline(smem_u32(&bar), parity & 1u, abort_flag, p.err); };
   // the same for a whole warp, with one answer for all of it
   auto wait_warp = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+  // A segment's key tiles are taken from the last to the first: where a bias falls with distance, the largest scores come
+  // first, and the maximum stays
+  auto first_of = [&](const Segment& s, int n) { return s.key0 + (s.tiles - 1 - n) * kKeys; };
   // whether some row that sees keys at all does not see all of the tile's (none sees those past its ends), and whether
   // values there were not finite
   auto partly_seen = [&](const Segment& s, int n) {
-    const int first = s.key0 + n * kKeys;
+    const int first = first_of(s, n);
     return first < s.max_lo || first + kKeys > s.min_hi;
   };
   auto bad_keys = [&](uint32_t kn, int w) {
@@ -464,11 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const int buf = nt == 2 ? tile : n & 1;
           const uint32_t s_t = lanes + (uint32_t)(buf * 128);
           const uint32_t kn = keys_n + n;
-          const int key0 = first_key + n * kKeys;
+          const int place = T - 1 - n, key0 = first_of(s, n);
           // what can be done before the scores are there: the softmax's latency is what the tensor cores wait for
           if (!wait_warp(ctl->k_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
           const uint4 live = *reinterpret_cast<const uint4*>(ctl->live[kn % kMeta]);
-          const bool full = __all_sync(0xFFFFFFFFu, n >= whole_from && n < whole_to && (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu);
+          const bool full = __all_sync(0xFFFFFFFFu, place >= whole_from && place < whole_to && (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu);
           if (nt == 2 || buf == 0 ? !wait_warp(ctl->s_full[buf], nth++) : !wait_warp(ctl->s_full[1], other++)) { ok = false; break; }
           tc_fence_after();
           if (!kForm && !full) {
@@ -489,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           // Half a tile at a time, in a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
           // exponentials are formed with the maximum so far, while the half's own is found: o, the sum and P are in units of
-          // 2^m, m a whole number that follows the true maximum only when that is 2^8 beyond it, which hardly ever happens
+          // 2^m, m a whole number that follows the true maximum only when that is kLag beyond it, which hardly ever happens
           // after the first tile; then the half is done again.
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 64) {
@@ -499,12 +528,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             tmem_ld_wait();
             hold(x);
             if (kForm) {
-              const float back = (float)(pos - key0 - c);
+              // the form, two scores at a time; x in units of log 2 then
+              if (p.form.cap2 > 0.f) {
+                const float y1 = p.scale_log2 * p.form.cap_inv;
 #pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                float y = x[j] * p.scale_log2;
-                if (p.form.cap2 > 0.f) y = capped(y, p.form.cap2, p.form.cap_inv);
-                x[j] = fmaf(-slope, fabsf(back - (float)j), y);
+                for (int j = 0; j < 64; j += 2) {
+                  const float2 y = capped2({x[j], x[j + 1]}, y1, p.form.cap2);
+                  x[j] = y.x;
+                  x[j + 1] = y.y;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
+              }
+              if (p.form.slopes != nullptr) {
+                const float back = (float)(pos - key0 - c);
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[j] = fmaf(-slope, fabsf(back - (float)j), x[j]);
               }
               if (!full) {
 #pragma unroll
@@ -525,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
             float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[60], max3(x[61], x[62], x[63])));
             if (!kForm) top *= p.scale_log2;
-            const bool grown = top > m + 8.f;
+            const bool grown = top > m + kLag;
             const float base = m == -INFINITY ? 0.f : m;
             const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -585,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           if (!ok) break;
           tmem_st_wait();
-          if (n < plain_from || n >= plain_to) {
+          if (place < plain_from || place >= plain_to) {
             // some row does not see all of the tile's keys: values that are not finite must not reach it
             if (!wait_warp(ctl->v_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
             if (not_finite(kn)) {
@@ -611,10 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     tmem_ld_wait();
                     asm volatile("" : "+r"(pw));
                     const float pj = (j & 1) ? engram::bf16_hi(pw) : engram::bf16_lo(pw);
-                    const int at = (int)fast_div((uint32_t)(key0 + j), p.cache.div_page), place = key0 + j - at * p.cache.page_size;
+                    const int at = (int)fast_div((uint32_t)(key0 + j), p.cache.div_page), in_page = key0 + j - at * p.cache.page_size;
                     const int64_t page = p.table[(int64_t)s.b * p.table_stride + at];
-                    const uint8_t* row = p.cache.v + page * p.cache.page_b + s.head * p.cache.head_b + place * p.cache.tok_b;
-                    const uint8_t* scales = p.cache.vs + page * p.cache.spage_b + s.head * p.cache.shead_b + place * p.cache.stok_b;
+                    const uint8_t* row = p.cache.v + page * p.cache.page_b + s.head * p.cache.head_b + in_page * p.cache.tok_b;
+                    const uint8_t* scales = p.cache.vs + page * p.cache.spage_b + s.head * p.cache.shead_b + in_page * p.cache.stok_b;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                       float v;
@@ -939,11 +979,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         int pg[2] = {-1, -1}, pl[2] = {0, 0};
         uint32_t there[2] = {0, 0};
         auto request = [&](int batch, int& page, int& place) {
-          const int pos = first_key + (((batch << 5) + lane) << box_log);
+          const int at = ((batch << 5) + lane) << box_log;    // (tile for tile, from the last to the first)
+          const int pos = first_key + (T - 1 - at / kKeys) * kKeys + at % kKeys;
           const int i = (int)fast_div((uint32_t)pos, p.cache.div_page);
           page = -1;
           place = pos - i * p.cache.page_size;
-          if (pos < hull_hi && pos >= first_key) {     // (past 2^31 it would be negative)
+          if (pos < hull_hi && pos >= first_key) {     // (before: past the last tile)
             page = p.table[(int64_t)b * p.table_stride + i];
             if (page < 0 || page >= p.cache.num_pages) {
               page = -1;
@@ -1142,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                   const uint32_t addr = from + piece(row, k % pieces);
                   uint32_t v[4];
                   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-                  if (clean(v, row, s.key0 + n * kKeys))
+                  if (clean(v, row, first_of(s, n)))
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
                 }
               }
@@ -1177,7 +1218,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     y[2 * z] = pack_bf16(g0.x * scale, g0.y * scale);
                     y[2 * z + 1] = pack_bf16(g1.x * scale, g1.y * scale);
                   }
-                  if (partly) clean(y, row, s.key0 + n * kKeys);
+                  if (partly) clean(y, row, first_of(s, n));
                   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(row, 2 * c + e)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
                 }
               };
@@ -1200,7 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 // 26 rows of each warp; a lane looks one up
                 if (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1)) { ok = false; break; }
                 const int row0 = w * 26, rows = min(26, kKeys - row0);
-                const int pos = s.key0 + n * kKeys + row0 + lane;
+                const int pos = first_of(s, n) + row0 + lane;
                 int64_t off = -1, soff = 0;
                 if (lane < rows && pos < s.hull_hi) {
                   const int i = (int)fast_div((uint32_t)pos, p.cache.div_page), place = pos - i * p.cache.page_size;
@@ -1227,7 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                       const uint32_t addr = dst + piece(row, k % pieces);
                       uint32_t v[4];
                       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-                      if (clean(v, row, s.key0 + n * kKeys))
+                      if (clean(v, row, first_of(s, n)))
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
                     }
                   }
