@@ -481,6 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         const float slope = kForm && p.form.slopes != nullptr && valid ? p.form.slopes[s.head * G + g] * 1.44269504f : 0.f;
         float m = -INFINITY, l = 0.f;
+        // A score is x times + plus of what the loop below makes of a product: the product itself; with a form its score; or
+        // capped alone, by up to 128, the reciprocal in the tanh (see `only_cap`): off by 2^-22 cap, where `capped2`, for any
+        // cap, keeps a score's own bits at twice the price (8192 tokens capped at 30: 1143 us)
+        const bool only_cap = kForm && p.form.slopes == nullptr && p.form.cap2 > 0.f && p.form.cap2 <= 128.f * 1.4427f;
+        const float times = !kForm ? p.scale_log2 : only_cap ? 2.f * p.form.cap2 : 1.f, plus = only_cap ? p.form.cap2 : 0.f;
+        const float to_exp = p.scale_log2 * p.form.cap_inv * 2.88539008f;
         // Tiles [whole_from, whole_to) are seen whole by every row of the warp, tiles [plain_from, plain_to) by every row of
         // the pair that sees any
         const int T = s.tiles, nt = s.nt, first_key = s.key0;
@@ -528,8 +534,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             tmem_ld_wait();
             hold(x);
             if (kForm) {
-              // the form, two scores at a time; x in units of log 2 then
-              if (p.form.cap2 > 0.f) {
+              // the form, two scores at a time
+              if (only_cap) {
+                // cap tanh(y) = cap - 2 cap / (1 + exp(2 y)): x becomes the negative reciprocal
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) {
+                  const float2 z = mul2({x[j], x[j + 1]}, {to_exp, to_exp});
+                  const float2 e = fma2({ex2(z.x), ex2(z.y)}, {-1.f, -1.f}, {-1.f, -1.f});
+                  x[j] = rcp(e.x);
+                  x[j + 1] = rcp(e.y);
+                }
+              } else if (p.form.cap2 > 0.f) {
                 const float y1 = p.scale_log2 * p.form.cap_inv;
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
@@ -564,16 +579,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
               for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
             float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[60], max3(x[61], x[62], x[63])));
-            if (!kForm) top *= p.scale_log2;
+            top = fmaf(top, times, plus);
             const bool grown = top > m + kLag;
             const float base = m == -INFINITY ? 0.f : m;
-            const float2 scale2 = {p.scale_log2, p.scale_log2}, base2 = {-base, -base};
+            const float2 times2 = {times, times}, plus2 = {plus - base, plus - base};
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
             uint32_t w[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float2 xx = {x[2 * j], x[2 * j + 1]};
-              const float2 y = kForm ? add2(xx, base2) : fma2(xx, scale2, base2);
+              const float2 y = fma2(xx, times2, plus2);
               const float2 e = {ex2(y.x), ex2(y.y)};
               sum[j & 1] = add2(sum[j & 1], e);
               w[j] = pack_bf16(e.x, e.y);
