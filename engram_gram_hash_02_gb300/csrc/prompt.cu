@@ -8,7 +8,6 @@ namespace prompt {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kEntryLanes = 8;                        // of the plan for one entry: they look at its tokens in turn
 
 // inclusive sum over the block; `total` for all
 __device__ int64_t block_scan(int64_t x, int64_t* warps, int64_t& total) {
@@ -63,11 +62,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   }
   const int E = (int)min(run, a.max_entries);
   __syncthreads();
-  // ---- what their rows see
-  for (int e0 = 0; e0 < E; e0 += kPlanThreads / kEntryLanes) {
-    const int e = e0 + threadIdx.x / kEntryLanes, sub = threadIdx.x % kEntryLanes;
+  // ---- what their rows see: up to eight lanes to an entry, which look at its tokens in turn
+  const int lanes_log = E <= kPlanThreads / 8 ? 3 : E <= kPlanThreads / 4 ? 2 : E <= kPlanThreads / 2 ? 1 : 0, lanes = 1 << lanes_log;
+  const bool arrays = p.doc_starts != nullptr || p.prefix_ends != nullptr;
+  for (int e0 = 0; e0 < E; e0 += kPlanThreads >> lanes_log) {
+    const int e = e0 + (threadIdx.x >> lanes_log), sub = threadIdx.x & (lanes - 1);
     Entry x{};
     int lo = 0x7FFFFFFF, hi = 0, max_lo = 0, min_hi = 0x7FFFFFFF;
+    auto take = [&](int i) {
+      int l, h, pos;
+      visible(p, x.s0, x.n, x.len, i, l, h, pos);
+      if (l < h) {
+        lo = min(lo, l);
+        hi = max(hi, h);
+        max_lo = max(max_lo, l);
+        min_hi = min(min_hi, h);
+      }
+    };
     if (e < E) {
       int first = 0, past = p.B;                      // the last sequence whose first pair is e or before
       while (past - first > 1) {
@@ -78,23 +89,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
       bounds(x.b, x.s0, x.n, x.len);
       x.row0 = (e - a.offsets[x.b]) * R;
       x.rows = (int)min((int64_t)x.n * p.G, (int64_t)x.row0 + R);
-      const int i0 = x.row0 / p.G, i1 = (x.rows - 1) / p.G;
-      // without arrays lo and hi only grow along the tokens: the first that sees anything and the last say it all
-      const bool arrays = p.doc_starts != nullptr || p.prefix_ends != nullptr;
-      const int from = arrays ? i0 : p.own_lens == nullptr && p.causal ? max(i0, x.n - x.len) : i0;
-      for (int i = from + (arrays ? sub : sub * max(i1 - from, 1)); i <= i1; i += arrays ? kEntryLanes : max(i1 - from, 1) * kEntryLanes) {
-        int l, h, pos;
-        visible(p, x.s0, x.n, x.len, i, l, h, pos);
-        if (l < h) {
-          lo = min(lo, l);
-          hi = max(hi, h);
-          max_lo = max(max_lo, l);
-          min_hi = min(min_hi, h);
+      const int i0 = (int)fast_div((uint32_t)x.row0, a.div_g), i1 = (int)fast_div((uint32_t)(x.rows - 1), a.div_g);
+      if (arrays) {
+#pragma unroll 4
+        for (int i = i0 + sub; i <= i1; i += lanes) take(i);
+      } else if (sub == 0) {
+        // without arrays lo and hi only grow along the tokens: the first that sees anything and the last say it all
+        const int from = p.own_lens == nullptr && p.causal ? max(i0, x.n - x.len) : i0;
+        if (from <= i1) {
+          take(from);
+          take(i1);
         }
       }
     }
-#pragma unroll
-    for (int o = 1; o < kEntryLanes; o <<= 1) {
+    for (int o = 1; o < lanes; o <<= 1) {
       lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
       hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
       max_lo = max(max_lo, __shfl_xor_sync(0xFFFFFFFFu, max_lo, o));
@@ -127,12 +135,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
     a.header->per_cta = per;
   }
   __syncthreads();
-  for (int64_t k = threadIdx.x; k < (int64_t)E * p.Hk; k += kPlanThreads) {
-    const int head = (int)(k / E), e = (int)(k % E);
-    const int units = a.entries[e].units;
-    if (units == 0) continue;
-    const int64_t first = head * U + a.entries[e].place, past = first + units + kRunCost;
-    for (int64_t c = (first + per - 1) / per; c < a.ctas && c * per < past; ++c) a.starts[c] = Start{head, e};
+  // a CTA's first place is in the last entry of work that starts there or before
+  for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
+    const int64_t at = c * per;
+    if (at >= all) continue;
+    const int head = (int)(at / U);
+    const int64_t in_head = at - head * U;
+    int first = 0, past = E;
+    while (past - first > 1) {
+      const int mid = (first + past) / 2;
+      (a.entries[mid].place <= in_head ? first : past) = mid;
+    }
+    a.starts[c] = Start{head, first};
   }
 }
 
@@ -142,20 +156,21 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   const int R = pair_rows(p.D), lane = threadIdx.x & 31;
   pdl_wait();
   const int64_t E = a.header->entries, U = a.header->places, per = a.header->per_cta;
-  const int blocks = (R / 32) * (p.D / 16);
-  const int64_t warps = (int64_t)gridDim.x * 8, all = E * p.Hk * blocks;
-  for (int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); k < all; k += warps) {
-    const int64_t item = k / blocks;
-    const int block = (int)(k % blocks), head = (int)(item / E);
-    const Entry& x = a.entries[item % E];
+  const int64_t warps = (int64_t)gridDim.x * 8, items = E * p.Hk;
+  // where there are pairs enough, a warp goes through a pair's rows itself: most of them may be short of rows
+  const int chunks = p.D / 16, split = items * chunks >= warps / 2 ? 1 : R / 32;
+  for (int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); k < items * chunks * split; k += warps) {
+    const int64_t item = k / (chunks * split);
+    const int rest = (int)(k - item * (chunks * split)), head = (int)(item / E);
+    const Entry& x = a.entries[item - head * E];
     if (x.units == 0) continue;
     const int64_t run0 = head * U + x.place + kRunCost;
     const int first = (int)(run0 / per), last = (int)((run0 + x.units - 1) / per);
     if (first == last) continue;
-    const int r_in = (block % (R / 32)) * 32 + lane, r = x.row0 + r_in;
-    if (r >= x.rows) continue;
-    const int i = (int)fast_div((uint32_t)r, a.div_g);
-    join16(a, first, last, R, r_in, (int64_t)x.s0 + i, head * p.G + r - i * p.G, (block / (R / 32)) * 16);
+    for (int r_in = (rest % split) * 32 + lane; r_in < x.rows - x.row0; r_in += split * 32) {
+      const int r = x.row0 + r_in, i = (int)fast_div((uint32_t)r, a.div_g);
+      join16(a, first, last, R, r_in, (int64_t)x.s0 + i, head * p.G + r - i * p.G, (rest / split) * 16);
+    }
   }
 }
 

@@ -15,7 +15,7 @@
 //   warp 12            looks pages up and requests K and V tiles in the order in which they are used: TMA boxes of the
 //                      cache's own layout, up to 64 tokens of a page at once. bf16 goes to a ring of 32 KB slots that
 //                      the MMAs read, FP8 to stages
-//   warps 10, 11, 13..15   bring Q in (16-byte copies); FP8: convert a stage's rows to bf16 into the ring (exact). Pages
+//   warps 10, 11, 13..15 (FP8: ..19)   bring Q in (16-byte copies); FP8: convert a stage's rows to bf16 into the ring (exact). Pages
 //                      that are no multiple of 8 tokens do not divide into boxes: these warps then fetch the rows themselves
 // While the softmax of one tile runs, the tensor cores work on the other; with one tile, on the next key tile.
 //
@@ -46,8 +46,10 @@ __host__ __device__ constexpr int staging_bytes(bool fp8) { return 32 * 16 * sta
 constexpr int kStages = 3;                            // FP8: of 128 codes and their scale word for each of 128 keys
 constexpr int kStageBytes = kBlockBytes + 512;
 constexpr int kQBytes = 65536;
-constexpr int kThreads = 512;
-constexpr int kHelpers = 5;                           // warps
+// Warps that convert FP8 rows are what bounds it: four more of them, with fewer registers each
+__host__ __device__ constexpr int threads_of(bool fp8) { return fp8 ? 640 : 512; }
+__host__ __device__ constexpr int helpers_of(bool fp8) { return fp8 ? 9 : 5; }   // warps
+constexpr int kMaxHelpers = 9;
 constexpr int kMeta = 8;                              // key tiles whose masks are kept
 constexpr int kRunCost = 1;                           // a pair's fixed cost in key tiles, when work is divided
 // How far a row's maximum may run ahead of the one its sums are in units of, log 2. fp32 and bf16 keep their bits there;
@@ -260,7 +262,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(is));
   return is != 0;
 }
-// (the four warpgroups' shares come to what the block is launched with: 2 * 168 + 2 * 88 = 4 * 128 a thread)
+// (the warpgroups' shares come to what the block is launched with: 2 * 168 + 2 * 88 = 4 * 128 a thread; FP8 2 * 144 + 3 * 64 = 5 * 96)
 template <int kRegs>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
@@ -318,13 +320,12 @@ struct Ctl {
   uint64_t drained;
   Segment seg[2];
   alignas(16) uint32_t live[kMeta][4];                // which keys of a tile are there
-  uint32_t v_bad[kMeta][kHelpers][4];                 // keys whose values are not all finite (in tiles that some row sees partly)
+  uint32_t v_bad[kMeta][kMaxHelpers][4];              // keys whose values are not all finite (in tiles that some row sees partly)
   uint32_t tmem_base;
   int32_t abort_flag;
 };
 constexpr int smem_bytes(bool fp8) { return 1024 + kQBytes + slots_of(fp8) * kSlotBytes + (fp8 ? kStages * kStageBytes : 0) + 8 * staging_bytes(fp8) + (int)sizeof(Ctl); }
 static_assert(smem_bytes(false) <= kSmemBudget && smem_bytes(true) <= kSmemBudget, "one CTA's shared memory");
-constexpr int kSegReaders = 8 + 1 + 1 + kHelpers;
 
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 // ---- two values at once; the largest of three ------------------------------------------------------------------
@@ -372,14 +373,14 @@ __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)((c >
 // kWide: heads of more than 128 values (one tile of rows, two slots per key or value tile). kForm: scores with a form, or a
 // scale that is not positive
 template <bool kWide, bool kFp8, bool kForm>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+__global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                                                              const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
   const PromptParams& p = a.p;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t q_smem = (raw + 1023u) & ~1023u;
   const uint32_t ring = q_smem + kQBytes;
-  constexpr int kSlots = slots_of(kFp8);
+  constexpr int kSlots = slots_of(kFp8), kHelpers = helpers_of(kFp8);
   const uint32_t stages = ring + kSlots * kSlotBytes;
   const uint32_t staging = stages + (kFp8 ? kStages * kStageBytes : 0);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (staging + 8 * staging_bytes(kFp8) - raw));
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(smem_u32(&ctl->p_full[i]), 4);
       mbar_init(smem_u32(&ctl->o_final[i]), 1);
       mbar_init(smem_u32(&ctl->seg_full[i]), 1);
-      mbar_init(smem_u32(&ctl->seg_empty[i]), kSegReaders);
+      mbar_init(smem_u32(&ctl->seg_empty[i]), 8 + 1 + 1 + kHelpers);
     }
     mbar_init(smem_u32(&ctl->o_done), 1);
     ctl->abort_flag = 0;
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    more_registers<168>();
+    more_registers<kFp8 ? 144 : 168>();
     const int tile = warp >> 2, wl = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     const uint32_t o_t = lanes + kOCol + (uint32_t)(tile * 128);
@@ -791,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       ++seg_n;
     }
   } else {
-    fewer_registers<88>();
+    fewer_registers<kFp8 ? 64 : 88>();
     if (warp == 8) {
       // -------------------------------------------------------------- MMA
       // The warp stays together: every lane waits, one issues. (Uniform registers hold the descriptors.)
@@ -1155,19 +1156,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         uint32_t bad[4] = {0, 0, 0, 0};               // keys of the tile in which this thread has found a value that is not finite
         // eight bf16 of key `row`: what is not finite becomes zero, and is noted
         auto clean = [&](uint32_t (&v)[4], int row, int first) {
-          bool found = false;
+          uint32_t ones = 0;                          // exponents of ones: 0x7F80 + 0x80 carries into the sign's place
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ones |= (v[e] & 0x7F807F80u) + 0x00800080u;
+          if ((ones & 0x80008000u) == 0) return false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t lo = (v[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (v[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-            found |= (lo | hi) != 0;
             v[e] &= ~(lo | hi);
           }
-          if (found && first + row < s.hull_hi) {     // (what lies behind the sequence is nobody's)
+          if (first + row < s.hull_hi) {              // (what lies behind the sequence is nobody's)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               if (row >> 5 == x) bad[x] |= 1u << (row & 31);
           }
-          return found;
+          return true;
+        };
+        // rows [0, before) and [past, kKeys) of tile n are those that some row may not see
+        auto seen_before = [&](int n) { return min(max(s.max_lo - first_of(s, n), 0), kKeys); };
+        auto seen_past = [&](int n) { return min(max(s.min_hi - first_of(s, n), 0), kKeys); };
+        // those rows of a slot, `count` from `row0` on, 32 / kLanes at a time with `stride` turns between
+        auto look_through = [&](uint32_t slot_at, int pieces, int row0, int row1, int step, int n) {
+          const int c = lane & 15, before = seen_before(n), past = seen_past(n), first = first_of(s, n);
+          for (int row = row0 + (lane >> 4); row < row1; row += step) {
+            if (c >= pieces || (row >= before && row < past)) continue;
+            const uint32_t addr = slot_at + piece(row, c);
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+            if (clean(v, row, first))
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+          }
+          __syncwarp();
         };
         auto note = [&](int m, bool partly) {         // a value tile is through
           if (partly) {
@@ -1191,16 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               for (int part = 0; part < kSlotsPerTile; ++part) {
                 const uint32_t at = seq + (uint32_t)((min(T, n + lead) + n) * kSlotsPerTile + part);
                 if (!wait_warp(ctl->full[at % kSlots], at / kSlots)) { ok = false; break; }
-                const uint32_t from = ring + (at % kSlots) * kSlotBytes;
-                const int pieces = min(16, (D - part * 128) / 8);
-                for (int k = w * 32 + lane; k < kKeys * pieces; k += kHelpers * 32) {
-                  const int row = k / pieces;
-                  const uint32_t addr = from + piece(row, k % pieces);
-                  uint32_t v[4];
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-                  if (clean(v, row, first_of(s, n)))
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-                }
+                look_through(ring + (at % kSlots) * kSlotBytes, min(16, (D - part * 128) / 8), 2 * w, kKeys, 2 * kHelpers, n);
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
@@ -1218,6 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int part = 0; part < kSlotsPerTile; ++part, ++seq) {
               const uint32_t dst = ring + (seq % kSlots) * kSlotBytes;
               const int pieces = min(16, (D - part * 128) / 8);
+              const int before = seen_before(n), past = seen_past(n), first = first_of(s, n);
               // codes (16 of a row) to bf16
               auto convert = [&](const uint4& x, float scale, int row, int c) {
                 const uint32_t codes[4] = {x.x, x.y, x.z, x.w};
@@ -1233,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     y[2 * z] = pack_bf16(g0.x * scale, g0.y * scale);
                     y[2 * z + 1] = pack_bf16(g1.x * scale, g1.y * scale);
                   }
-                  if (partly) clean(y, row, first_of(s, n));
+                  if (partly && (row < before || row >= past)) clean(y, row, first);
                   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(row, 2 * c + e)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
                 }
               };
@@ -1253,9 +1264,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) arrive(ctl->st_empty[st]);
               } else {
-                // 26 rows of each warp; a lane looks one up
+                // a run of rows for each warp; a lane looks one up
                 if (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1)) { ok = false; break; }
-                const int row0 = w * 26, rows = min(26, kKeys - row0);
+                constexpr int kRows = (kKeys + kHelpers - 1) / kHelpers;
+                const int row0 = w * kRows, rows = min(kRows, kKeys - row0);
                 const int pos = first_of(s, n) + row0 + lane;
                 int64_t off = -1, soff = 0;
                 if (lane < rows && pos < s.hull_hi) {
@@ -1269,7 +1281,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 const uint8_t* from = values ? p.cache.v : p.cache.k;
                 if (!kFp8) {
                   const int c = lane & 15, sub = lane >> 4;
-                  for (int k = 0; k < 13; ++k) {
+                  for (int k = 0; k < (kRows + 1) / 2; ++k) {
                     const int row = 2 * k + sub;
                     const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
                     if (row < rows && c < pieces) copy16_or_zero(dst + piece(row0 + row, c), from + (o < 0 ? 0 : o) + part * 256 + c * 16, o >= 0);
@@ -1277,21 +1289,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                   cp_async_commit();
                   cp_async_wait<0>();
                   __syncwarp();
-                  if (partly) {
-                    for (int k = lane; k < rows * pieces; k += 32) {
-                      const int row = row0 + k / pieces;
-                      const uint32_t addr = dst + piece(row, k % pieces);
-                      uint32_t v[4];
-                      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-                      if (clean(v, row, first_of(s, n)))
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-                    }
-                  }
+                  if (partly) look_through(dst, pieces, row0, row0 + rows, 2, n);
                 } else {
                   uint32_t word = 0;
                   if (off >= 0) word = *reinterpret_cast<const uint32_t*>((values ? p.cache.vs : p.cache.ks) + soff + 4 * part);
                   const int c = lane & 7, sub = lane >> 3;
-                  for (int k = 0; k < 7; ++k) {
+                  for (int k = 0; k < (kRows + 3) / 4; ++k) {
                     const int row = 4 * k + sub;
                     const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
                     const uint32_t sw = __shfl_sync(0xFFFFFFFFu, word, row);
@@ -1374,7 +1377,7 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUten
     return cudaFuncSetAttribute(prompt_kernel<kWide, kFp8, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kFp8));
   });
   if (e != cudaSuccess) return e;
-  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(kThreads), smem_bytes(kFp8), stream, true, tm_k, tm_v, tm_q, a);
+  return launch_k(prompt_kernel<kWide, kFp8, kForm>, dim3((unsigned)a.ctas), dim3(threads_of(kFp8)), smem_bytes(kFp8), stream, true, tm_k, tm_v, tm_q, a);
 }
 
 template <bool kFp8>
