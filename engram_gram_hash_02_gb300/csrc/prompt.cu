@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   }
   const int E = (int)min(run, a.max_entries);
   __syncthreads();
-  // ---- what their rows see: up to eight lanes to an entry, which look at its tokens in turn
-  const int lanes_log = E <= kPlanThreads / 8 ? 3 : E <= kPlanThreads / 4 ? 2 : E <= kPlanThreads / 2 ? 1 : 0, lanes = 1 << lanes_log;
+  // ---- what their rows see: up to 32 lanes to an entry, which look at its tokens in turn
+  const int lanes_log = E <= kPlanThreads / 32 ? 5 : E <= kPlanThreads / 16 ? 4 : E <= kPlanThreads / 8 ? 3 : E <= kPlanThreads / 4 ? 2 : E <= kPlanThreads / 2 ? 1 : 0, lanes = 1 << lanes_log;
   const bool arrays = p.doc_starts != nullptr || p.prefix_ends != nullptr;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads >> lanes_log) {
     const int e = e0 + (threadIdx.x >> lanes_log), sub = threadIdx.x & (lanes - 1);

@@ -855,7 +855,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               const int v = slot;
               if (!wait_warp(ctl->full[slot], phase)) { ok = false; break; }
               next_slot();
-              if (n + 1 < T && !wait_warp(ctl->full[slot], phase)) { ok = false; break; }
               const bool partly = partly_seen(s, n);
               if (partly && !wait_warp(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
               const bool add = n > 0 || (partly && not_finite(kn + n));
@@ -865,6 +864,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                 pv(t, t, v, 0, add);
                 if (t == 1) commit(ctl->empty[v]);
                 if (n + 1 < T) {
+                  if (t == 0) {                       // (not before these products: they need no keys)
+                    if (!wait_warp(ctl->full[slot], phase)) { ok = false; break; }
+                    tc_fence_after();
+                  }
                   qk(t, t, slot, 0);
                   commit(ctl->s_full[t]);
                 } else {
@@ -1233,16 +1236,16 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               auto convert = [&](const uint4& x, float scale, int row, int c) {
                 const uint32_t codes[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e0 = 0; e0 < 2; ++e0) {
-                  const int e = e0 ^ ((c >> 2) & 1);  // (eight lanes of a row, eight different bank groups)
+                for (int e = 0; e < 2; ++e) {
                   uint32_t y[4];
 #pragma unroll
                   for (int z = 0; z < 2; ++z) {
                     uint32_t f0, f1;
-                    e4m3x4_to_f16x2(e == 0 ? codes[z] : codes[2 + z], f0, f1);
-                    const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&f0)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
-                    y[2 * z] = pack_bf16(g0.x * scale, g0.y * scale);
-                    y[2 * z + 1] = pack_bf16(g1.x * scale, g1.y * scale);
+                    e4m3x4_to_f16x2(codes[2 * e + z], f0, f1);
+                    const float2 g0 = mul2(__half22float2(*reinterpret_cast<const __half2*>(&f0)), {scale, scale});
+                    const float2 g1 = mul2(__half22float2(*reinterpret_cast<const __half2*>(&f1)), {scale, scale});
+                    y[2 * z] = pack_bf16(g0.x, g0.y);
+                    y[2 * z + 1] = pack_bf16(g1.x, g1.y);
                   }
                   if (partly && (row < before || row >= past)) clean(y, row, first);
                   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(row, 2 * c + e)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
@@ -1251,10 +1254,12 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               if (kFp8 && a.box > 0) {
                 const uint32_t st = seq % kStages, from = stages + st * kStageBytes;
                 if (!wait_warp(ctl->st_full[st], seq / kStages) || (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1))) { ok = false; break; }
-                const int per_row = pieces / 2;
+                // a lane takes 16 codes of a row: eight lanes that store at once have four pieces of two rows, which the
+                // swizzle keeps in different banks
+                const int per_row = pieces / 2, c = (lane & 3) | (lane >> 1 & 4);
 #pragma unroll 2
-                for (int k = w * 32 + lane; k < kKeys * per_row; k += kHelpers * 32) {
-                  const int row = per_row == 8 ? k >> 3 : k / per_row, c = k - row * per_row;
+                for (int row = w * 4 + ((lane >> 2 & 1) | (lane >> 3 & 2)); row < kKeys; row += kHelpers * 4) {
+                  if (c >= per_row) continue;
                   uint4 x;
                   uint32_t word;
                   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(from + row * 128 + c * 16) : "memory");
