@@ -12,11 +12,12 @@
 //   warp 8             issues the MMAs:  S = Q K^T (both from shared memory),  O += P V (P from tensor memory, V as it
 //                      lies, by rows of keys: an MN-major operand)
 //   warp 9             walks the CTA's share of the work and hands segments (a run of key tiles of one pair of tiles) out
-//   warp 12            looks pages up and requests K and V tiles in the order in which they are used: TMA boxes of the
-//                      cache's own layout, up to 64 tokens of a page at once. bf16 goes to a ring of 32 KB slots that
-//                      the MMAs read, FP8 to stages
-//   warps 10, 11, 13..15 (FP8: ..19)   bring Q in (16-byte copies); FP8: convert a stage's rows to bf16 into the ring (exact). Pages
-//                      that are no multiple of 8 tokens do not divide into boxes: these warps then fetch the rows themselves
+//   warps 12, 13       look pages up and request K and V tiles in the order in which they are used: TMA boxes of
+//                      the cache's own layout, up to 64 tokens of a page at once. bf16 goes to a ring of 32 KB slots
+//                      that the MMAs read, FP8 to stages
+//   warps 10, 11, 14, 15 (FP8: ..19)   bring Q in, look through values (below); FP8: convert a stage's rows to bf16 into the
+//                      ring (exact). Pages that are no multiple of 8 tokens do not divide into boxes: these warps, and all
+//                      loaders but one, then fetch the rows themselves
 // While the softmax of one tile runs, the tensor cores work on the other; with one tile, on the next key tile.
 //
 // Work is cut at key tiles: a first kernel (one CTA) lists the pairs of tiles with the hull of their keys, and every CTA
@@ -48,7 +49,10 @@ constexpr int kStageBytes = kBlockBytes + 512;
 constexpr int kQBytes = 65536;
 // Warps that convert FP8 rows are what bounds it: four more of them, with fewer registers each
 __host__ __device__ constexpr int threads_of(bool fp8) { return fp8 ? 640 : 512; }
-__host__ __device__ constexpr int helpers_of(bool fp8) { return fp8 ? 9 : 5; }   // warps
+// Behind the softmax, MMA and dividing warps: those that request boxes (one requests a box in about 200 cycles, and a page of
+// 16 tokens is a box), and helpers. Where rows are fetched one by one only the first loader is one.
+__host__ __device__ constexpr int loaders_of(bool fp8) { return 2; }
+__host__ __device__ constexpr int helpers_of(bool fp8) { return fp8 ? 8 : 4; }
 constexpr int kMaxHelpers = 9;
 constexpr int kMeta = 8;                              // key tiles whose masks are kept
 constexpr int kRunCost = 1;                           // a pair's fixed cost in key tiles, when work is divided
@@ -380,7 +384,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t q_smem = (raw + 1023u) & ~1023u;
   const uint32_t ring = q_smem + kQBytes;
-  constexpr int kSlots = slots_of(kFp8), kHelpers = helpers_of(kFp8);
+  constexpr int kSlots = slots_of(kFp8);
+  const int loaders = a.box > 0 ? loaders_of(kFp8) : 1, helpers = helpers_of(kFp8) + loaders_of(kFp8) - loaders;
   const uint32_t stages = ring + kSlots * kSlotBytes;
   const uint32_t staging = stages + (kFp8 ? kStages * kStageBytes : 0);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (staging + 8 * staging_bytes(kFp8) - raw));
@@ -392,25 +397,25 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), !kFp8 && a.box > 0 ? 1 : kHelpers);
+      mbar_init(smem_u32(&ctl->full[s]), !kFp8 && a.box > 0 ? loaders : helpers);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&ctl->st_full[s]), 1 + 32);  // the boxes, and every lane's scale words
-      mbar_init(smem_u32(&ctl->st_empty[s]), kHelpers);
+      mbar_init(smem_u32(&ctl->st_full[s]), loaders + 32);  // the boxes, and every lane's scale words
+      mbar_init(smem_u32(&ctl->st_empty[s]), helpers);
     }
-    mbar_init(smem_u32(&ctl->q_full), a.q_box ? 1 : kHelpers);
+    mbar_init(smem_u32(&ctl->q_full), a.q_box ? 1 : helpers);
     mbar_init(smem_u32(&ctl->q_empty), 1);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(smem_u32(&ctl->k_meta[i]), 1);
-      mbar_init(smem_u32(&ctl->v_meta[i]), kHelpers);
+      mbar_init(smem_u32(&ctl->v_meta[i]), helpers);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
       mbar_init(smem_u32(&ctl->p_full[i]), 4);
       mbar_init(smem_u32(&ctl->o_final[i]), 1);
       mbar_init(smem_u32(&ctl->seg_full[i]), 1);
-      mbar_init(smem_u32(&ctl->seg_empty[i]), 8 + 1 + 1 + kHelpers);
+      mbar_init(smem_u32(&ctl->seg_empty[i]), 8 + 1 + loaders + helpers);
     }
     mbar_init(smem_u32(&ctl->o_done), 1);
     ctl->abort_flag = 0;
@@ -445,8 +450,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
   };
   auto bad_keys = [&](uint32_t kn, int w) {
     uint32_t y = 0;
-#pragma unroll
-    for (int h = 0; h < kHelpers; ++h) y |= *(volatile uint32_t*)&ctl->v_bad[kn % kMeta][h][w];
+    for (int h = 0; h < helpers; ++h) y |= *(volatile uint32_t*)&ctl->v_bad[kn % kMeta][h][w];
     return y;
   };
   auto not_finite = [&](uint32_t kn) { return (bad_keys(kn, 0) | bad_keys(kn, 1) | bad_keys(kn, 2) | bad_keys(kn, 3)) != 0; };
@@ -510,16 +514,17 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           if (!kForm && !full) {
             // masked before: hardly any tile is, and the loop below stays small
 #pragma unroll 1
-            for (int c = 0; c < kKeys; c += 16) {
-              float y[16];
-              tmem_ld16(s_t + c, reinterpret_cast<uint32_t*>(y));
-              const uint32_t sees = (ctl->live[kn % kMeta][c >> 5] >> (c & 16)) & bits_below(hi - key0 - c) & ~bits_below(lo - key0 - c);
+            for (int c = 0; c < kKeys; c += 32) {
+              float y[32];
+              tmem_ld32(s_t + c, y);
+              const uint32_t sees = ctl->live[kn % kMeta][c >> 5] & bits_below(hi - key0 - c) & ~bits_below(lo - key0 - c);
               tmem_ld_wait();
               hold(y);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
+              for (int e = 0; e < 32; ++e)
                 if (!((sees >> e) & 1u)) y[e] = -INFINITY;
               tmem_st16(s_t + c, reinterpret_cast<const uint32_t*>(y));
+              tmem_st16(s_t + c + 16, reinterpret_cast<const uint32_t*>(y + 16));
             }
             tmem_st_wait();
           }
@@ -581,6 +586,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
             float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[60], max3(x[61], x[62], x[63])));
             top = fmaf(top, times, plus);
+            if (n == 0 && c == 0) m = ceilf(top);     // (nothing is summed yet)
             const bool grown = top > m + kLag;
             const float base = m == -INFINITY ? 0.f : m;
             const float2 times2 = {times, times}, plus2 = {plus - base, plus - base};
@@ -980,9 +986,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
         if (ok) put(end);
       }
       __syncwarp();
-    } else if (warp == 12) {
+    } else if (warp >= 12 && warp < 12 + loaders) {
       // -------------------------------------------------------------- pages, and boxes of K and V
       const bool leader = elect_one();
+      const int loader = warp - 12;
       int slot = 0, stage = 0;
       uint32_t phase = 0, st_phase = 0, kn = 0;
       bool ok = true;
@@ -1007,7 +1014,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             page = p.table[(int64_t)b * p.table_stride + i];
             if (page < 0 || page >= p.cache.num_pages) {
               page = -1;
-              if (p.err != nullptr) atomicOr(p.err, ENGRAM_ERR_PAGE);
+              if (p.err != nullptr && loader == 0) atomicOr(p.err, ENGRAM_ERR_PAGE);
             }
           }
         };
@@ -1026,7 +1033,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           const bool next_batch = a.box > 0 && (n >> batch_log) != batch;
           const int page = next_batch ? pg[1] : pg[0], place = next_batch ? pl[1] : pl[0];
           const int at = (n * boxes) & 31;            // the tile's first box in its batch
-          if (!values) {
+          if (!values && loader == 0) {
             const int m = (kn + n) % kMeta;
             if (a.box > 0) {
               const uint32_t all = boxes == 16 ? 0xFFFFu : (1u << boxes) - 1u, has = ((next_batch ? there[1] : there[0]) >> at) & all;
@@ -1054,11 +1061,13 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               const bool two = !kFp8 && D - part * 128 > 64;   // blocks of 64 values
               const uint32_t dst = kFp8 ? stages + (uint32_t)(stage * kStageBytes) : ring + (uint32_t)(slot * kSlotBytes);
               const uint32_t bar = smem_u32(kFp8 ? &ctl->st_full[stage] : &ctl->full[slot]);
-              if (leader) mbar_expect_tx(bar, two ? 2 * kBlockBytes : kBlockBytes);
+              // this loader's boxes: every so many from its own on
+              const int mine = (boxes - loader + loaders - 1) / loaders;
+              if (leader) mbar_expect_tx(bar, (uint32_t)((mine << box_log) * (two ? 256 : 128)));
               // One lane requests all boxes (lanes of their own would take turns all the same, at a higher price). A page that
               // is not there reads as zeros.
               const CUtensorMap* map = values ? &tm_v : &tm_k;
-              for (int k = 0; k < boxes; ++k) {
+              for (int k = loader; k < boxes; k += loaders) {
                 const int y = __shfl_sync(0xFFFFFFFFu, place, at + k), z = __shfl_sync(0xFFFFFFFFu, page, at + k);
                 const uint32_t to = dst + (uint32_t)((k << box_log) * 128);
                 if (leader) {
@@ -1066,7 +1075,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                   if (two) tma_load_4d(to + kBlockBytes, map, bar, part * 128 + 64, y, head, z);
                 }
               }
-              if (kFp8) {
+              if (kFp8 && loader == 0) {
                 // scale words: keys 4 * lane .. + 3, all in one box
                 const int key = 4 * lane, from_lane = at + (key >> box_log);
                 const int pb = __shfl_sync(0xFFFFFFFFu, page, from_lane);
@@ -1111,7 +1120,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
       cp_async_wait<0>();
     } else {
       // -------------------------------------------------------------- Q; rows to convert, to fetch or to look through
-      const int w = warp < 12 ? warp - 10 : warp - 11;
+      const int w = warp < 12 ? warp - 10 : warp - 10 - loaders;
       const bool rows_here = kFp8 || a.box == 0;      // the slots are filled here
       uint32_t kn = 0, q_n = 0, seq = 0;              // key tiles, segments, slots so far
       bool ok = true;
@@ -1133,7 +1142,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           __syncwarp();
         } else {
           const int pieces = D / 8;
-          for (int g = w; g < s.nt * 4; g += kHelpers) {
+          for (int g = w; g < s.nt * 4; g += helpers) {
             const int r = s.row0 + g * 32 + lane;
             int64_t off = -1;
             if (r < s.rows) {
@@ -1178,16 +1187,32 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
         // rows [0, before) and [past, kKeys) of tile n are those that some row may not see
         auto seen_before = [&](int n) { return min(max(s.max_lo - first_of(s, n), 0), kKeys); };
         auto seen_past = [&](int n) { return min(max(s.min_hi - first_of(s, n), 0), kKeys); };
-        // those rows of a slot, `count` from `row0` on, 32 / kLanes at a time with `stride` turns between
+        // those of rows [row0, row1) of a slot, two at a time, the next ones `step` on; four turns under way together
         auto look_through = [&](uint32_t slot_at, int pieces, int row0, int row1, int step, int n) {
           const int c = lane & 15, before = seen_before(n), past = seen_past(n), first = first_of(s, n);
-          for (int row = row0 + (lane >> 4); row < row1; row += step) {
-            if (c >= pieces || (row >= before && row < past)) continue;
-            const uint32_t addr = slot_at + piece(row, c);
-            uint32_t v[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-            if (clean(v, row, first))
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+          for (int row = row0 + (lane >> 4); row < row1; row += 4 * step) {
+            uint32_t v[4][4], ones = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int r = row + u * step;
+              v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0;
+              if (r < row1 && c < pieces && (r < before || r >= past))
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[u][0]), "=r"(v[u][1]), "=r"(v[u][2]), "=r"(v[u][3])
+                             : "r"(slot_at + piece(r, c)) : "memory");
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ones |= (v[u][e] & 0x7F807F80u) + 0x00800080u;
+            if ((ones & 0x80008000u) != 0) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int r = row + u * step;
+                if (clean(v[u], r, first))
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot_at + piece(r, c)), "r"(v[u][0]), "r"(v[u][1]), "r"(v[u][2]),
+                               "r"(v[u][3]) : "memory");
+              }
+            }
           }
           __syncwarp();
         };
@@ -1213,7 +1238,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               for (int part = 0; part < kSlotsPerTile; ++part) {
                 const uint32_t at = seq + (uint32_t)((min(T, n + lead) + n) * kSlotsPerTile + part);
                 if (!wait_warp(ctl->full[at % kSlots], at / kSlots)) { ok = false; break; }
-                look_through(ring + (at % kSlots) * kSlotBytes, min(16, (D - part * 128) / 8), 2 * w, kKeys, 2 * kHelpers, n);
+                look_through(ring + (at % kSlots) * kSlotBytes, min(16, (D - part * 128) / 8), 2 * w, kKeys, 2 * helpers, n);
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
@@ -1258,7 +1283,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                 // swizzle keeps in different banks
                 const int per_row = pieces / 2, c = (lane & 3) | (lane >> 1 & 4);
 #pragma unroll 2
-                for (int row = w * 4 + ((lane >> 2 & 1) | (lane >> 3 & 2)); row < kKeys; row += kHelpers * 4) {
+                for (int row = w * 4 + ((lane >> 2 & 1) | (lane >> 3 & 2)); row < kKeys; row += helpers * 4) {
                   if (c >= per_row) continue;
                   uint4 x;
                   uint32_t word;
@@ -1271,7 +1296,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               } else {
                 // a run of rows for each warp; a lane looks one up
                 if (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1)) { ok = false; break; }
-                constexpr int kRows = (kKeys + kHelpers - 1) / kHelpers;
+                // (more helpers then: 128 / 5 or 9)
+                constexpr int kRows = (kKeys + helpers_of(kFp8) + loaders_of(kFp8) - 2) / (helpers_of(kFp8) + loaders_of(kFp8) - 1);
                 const int row0 = w * kRows, rows = min(kRows, kKeys - row0);
                 const int pos = first_of(s, n) + row0 + lane;
                 int64_t off = -1, soff = 0;
