@@ -318,7 +318,8 @@ struct Ctl {
   uint64_t full[4], empty[4];
   uint64_t st_full[kStages], st_empty[kStages];
   uint64_t q_full, q_empty;
-  uint64_t k_meta[kMeta], v_meta[kMeta];
+  uint64_t k_meta[kMeta];                             // of key tiles, in turn: `live` is there
+  uint64_t v_go[kMeta], v_meta[kMeta];                // of value tiles that some row sees partly: requested; looked through
   uint64_t s_full[2], p_full[2], o_final[2], o_done;
   uint64_t seg_full[2], seg_empty[2];
   uint64_t drained;
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
     mbar_init(smem_u32(&ctl->q_empty), 1);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(smem_u32(&ctl->k_meta[i]), 1);
+      mbar_init(smem_u32(&ctl->v_go[i]), 1);
       mbar_init(smem_u32(&ctl->v_meta[i]), helpers);
     }
     for (int i = 0; i < 2; ++i) {
@@ -448,12 +450,14 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
     const int first = first_of(s, n);
     return first < s.max_lo || first + kKeys > s.min_hi;
   };
-  auto bad_keys = [&](uint32_t kn, int w) {
+  // (of the pc-th such tile. Barriers tell their phases apart by parity alone, so nobody may wait for one that lies two
+  // behind or ahead of where it is: these are counted in tiles that all who meet there wait for.)
+  auto bad_keys = [&](uint32_t pc, int w) {
     uint32_t y = 0;
-    for (int h = 0; h < helpers; ++h) y |= *(volatile uint32_t*)&ctl->v_bad[kn % kMeta][h][w];
+    for (int h = 0; h < helpers; ++h) y |= *(volatile uint32_t*)&ctl->v_bad[pc % kMeta][h][w];
     return y;
   };
-  auto not_finite = [&](uint32_t kn) { return (bad_keys(kn, 0) | bad_keys(kn, 1) | bad_keys(kn, 2) | bad_keys(kn, 3)) != 0; };
+  auto not_finite = [&](uint32_t pc) { return (bad_keys(pc, 0) | bad_keys(pc, 1) | bad_keys(pc, 2) | bad_keys(pc, 3)) != 0; };
   auto arrive = [&](uint64_t& bar) { mbar_arrive(smem_u32(&bar)); };
   uint32_t seg_n = 0;                                 // segments read so far
   auto next_segment = [&](bool whole_warp) {
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     const uint32_t o_t = lanes + kOCol + (uint32_t)(tile * 128);
     uint32_t used[2] = {0, 0};                        // tiles that went through the S buffers
-    uint32_t finals = 0, dones = 0, keys_n = 0;       // o_final and o_done phases; key tiles
+    uint32_t finals = 0, dones = 0, keys_n = 0, pc = 0;   // o_final and o_done phases; key tiles; those some row sees partly
     bool ok = true;
     while (ok && next_segment(true)) {
       const Segment& s = ctl->seg[seg_n & 1];         // read where it lies: registers are for the scores
@@ -649,8 +653,9 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           tmem_st_wait();
           if (place < plain_from || place >= plain_to) {
             // some row does not see all of the tile's keys: values that are not finite must not reach it
-            if (!wait_warp(ctl->v_meta[kn % kMeta], kn / kMeta)) { ok = false; break; }
-            if (not_finite(kn)) {
+            const uint32_t now = pc++;
+            if (!wait_warp(ctl->v_meta[now % kMeta], now / kMeta)) { ok = false; break; }
+            if (not_finite(now)) {
               if (nt == 1 && n > 0 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
               tc_fence_after();
 #pragma unroll 1
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                 }
                 for (int w = 0; w < 4; ++w) {
                   const uint32_t sees = ctl->live[kn % kMeta][w] & bits_below(hi - key0 - 32 * w) & ~bits_below(lo - key0 - 32 * w);
-                  for (uint32_t left = bad_keys(kn, w); left != 0; left &= left - 1) {
+                  for (uint32_t left = bad_keys(now, w); left != 0; left &= left - 1) {
                     const int j = 32 * w + __ffs(left) - 1;
                     if (!__any_sync(0xFFFFFFFFu, (sees >> (j & 31)) & 1u)) continue;   // (past the sequence, maybe: no page)
                     uint32_t pw = tmem_ld1(s_t + (j >> 1));
@@ -783,6 +788,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
       // The second tile's warps stay with a segment of one tile: a barrier's phases are told apart by their parity alone
       if (!kWide && !mine) {
         for (int n = 1; ok && n < s.tiles; n += 2) ok = wait_warp(ctl->s_full[1], used[1] + (n >> 1));
+        for (int n = 0; n < s.tiles; ++n) pc += partly_seen(s, n);
       }
       if (s.nt == 2) {
         used[0] += s.tiles;
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
       // The warp stays together: every lane waits, one issues. (Uniform registers hold the descriptors.)
       {
         const bool leader = elect_one();
-        uint32_t used[2] = {0, 0}, kn = 0, q_n = 0;
+        uint32_t used[2] = {0, 0}, pc = 0, q_n = 0;
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -862,8 +868,9 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               if (!wait_warp(ctl->full[slot], phase)) { ok = false; break; }
               next_slot();
               const bool partly = partly_seen(s, n);
-              if (partly && !wait_warp(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
-              const bool add = n > 0 || (partly && not_finite(kn + n));
+              if (partly && !wait_warp(ctl->v_meta[pc % kMeta], pc / kMeta)) { ok = false; break; }
+              const bool add = n > 0 || (partly && not_finite(pc));
+              pc += partly;
               for (int t = 0; t < 2; ++t) {
                 if (!wait_warp(ctl->p_full[t], used[t] + n)) { ok = false; break; }
                 tc_fence_after();
@@ -906,8 +913,9 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             for (int n = 0; ok && n < T; ++n) {
               if (!wait_warp(ctl->p_full[n & 1], used[n & 1] + (n >> 1))) { ok = false; break; }
               const bool partly = partly_seen(s, n);
-              if (partly && !wait_warp(ctl->v_meta[(kn + n) % kMeta], (kn + n) / kMeta)) { ok = false; break; }
-              const bool add = n > 0 || (partly && not_finite(kn + n));
+              if (partly && !wait_warp(ctl->v_meta[pc % kMeta], pc / kMeta)) { ok = false; break; }
+              const bool add = n > 0 || (partly && not_finite(pc));
+              pc += partly;
               for (int part = 0; part < kSlotsPerTile; ++part) {
                 if (!wait_warp(ctl->full[slot], phase)) { ok = false; break; }
                 tc_fence_after();
@@ -924,7 +932,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             used[1] += T >> 1;
           }
           if (!ok) break;
-          kn += T;
           ++q_n;
           if (leader) arrive(ctl->seg_empty[seg_n & 1]);
           ++seg_n;
@@ -991,7 +998,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
       const bool leader = elect_one();
       const int loader = warp - 12;
       int slot = 0, stage = 0;
-      uint32_t phase = 0, st_phase = 0, kn = 0;
+      uint32_t phase = 0, st_phase = 0, kn = 0, pc = 0;
       bool ok = true;
       while (ok && next_segment(true)) {
         const Segment& s = ctl->seg[seg_n & 1];
@@ -1057,6 +1064,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           }
           for (int part = 0; part < kSlotsPerTile; ++part) {
             if (kFp8 && a.box > 0 ? !wait_warp(ctl->st_empty[stage], st_phase ^ 1u) : !wait_warp(ctl->empty[slot], phase ^ 1u)) { ok = false; break; }
+            if (values && part + 1 == kSlotsPerTile && loader == 0 && partly_seen(s, n)) {
+              if (lane == 0) arrive(ctl->v_go[pc % kMeta]);
+              ++pc;
+            }
             if (a.box > 0) {
               const bool two = !kFp8 && D - part * 128 > 64;   // blocks of 64 values
               const uint32_t dst = kFp8 ? stages + (uint32_t)(stage * kStageBytes) : ring + (uint32_t)(slot * kSlotBytes);
@@ -1122,7 +1133,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
       // -------------------------------------------------------------- Q; rows to convert, to fetch or to look through
       const int w = warp < 12 ? warp - 10 : warp - 10 - loaders;
       const bool rows_here = kFp8 || a.box == 0;      // the slots are filled here
-      uint32_t kn = 0, q_n = 0, seq = 0;              // key tiles, segments, slots so far
+      uint32_t pc = 0, q_n = 0, seq = 0;              // tiles that some row sees partly, segments, slots so far
       bool ok = true;
       while (ok && next_segment(true)) {
         const Segment& s = ctl->seg[seg_n & 1];
@@ -1216,34 +1227,31 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           }
           __syncwarp();
         };
-        auto note = [&](int m, bool partly) {         // a value tile is through
-          if (partly) {
+        auto note = [&] {                             // a value tile that some row sees partly is through
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, bad[x]);
-              if (lane == x) ctl->v_bad[m][w][x] = any;
-              bad[x] = 0;
-            }
-            __syncwarp();
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, bad[x]);
+            if (lane == x) ctl->v_bad[pc % kMeta][w][x] = any;
+            bad[x] = 0;
           }
-          if (lane == 0) arrive(ctl->v_meta[m]);
+          __syncwarp();
+          if (lane == 0) arrive(ctl->v_meta[pc % kMeta]);
+          ++pc;
         };
         if (!rows_here) {
-          // value tiles that some row sees partly, once they have landed
+          // value tiles that some row sees partly, once they have landed (and not before they are asked for: the slot's
+          // barrier may be a phase behind)
           for (int n = 0; ok && n < T; ++n) {
-            const int m = (kn + n) % kMeta;
-            if (!wait_warp(ctl->k_meta[m], (kn + n) / kMeta)) { ok = false; break; }   // (not further ahead than the ring)
-            const bool partly = partly_seen(s, n);
-            if (partly) {
-              for (int part = 0; part < kSlotsPerTile; ++part) {
-                const uint32_t at = seq + (uint32_t)((min(T, n + lead) + n) * kSlotsPerTile + part);
-                if (!wait_warp(ctl->full[at % kSlots], at / kSlots)) { ok = false; break; }
-                look_through(ring + (at % kSlots) * kSlotBytes, min(16, (D - part * 128) / 8), 2 * w, kKeys, 2 * helpers, n);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
+            if (!partly_seen(s, n)) continue;
+            if (!wait_warp(ctl->v_go[pc % kMeta], pc / kMeta)) { ok = false; break; }
+            for (int part = 0; part < kSlotsPerTile; ++part) {
+              const uint32_t at = seq + (uint32_t)((min(T, n + lead) + n) * kSlotsPerTile + part);
+              if (!wait_warp(ctl->full[at % kSlots], at / kSlots)) { ok = false; break; }
+              look_through(ring + (at % kSlots) * kSlotBytes, min(16, (D - part * 128) / 8), 2 * w, kKeys, 2 * helpers, n);
             }
-            if (ok) note(m, partly);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (ok) note();
           }
           seq += (uint32_t)(2 * T * kSlotsPerTile);
         } else {
@@ -1251,7 +1259,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           while (ok && next_v < T) {
             const bool values = next_k == min(T, next_v + lead);
             const int n = values ? next_v++ : next_k++;
-            const int m = (kn + n) % kMeta;
             const bool partly = values && partly_seen(s, n);
             for (int part = 0; part < kSlotsPerTile; ++part, ++seq) {
               const uint32_t dst = ring + (seq % kSlots) * kSlotBytes;
@@ -1341,11 +1348,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               __syncwarp();
               if (lane == 0) arrive(ctl->full[seq % kSlots]);
             }
-            if (ok && values) note(m, partly);
+            if (ok && partly) note();
           }
         }
         if (!ok) break;
-        kn += T;
         ++q_n;
         __syncwarp();
         if (lane == 0) arrive(ctl->seg_empty[seg_n & 1]);

@@ -404,3 +404,20 @@ def test_pairs_of_tiles_and_single_ones_in_turn(slopes):
                                              slopes=None if sl is None else P.dev(sl, torch.float32))
     assert int(err) == 0
     P.check_prompt(cache, table, new, new, q, out, lse, 64 ** -0.5, slopes=sl)
+
+
+def test_few_new_tokens_over_long_caches_many_times():
+    """Drafted tokens: one tile of rows, key tiles that are cut between blocks, and nothing behind a sequence's last key that
+    may be used. Every call gives the same bits."""
+    E = H.pkg()
+    new, lens = [5] * 32, [1024 + 97 * b for b in range(32)]
+    cache, table = H.filled(lens, 64, 8, 128, "bf16", 42)
+    q = randn(43, (160, 32, 128))
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    ws, err = E.prompt_workspace(cache, 32, 160, 32), word()
+    out, lse = E.engram_prompt_attention(cache, q, *args, lse=True, workspace=ws, err=err)
+    P.check_prompt(cache, table, new, lens, q, out, lse, 128 ** -0.5)
+    for _ in range(30):
+        again = E.engram_prompt_attention(cache, q, *args, lse=True, workspace=ws, err=err)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    assert int(err) == 0
