@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), !kFp8 && a.box > 0 ? loaders : helpers);
+      mbar_init(smem_u32(&ctl->full[s]), a.box == 0 ? helpers : kFp8 ? helpers / 2 : loaders);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -1285,12 +1285,20 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               };
               if (kFp8 && a.box > 0) {
                 const uint32_t st = seq % kStages, from = stages + st * kStageBytes;
-                if (!wait_warp(ctl->st_full[st], seq / kStages) || (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1))) { ok = false; break; }
+                // Half of the warps take a slot, the others the next one: what a slot costs beside the conversion (barriers, the
+                // fence) is then hidden behind the other's. All wait for every stage and give it back, so that no barrier is two
+                // phases away from anyone who waits for it (a slot's is behind its stage's)
+                if (!wait_warp(ctl->st_full[st], seq / kStages)) { ok = false; break; }
+                if ((int)(seq & 1u) != (w >> 2)) {
+                  if (lane == 0) arrive(ctl->st_empty[st]);
+                  continue;
+                }
+                if (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1)) { ok = false; break; }
                 // a lane takes 16 codes of a row: eight lanes that store at once have four pieces of two rows, which the
                 // swizzle keeps in different banks
                 const int per_row = pieces / 2, c = (lane & 3) | (lane >> 1 & 4);
-#pragma unroll 2
-                for (int row = w * 4 + ((lane >> 2 & 1) | (lane >> 3 & 2)); row < kKeys; row += helpers * 4) {
+#pragma unroll 1
+                for (int row = (w & 3) * 4 + ((lane >> 2 & 1) | (lane >> 3 & 2)); row < kKeys; row += helpers * 2) {
                   if (c >= per_row) continue;
                   uint4 x;
                   uint32_t word;
