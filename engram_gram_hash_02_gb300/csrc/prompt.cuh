@@ -1263,7 +1263,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             for (int part = 0; part < kSlotsPerTile; ++part, ++seq) {
               const uint32_t dst = ring + (seq % kSlots) * kSlotBytes;
               const int pieces = min(16, (D - part * 128) / 8);
-              const int before = seen_before(n), past = seen_past(n), first = first_of(s, n);
               // codes (16 of a row) to bf16
               auto convert = [&](const uint4& x, float scale, int row, int c) {
                 const uint32_t codes[4] = {x.x, x.y, x.z, x.w};
@@ -1279,7 +1278,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                     y[2 * z] = pack_bf16(g0.x, g0.y);
                     y[2 * z + 1] = pack_bf16(g1.x, g1.y);
                   }
-                  if (partly && (row < before || row >= past)) clean(y, row, first);
                   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + piece(row, 2 * c + e)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
                 }
               };
@@ -1308,6 +1306,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                 }
                 __syncwarp();
                 if (lane == 0) arrive(ctl->st_empty[st]);
+                if (partly) {                         // (the same rows: four of every sixteen)
+                  look_through(dst, pieces, (w & 3) * 4, kKeys, helpers * 2, n);
+                  look_through(dst, pieces, (w & 3) * 4 + 2, kKeys, helpers * 2, n);
+                }
               } else {
                 // a run of rows for each warp; a lane looks one up
                 if (seq >= kSlots && !wait_warp(ctl->empty[seq % kSlots], seq / kSlots - 1)) { ok = false; break; }
@@ -1334,8 +1336,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                   }
                   cp_async_commit();
                   cp_async_wait<0>();
-                  __syncwarp();
-                  if (partly) look_through(dst, pieces, row0, row0 + rows, 2, n);
                 } else {
                   uint32_t word = 0;
                   if (off >= 0) word = *reinterpret_cast<const uint32_t*>((values ? p.cache.vs : p.cache.ks) + soff + 4 * part);
@@ -1351,6 +1351,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                     }
                   }
                 }
+                __syncwarp();
+                if (partly) look_through(dst, pieces, row0, row0 + rows, 2, n);
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
