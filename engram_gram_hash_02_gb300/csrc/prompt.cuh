@@ -6,9 +6,9 @@
 // head, so that a key row is used by all of them; 128 rows make a tile (the MMA's M), two tiles share every key and value
 // tile that is brought in (heads of up to 128; one tile for wider heads, whose sums fill tensor memory).
 //
-// One CTA per SM, 16 warps with roles of their own, joined by mbarriers only:
+// One CTA per SM, 16 warps (FP8: 20) with roles of their own, joined by mbarriers only:
 //   warps 0..3, 4..7   softmax of tile 0 and 1: a thread has a row. S (fp32) comes from tensor memory, P goes back there
-//                      as bf16, in S's place; o is multiplied there only when the maximum grows by more than 2^8
+//                      as bf16, in S's place; o is multiplied there only when the maximum grows by more than 2^30
 //   warp 8             issues the MMAs:  S = Q K^T (both from shared memory),  O += P V (P from tensor memory, V as it
 //                      lies, by rows of keys: an MN-major operand)
 //   warp 9             walks the CTA's share of the work and hands segments (a run of key tiles of one pair of tiles) out
@@ -16,8 +16,8 @@
 //                      the cache's own layout, up to 64 tokens of a page at once. bf16 goes to a ring of 32 KB slots
 //                      that the MMAs read, FP8 to stages
 //   warps 10, 11, 14, 15 (FP8: ..19)   bring Q in, look through values (below); FP8: convert a stage's rows to bf16 into the
-//                      ring (exact). Pages that are no multiple of 8 tokens do not divide into boxes: these warps, and all
-//                      loaders but one, then fetch the rows themselves
+//                      ring (exact), half of them a slot in turn. Pages that are no multiple of 8 tokens do not divide
+//                      into boxes: these warps, and all loaders but one, then fetch the rows themselves
 // While the softmax of one tile runs, the tensor cores work on the other; with one tile, on the next key tile.
 //
 // Work is cut at key tiles: a first kernel (one CTA) lists the pairs of tiles with the hull of their keys, and every CTA
@@ -532,15 +532,19 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             }
             tmem_st_wait();
           }
-          // Half a tile at a time, in a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
+          // Scores at a time: half a tile; a quarter over FP8 where 144 registers do not hold the form or the wide loop beside
+          // half a tile's (8192 tokens capped at 30: 998 us against 1086; heads of 256: 1027 against 1100; elsewhere halves are
+          // better, bf16 467 against 499)
+          constexpr int kCols = kFp8 && (kWide || kForm) ? 32 : 64;
+          // In a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
           // exponentials are formed with the maximum so far, while the half's own is found: o, the sum and P are in units of
           // 2^m, m a whole number that follows the true maximum only when that is kLag beyond it, which hardly ever happens
           // after the first tile; then the half is done again.
 #pragma unroll 1
-          for (int c = 0; c < kKeys; c += 64) {
-            float x[64];
+          for (int c = 0; c < kKeys; c += kCols) {
+            float x[kCols];
             tmem_ld32(s_t + c, x);
-            tmem_ld32(s_t + c + 32, x + 32);
+            if constexpr (kCols == 64) tmem_ld32(s_t + c + 32, x + 32);
             tmem_ld_wait();
             hold(x);
             if (kForm) {
@@ -548,7 +552,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               if (only_cap) {
                 // cap tanh(y) = cap - 2 cap / (1 + exp(2 y)): x becomes the negative reciprocal
 #pragma unroll
-                for (int j = 0; j < 64; j += 2) {
+                for (int j = 0; j < kCols; j += 2) {
                   const float2 z = mul2({x[j], x[j + 1]}, {to_exp, to_exp});
                   const float2 e = fma2({ex2(z.x), ex2(z.y)}, {-1.f, -1.f}, {-1.f, -1.f});
                   x[j] = rcp(e.x);
@@ -557,23 +561,23 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               } else if (p.form.cap2 > 0.f) {
                 const float y1 = p.scale_log2 * p.form.cap_inv;
 #pragma unroll
-                for (int j = 0; j < 64; j += 2) {
+                for (int j = 0; j < kCols; j += 2) {
                   const float2 y = capped2({x[j], x[j + 1]}, y1, p.form.cap2);
                   x[j] = y.x;
                   x[j + 1] = y.y;
                 }
               } else {
 #pragma unroll
-                for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
+                for (int j = 0; j < kCols; ++j) x[j] *= p.scale_log2;
               }
               if (p.form.slopes != nullptr) {
                 const float back = (float)(pos - key0 - c);
 #pragma unroll
-                for (int j = 0; j < 64; ++j) x[j] = fmaf(-slope, fabsf(back - (float)j), x[j]);
+                for (int j = 0; j < kCols; ++j) x[j] = fmaf(-slope, fabsf(back - (float)j), x[j]);
               }
               if (!full) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
+                for (int w = 0; w < kCols / 32; ++w) {
                   const uint32_t sees = ctl->live[kn % kMeta][c / 32 + w] & bits_below(hi - key0 - c - 32 * w) & ~bits_below(lo - key0 - c - 32 * w);
 #pragma unroll
                   for (int j = 0; j < 32; ++j)
@@ -585,19 +589,19 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = max3(x[e], x[4 + e], x[8 + e]);
 #pragma unroll
-            for (int j = 12; j < 60; j += 8)
+            for (int j = 12; j < kCols - 4; j += 8)
 #pragma unroll
               for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
-            float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[60], max3(x[61], x[62], x[63])));
+            float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[kCols - 4], max3(x[kCols - 3], x[kCols - 2], x[kCols - 1])));
             top = fmaf(top, times, plus);
             if (n == 0 && c == 0) m = ceilf(top);     // (nothing is summed yet)
             const bool grown = top > m + kLag;
             const float base = m == -INFINITY ? 0.f : m;
             const float2 times2 = {times, times}, plus2 = {plus - base, plus - base};
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            uint32_t w[32];
+            uint32_t w[kCols / 2];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < kCols / 2; ++j) {
               const float2 xx = {x[2 * j], x[2 * j + 1]};
               const float2 y = fma2(xx, times2, plus2);
               const float2 e = {ex2(y.x), ex2(y.y)};
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                 tmem_st_wait();                       // this tile's P so far
                 const __nv_bfloat162 by = __float2bfloat162_rn(alpha);
 #pragma unroll 1
-                for (int d = 0; d < 32; d += 16) {
+                for (int d = 0; d < c / 2; d += 16) {
                   float y[16];
                   tmem_ld16(s_t + d, reinterpret_cast<uint32_t*>(y));
                   tmem_ld_wait();
@@ -641,11 +645,11 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                   tmem_st16(s_t + d, reinterpret_cast<const uint32_t*>(y));
                 }
               }
-              c -= 64;
+              c -= kCols;
               continue;
             }
             tmem_st16(s_t + c / 2, w);                // over scores that have been read
-            tmem_st16(s_t + c / 2 + 16, w + 16);
+            if constexpr (kCols == 64) tmem_st16(s_t + c / 2 + 16, w + 16);
             const float2 sums = add2(sum[0], sum[1]);
             l += sums.x + sums.y;
           }
@@ -713,15 +717,15 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
         const int h = s.head * G + g;
         if (s.whole && p.out != nullptr) {
           // through shared memory, so that rows leave in longer pieces than a thread's 16 bytes
-          constexpr int kPieces = staging_pieces(kFp8), kCols = 8 * kPieces;
+          constexpr int kPieces = staging_pieces(kFp8), kStaged = 8 * kPieces;
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const int64_t row = token * p.out_ts + (int64_t)h * p.out_hs;
           const uint32_t stage = staging + (uint32_t)(warp * staging_bytes(kFp8));
           auto place = [&](int r, int c) { return stage + (uint32_t)(r * 16 * kPieces + ((c ^ ((r * kPieces >> 3) & (kPieces - 1))) << 4)); };
 #pragma unroll 1
-          for (int d = 0; d < D; d += kCols) {
-            float y[kCols];
-            if (kCols == 32) tmem_ld32(o_t + d, y); else tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
+          for (int d = 0; d < D; d += kStaged) {
+            float y[kStaged];
+            if (kStaged == 32) tmem_ld32(o_t + d, y); else tmem_ld16(o_t + d, reinterpret_cast<uint32_t*>(y));
             tmem_ld_wait();
             hold(y);
 #pragma unroll

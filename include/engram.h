@@ -622,7 +622,8 @@ int engram_attention_step(const EngramNormRope* nr, const EngramKVCache* cache, 
  * A form of scores, for the calls that take one (NULL: none). With x_j = scale * <q_h, k_j>, query position p
  * and key position j:
  *     s_j = (cap > 0 ? cap * tanh(x_j / cap) : x_j) - slopes_h * |p - j|
- *   cap     0: scores are not capped. Else in [2^-60, 2^60]; a capped score is off by 2^-19 of itself at most
+ *   cap     0: scores are not capped. Else in [2^-60, 2^60]; a capped score is off by 2^-19 of itself at most (of prompts
+ *           and shared prefixes with a cap of up to 128 and no slopes: by 2^-21 of the cap)
  *   slopes  device fp32 [q_heads], 4-byte aligned, or NULL: no bias
  */
 typedef struct EngramScores {
@@ -678,9 +679,11 @@ size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  *   out         bf16 rows [T, q_heads, head_dim]       lse  device fp32 [T, q_heads], or NULL
  *   workspace   as engram_paged_attention (the same zeroed start); one may serve all the attention calls in order
  * T * q_heads / kv_heads < 2^31. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
- * (a code times a power of two; below 2^-133 rounded), and weights exp(s_j - m), m the running maximum as it was last
- * moved (within 2^8 of the true one), are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32.
- * Results do not depend on timing. Two launches, the first of one CTA, chained with programmatic dependent launch.
+ * (a code times a power of two; below 2^-133 rounded), and weights 2^(s_j log2(e) - m), m a whole number that the running
+ * maximum may be up to 30 ahead of, are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32:
+ * values times the number of keys seen should stay below 2^97, or a sum may overflow. Results do not depend on timing. Two
+ * launches, the first of one CTA, and a third that joins cut work where tokens are few, chained with programmatic dependent
+ * launch.
  */
 int engram_prompt_attention(const EngramKVCache* cache, const EngramPagedSeqs* seqs, int64_t T,
                             const int32_t* cu_seqlens, const EngramHeads* q, float scale, const EngramVisible* visible,
@@ -704,7 +707,7 @@ size_t engram_shared_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  *   out, lse, scores, err_flag  as engram_paged_attention2; over all of a sequence's keys
  *   workspace     engram_shared_workspace_bytes; its zeroed start as engram_paged_attention
  * The prefix's part is summed as in engram_prompt_attention, the own part as in engram_paged_attention; they are
- * joined in fp32. Three launches.
+ * joined in fp32. Three launches, or four (engram_prompt_attention's, then engram_paged_attention's).
  */
 int engram_shared_attention(const EngramKVCache* cache, const EngramPagedSeqs* prefix, const int32_t* group_starts,
                             const EngramPagedSeqs* seqs, const EngramHeads* q, float scale, const EngramScores* scores,
