@@ -538,8 +538,9 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           constexpr int kCols = kFp8 && (kWide || kForm) ? 32 : 64;
           // In a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
           // exponentials are formed with the maximum so far, while the half's own is found: o, the sum and P are in units of
-          // 2^m, m a whole number that follows the true maximum only when that is kLag beyond it, which hardly ever happens
-          // after the first tile; then the half is done again.
+          // 2^m, and m follows the true maximum only when that is kLag beyond it, which hardly ever happens after the first
+          // tile; then the half is done again. m itself is no whole number, so that the largest weight (a row's only one, where
+          // it sees one key) is 1 and loses nothing as bf16: rows of documents of a few tokens were off by up to 2^-8 for it.
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += kCols) {
             float x[kCols];
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
             float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[kCols - 4], max3(x[kCols - 3], x[kCols - 2], x[kCols - 1])));
             top = fmaf(top, times, plus);
-            if (n == 0 && c == 0) m = ceilf(top);     // (nothing is summed yet)
+            if (n == 0 && c == 0) m = top;            // (nothing is summed yet)
             const bool grown = top > m + kLag;
             const float base = m == -INFINITY ? 0.f : m;
             const float2 times2 = {times, times}, plus2 = {plus - base, plus - base};
@@ -609,8 +610,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               w[j] = pack_bf16(e.x, e.y);
             }
             if (__any_sync(0xFFFFFFFFu, grown)) {
-              const float to = grown ? ceilf(top) : m;
-              const float alpha = grown ? ex2(m - to) : 1.f;  // a power of two: exact, also for P
+              const float to = grown ? top : m;
+              const float alpha = grown ? ex2(m - to) : 1.f;  // 2^-30 at most: what it rounds (P, too) hardly counts any more
               m = to;
               l *= alpha;
               if (n > 0) {

@@ -679,8 +679,8 @@ size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  *   out         bf16 rows [T, q_heads, head_dim]       lse  device fp32 [T, q_heads], or NULL
  *   workspace   as engram_paged_attention (the same zeroed start); one may serve all the attention calls in order
  * T * q_heads / kv_heads < 2^31. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
- * (a code times a power of two; below 2^-133 rounded), and weights 2^(s_j log2(e) - m), m a whole number that the running
- * maximum may be up to 30 ahead of, are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32:
+ * (a code times a power of two; below 2^-133 rounded), and weights 2^(s_j log2(e) - m), m the running maximum or up to
+ * 30 behind it, are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32:
  * values times the number of keys seen should stay below 2^97, or a sum may overflow. Results do not depend on timing. Two
  * launches, the first of one CTA, and a third that joins cut work where tokens are few, chained with programmatic dependent
  * launch.

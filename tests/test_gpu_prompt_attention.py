@@ -421,3 +421,18 @@ def test_few_new_tokens_over_long_caches_many_times():
         again = E.engram_prompt_attention(cache, q, *args, lse=True, workspace=ws, err=err)
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("D,cap,slopes,fmt", [(128, 0.0, False, "bf16"), (64, 0.0, True, "bf16"), (128, 30.0, False, "bf16"), (192, 0.0, False, "fp8"),
+                                              (128, 50.0, True, "fp8"), (256, 300.0, False, "bf16")])
+def test_a_token_that_sees_one_key_gives_its_value(D, cap, slopes, fmt):
+    """The only weight is 1 up to 2^-18 (of scores up to 2^6), so that a value that bf16 holds comes out as it is."""
+    E = H.pkg()
+    new = [300, 1, 77]
+    cache, table = H.filled(new, 16, 2, D, fmt, 44)
+    q = randn(45, (378, 8, D))
+    at = np.concatenate([np.arange(n) for n in new])
+    args = dict(cap=cap, slopes=P.dev(P.alibi(8), torch.float32) if slopes else None)
+    out = E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(new), doc_starts=P.dev(at), **args)
+    values = np.concatenate([P.rows_of(cache, table, b, n)[1] for b, n in enumerate(new)])
+    assert np.array_equal(out.double().cpu().numpy(), np.repeat(values, 4, axis=1))
