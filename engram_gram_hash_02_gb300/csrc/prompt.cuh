@@ -29,6 +29,11 @@
 // them.
 //
 // Roundings below 32 bits: P to bf16 (2^-8 of itself at most). The sums take P before that.
+//
+// Measured (one GB300, 8192 tokens of one prompt, 32 / 8 heads of 128): bf16 467 us, 1.18 PFLOP/s, the tensor pipe 56 % busy; a
+// cap 811 us, slopes 675, FP8 720. Heads of 256 (16 / 2): 592 us, bound by key and value tiles from L2 for every 128 rows
+// (without softmax and MMAs 425). Without the softmax heads of 128 take 363 us: its latency per tile is what bounds them, and over FP8 the
+// codes' conversion beside it.
 #pragma once
 
 #include "attn.cuh"
