@@ -436,3 +436,54 @@ def test_a_token_that_sees_one_key_gives_its_value(D, cap, slopes, fmt):
     out = E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(new), doc_starts=P.dev(at), **args)
     values = np.concatenate([P.rows_of(cache, table, b, n)[1] for b, n in enumerate(new)])
     assert np.array_equal(out.double().cpu().numpy(), np.repeat(values, 4, axis=1))
+
+
+@pytest.mark.parametrize("new,old,page,Hq,Hk,D,mask", [
+    ([300], [40], 5, 8, 2, 128, "docs"), ([130, 7, 260], [0, 500, 3], 12, 3, 3, 192, "causal"), ([515], [100], 1, 4, 1, 64, "window"),
+    ([200, 90], [0, 700], 20, 16, 2, 256, "prefix")])
+def test_fp8_pages_that_do_not_divide_into_boxes(new, old, page, Hq, Hk, D, mask):
+    test_prompts_match_the_formula(new, old, page, Hq, Hk, D, "fp8", "hnd", mask, 0.0, False)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("D,page", [(128, 64), (256, 16), (256, 5), (160, 32), (128, 6)])
+def test_values_that_are_not_finite_stay_with_those_that_see_them(fmt, D, page):
+    """Heads of one and of two tiles, boxes and rows, work that is cut between CTAs: NaN in one position of some values."""
+    E, new, lens = H.pkg(), [700, 333], [700, 1000]
+    cache, table = H.filled(lens, page, 2, D, fmt, 46)
+    q = randn(47, (1033, 8, D))
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    doc = documents(new, lens, 60, 5)
+    how = dict(doc_starts=P.dev(doc), lse=True)
+    want, want_lse = E.engram_prompt_attention(cache, q, *args, **how)
+    P.check_prompt(cache, table, new, lens, q, want, want_lse, D ** -0.5, doc_starts=doc)
+    bad = {0: [0, 90, 311, 640], 1: [667, 800, 999]}
+    at = D - 3
+    for b, keys in bad.items():
+        for j in keys:
+            s = H.slots_of(table, b, j, j + 1, page)[0]
+            cache.v[s // page, :, s % page, at] = float("nan") if fmt == "bf16" else 0x7F
+    out, lse = E.engram_prompt_attention(cache, q, *args, **how)
+    hit, t0 = np.zeros(1033, bool), 0
+    for b, (n, m) in enumerate(zip(new, lens)):
+        for i in range(n):
+            hit[t0 + i] = any(doc[t0 + i] <= j <= m - n + i for j in bad[b])
+        t0 += n
+    assert 50 < hit.sum() < 1000
+    hit = torch.from_numpy(hit).to(DEV)
+    assert torch.equal(lse, want_lse)
+    assert torch.isnan(out[hit][..., at]).all()
+    assert torch.equal(out[~hit], want[~hit])
+    rest = [d for d in range(D) if d != at]
+    # the other positions of rows that see one: its products are added one by one, in another order of fp32 sums
+    assert torch.isfinite(out[hit][..., rest]).all()
+    assert float((out[hit][..., rest].double() - want[hit][..., rest].double()).abs().max()) <= 2.0 ** -7 * float(want.double().abs().max())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_scales_that_are_not_positive(scale):
+    E, new, lens = H.pkg(), [300], [420]
+    cache, table = H.filled(lens, 16, 2, 128, "bf16", 48)
+    q = randn(49, (300, 8, 128))
+    out, lse = E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(lens), scale=scale, lse=True)
+    P.check_prompt(cache, table, new, lens, q, out, lse, scale)
