@@ -138,21 +138,25 @@ __device__ __forceinline__ float2* part_ml(float* slot, int R, int D, int r) {
 }
 __device__ __forceinline__ float ex2_rel(float x, float m) { return ex2(x - (m == -INFINITY ? 0.f : m)); }
 
-// 16 values of a row from value d on, and (with d 0) its log-sum-exp
-__device__ __forceinline__ void emit16(const PromptParams& p, int64_t token, int h, int d, const float (&o)[16], float m, float l) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+// 16 values of a row from value d on, and (with d 0) its log-sum-exp. A row without a weight is zero by a select, not by a
+// product: the MMAs have multiplied its weights of zero with values that may be infinite, and its sums are NaN then
+__device__ __forceinline__ void emit16(const PromptParams& p, int64_t token, int h, int d, const float (&sums)[16], float m, float l) {
+  const float inv = 1.f / l;
+  float o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : sums[i] * inv;
   const int64_t row = token * (p.Hk * p.G) + h;
   if (p.out != nullptr) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
     uint4* dst = reinterpret_cast<uint4*>(p.out + token * p.out_ts + (int64_t)h * p.out_hs + d);
     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
   } else {
     float4* dst = reinterpret_cast<float4*>(p.prior_o + row * p.D + d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
   }
   if (d == 0) {
     const float sum = l == 0.f ? -INFINITY : m + log2f(l);
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
         if (s.whole && p.out != nullptr) {
           // through shared memory, so that rows leave in longer pieces than a thread's 16 bytes
           constexpr int kPieces = staging_pieces(kFp8), kStaged = 8 * kPieces;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float inv = 1.f / l;
           const int64_t row = token * p.out_ts + (int64_t)h * p.out_hs;
           const uint32_t stage = staging + (uint32_t)(warp * staging_bytes(kFp8));
           auto place = [&](int r, int c) { return stage + (uint32_t)(r * 16 * kPieces + ((c ^ ((r * kPieces >> 3) & (kPieces - 1))) << 4)); };
@@ -735,10 +739,12 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             tmem_ld_wait();
             hold(y);
 #pragma unroll
+            for (int e = 0; e < kStaged; ++e) y[e] = l == 0.f ? 0.f : y[e] * inv;   // (see emit16)
+#pragma unroll
             for (int c = 0; c < kPieces; ++c) {
               uint32_t v[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = pack_bf16(y[8 * c + 2 * e] * inv, y[8 * c + 2 * e + 1] * inv);
+              for (int e = 0; e < 4; ++e) v[e] = pack_bf16(y[8 * c + 2 * e], y[8 * c + 2 * e + 1]);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(lane, c)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
             }
             __syncwarp();

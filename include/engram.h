@@ -665,8 +665,8 @@ size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  * Attention of all new tokens of ragged sequences over their cached tokens: prompts, chunks of prompts, drafted
  * tokens. Their keys and values are in the cache already (seq_lens counts them). Query head h reads key head
  * h / (q_heads / kv_heads); out_h = sum_j exp(s_j) v_j / sum_j exp(s_j), lse_h = log sum_j exp(s_j) over the keys
- * that the token sees. A token that sees nothing, or whose scores are all -inf, gives zeros and lse -inf. What
- * lies in keys and values that a token does not see has no part in its result, whatever it is.
+ * that the token sees. A token that sees nothing, or whose scores are all -inf, gives zeros and lse -inf, whatever the
+ * values. What lies in keys and values that a token does not see has no part in its result, whatever it is.
  *   q           bf16 rows [T, q_heads, head_dim]; q_heads a multiple of kv_heads
  *   cu_seqlens  device int32 [batch + 1]: sequence b's new tokens are rows [cu[b], cu[b + 1]). Rows before cu[0] and
  *               from cu[batch] on belong to no sequence and are left as they were. Values outside [0, T] are clamped
