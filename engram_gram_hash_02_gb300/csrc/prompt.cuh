@@ -128,7 +128,8 @@ __device__ __forceinline__ void visible(const PromptParams& p, int s0, int n, in
   hi = len;
   if (p.causal) hi = min(len, max(pos + 1, p.prefix_ends != nullptr ? __ldcg(p.prefix_ends + t) : 0));
   if (p.window > 0 && pos + 1 > p.window) lo = pos + 1 - p.window;
-  if (p.doc_starts != nullptr) lo = max(lo, __ldcg(p.doc_starts + t));
+  // (no further than the keys: any number may stand there, and what follows adds a tile's keys to it)
+  if (p.doc_starts != nullptr) lo = max(lo, min(__ldcg(p.doc_starts + t), len));
 }
 
 // ---- parts of cut pairs: o [D / 4][rows of a pair] of 4 floats, then (m, sum) [rows] ------------------------------

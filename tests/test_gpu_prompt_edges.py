@@ -60,3 +60,24 @@ def test_scores_that_are_all_minus_infinity_give_zeros_whatever_the_values(D):
     spoil(cache, table, 0, 150, D - 2)
     out, lse = E.engram_prompt_attention(cache, q, P.dev([0, 200]), P.dev(table), P.dev(lens), causal=False, lse=True)
     assert not out.any() and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("fmt,D,slopes", [("bf16", 64, False), ("bf16", 256, False), ("fp8", 128, True)])
+def test_masks_of_the_types_extremes(fmt, D, slopes):
+    """Documents that start at the largest and the smallest number there is, and prefixes that end there."""
+    E, new, lens = H.pkg(), [200, 130, 300], [500, 130, 300]
+    cache, table = H.filled(lens, 16, 2, D, fmt, 64)
+    T = sum(new)
+    q = randn(65, (T, 8, D))
+    top, low = 2 ** 31 - 1, -2 ** 31
+    doc, ends = np.zeros(T, np.int32), np.zeros(T, np.int32)
+    for i, x in enumerate((top, low, top - 126, top - 127, 2 ** 31 - 256, 100)):
+        doc[5 + 3 * i::40] = x
+    ends[200:330:9] = top
+    ends[203:330:9] = low
+    sl = P.alibi(8) if slopes else None
+    out, lse = torch.full_like(q, 7.0), torch.full((T, 8), 7.0, device=DEV)
+    E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(lens), doc_starts=P.dev(doc), prefix_ends=P.dev(ends),
+                              slopes=None if sl is None else P.dev(sl, torch.float32), out=out, lse=lse)
+    assert not out[5::40].any() and bool(torch.isneginf(lse[5::40]).all())
+    P.check_prompt(cache, table, new, lens, q, out, lse, D ** -0.5, doc_starts=doc, prefix_ends=ends, slopes=sl)
