@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           // In a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
           // exponentials are formed with the maximum so far, while the half's own is found: o, the sum and P are in units of
           // 2^m, and m follows the true maximum only when that is kLag beyond it, which hardly ever happens after the first
-          // tile; then the half is done again. m itself is no whole number, so that the largest weight (a row's only one, where
-          // it sees one key) is 1 and loses nothing as bf16: rows of documents of a few tokens were off by up to 2^-8 for it.
+          // tile; then the half is done again. At first m is that maximum and no whole number, so that the largest weight (a row's
+          // only one, where it sees one key) is 1 and loses nothing as bf16: rows of documents of a few tokens were off by up to 2^-8 for it.
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += kCols) {
             float x[kCols];
@@ -620,9 +620,13 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               w[j] = pack_bf16(e.x, e.y);
             }
             if (__any_sync(0xFFFFFFFFu, grown)) {
-              const float to = grown ? top : m;
-              const float alpha = grown ? ex2(m - to) : 1.f;  // 2^-30 at most: what it rounds (P, too) hardly counts any more
-              m = to;
+              // m moves by a whole number, so that what there is so far is multiplied by a power of two: this tile's P, whose
+              // weights may be 2^30 and come to as much as 1 now, keeps the one rounding it has had, and O and the sum theirs
+              // (by the maximum's own growth, P was rounded three times and off by 2.3 * 2^-8). Over 2^126 and from a maximum
+              // of -inf nothing is left of it, and m is the maximum
+              const float by = ceilf(top - m);
+              const float alpha = !grown ? 1.f : by < 127.f ? __uint_as_float((uint32_t)(127 - (int)by) << 23) : 0.f;
+              if (grown) m = by < 127.f ? m + by : top;
               l *= alpha;
               if (n > 0) {
                 if (nt == 1 && !wait_warp(ctl->o_done, dones + n - 1)) { ok = false; break; }
@@ -640,7 +644,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               }
               if (c > 0) {
                 tmem_st_wait();                       // this tile's P so far
-                const __nv_bfloat162 by = __float2bfloat162_rn(alpha);
+                const __nv_bfloat162 alpha2 = __float2bfloat162_rn(alpha);   // exact
 #pragma unroll 1
                 for (int d = 0; d < c / 2; d += 16) {
                   float y[16];
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
 #pragma unroll
                   for (int e = 0; e < 16; ++e) {
                     __nv_bfloat162 z = *reinterpret_cast<__nv_bfloat162*>(&y[e]);
-                    z = __hmul2(z, by);
+                    z = __hmul2(z, alpha2);
                     y[e] = *reinterpret_cast<float*>(&z);
                   }
                   tmem_st16(s_t + d, reinterpret_cast<const uint32_t*>(y));

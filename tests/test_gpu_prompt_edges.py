@@ -81,3 +81,59 @@ def test_masks_of_the_types_extremes(fmt, D, slopes):
                               slopes=None if sl is None else P.dev(sl, torch.float32), out=out, lse=lse)
     assert not out[5::40].any() and bool(torch.isneginf(lse[5::40]).all())
     P.check_prompt(cache, table, new, lens, q, out, lse, D ** -0.5, doc_starts=doc, prefix_ends=ends, slopes=sl)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("D,form", [(64, False), (64, True), (192, False)])
+def test_scores_that_rise_by_thirty_within_a_tile_of_keys(fmt, D, form):
+    """Three keys of 256 count: one of the second tile of keys, which is taken first, with score 0, and two of the first tile, of 20.1
+    (29 to 29.2 in units of log 2, below what moves the maximum) and 21.4 (30.9 to 31.1). Their weights are rounded once: by 2^-8
+    of themselves. The first one's value alone is not zero; its 64 different multiples of the weight tell how far the weight is off."""
+    E, B, n, Hk, G = H.pkg(), 20, 8, 8, 32
+    page, lens = 16, [256] * B
+    cache, table = H.filled(lens, page, Hk, D, fmt, 66)
+    k, v = (torch.zeros((256, Hk, D), device=DEV) for _ in range(2))
+    k[:, :, 4] = -1.0                                        # the others: -200
+    for j, row in ((131, (0, 0, 0, 0, 0)), (5, (20, 0.125, 0, 1, 0)), (70, (20, 1.375, 0.0625, 1, 0))):
+        k[j, :, :5] = torch.tensor(row, dtype=torch.float32, device=DEV)
+    v[5, :, :64] = 1 + torch.arange(64, device=DEV) / 64.0
+    if fmt == "fp8":
+        v[5, :, :64] = (1 + torch.arange(64, device=DEV) % 8 / 8.0) * 2.0 ** (torch.arange(64, device=DEV) // 8 % 4)
+    for b in range(B):
+        E.engram_kv_write(cache, k, v, torch.from_numpy(H.slots_of(table, b, 0, 256, page)).to(DEV))
+    q = torch.zeros((B * n, Hk * G, D), dtype=torch.bfloat16, device=DEV)
+    q[..., :3], q[..., 4] = 1.0, 200.0
+    q[..., 3] = (torch.rand((B * n, Hk * G), generator=torch.Generator(device=DEV).manual_seed(67), device=DEV) * 0.075 - 0.015).bfloat16()
+    how = dict(slopes=torch.zeros(Hk * G, device=DEV)) if form else {}
+    out = E.engram_prompt_attention(cache, q, P.dev(np.arange(B + 1) * n), P.dev(table), P.dev(lens), scale=1.0, **how)
+    free = q[..., 3].double()
+    s0, s1, s2 = torch.zeros_like(free), 20.125 + free, 21.4375 + free
+    weight = torch.exp(s1) / (torch.exp(s0) + torch.exp(s1) + torch.exp(s2))
+    want = weight[..., None] * v[5, 0].double()
+    got = out.double()
+    half_step = torch.exp2(torch.floor(torch.log2(got.abs().clamp_min(2.0 ** -100))) - 8)
+    # the weight's one rounding, the output's, and 2^-16 for scores of 21 and sums in 32 bits
+    bound = half_step + (2.0 ** -8 + 2.0 ** -16) * want
+    assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() / want.clamp_min(1e-30)).max() * 256)
+
+
+@pytest.mark.parametrize("rise", [31.0, 100.0, 200.0, 1e6])
+def test_scores_that_rise_by_any_number(rise):
+    """Every key half a tile on, in the order in which they are taken, has a score `rise` larger: its value is what comes out."""
+    E, lens = H.pkg(), [1024]
+    cache, table = H.filled(lens, 16, 1, 64, "bf16", 72)
+    slots = torch.from_numpy(H.slots_of(table, 0, 0, 1024, 16)).to(DEV)
+    step = np.concatenate([[2 * (7 - j // 128) + (j % 128) // 64] for j in range(1024)])
+    k, v = (torch.zeros((1024, 1, 64), device=DEV) for _ in range(2))
+    k[:, 0, 0] = torch.as_tensor(step - 7.0, device=DEV)
+    v[:] = torch.as_tensor(1.0 + step, device=DEV)[:, None, None]
+    E.engram_kv_write(cache, k, v, slots)
+    q = torch.zeros((130, 2, 64), dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1.0
+    for cap, slopes in ((0.0, None), (1e16, None), (0.0, torch.zeros(2, device=DEV))):
+        out, lse = E.engram_prompt_attention(cache, q, P.dev([0, 130]), P.dev(table), P.dev(lens), scale=rise, causal=False, cap=cap,
+                                             slopes=slopes, lse=True)
+        assert bool((out == 16.0).all())
+        # 64 keys of the largest score: fp32 of it, and of the logarithm (a capped one: 2^-19 of itself)
+        top = cap * np.tanh(8 * rise / cap) if cap else 8 * rise
+        assert float((lse.double() - (top + np.log(64.0))).abs().max()) <= top * (2.0 ** -21 + (2.0 ** -19 if cap else 0)) + 2.0 ** -20
