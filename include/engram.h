@@ -681,7 +681,8 @@ size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  * T * q_heads / kv_heads < 2^31. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
  * (a code times a power of two; below 2^-133 rounded), and weights 2^(s_j log2(e) - m), m the running maximum or up to
  * 30 behind it, are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32:
- * values times the number of keys seen should stay below 2^97, or a sum may overflow. Results do not depend on timing. Two
+ * values times the number of keys seen should stay below 2^97, or 2^92 where scores are beyond 2^20, and scores below 2^26 in
+ * magnitude (their rounding is a factor of all of a row's weights), or a sum may overflow. Results do not depend on timing. Two
  * launches, the first of one CTA, and a third that joins cut work where tokens are few, chained with programmatic dependent
  * launch.
  */

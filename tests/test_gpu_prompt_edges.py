@@ -137,3 +137,23 @@ def test_scores_that_rise_by_any_number(rise):
         # 64 keys of the largest score: fp32 of it, and of the logarithm (a capped one: 2^-19 of itself)
         top = cap * np.tanh(8 * rise / cap) if cap else 8 * rise
         assert float((lse.double() - (top + np.log(64.0))).abs().max()) <= top * (2.0 ** -21 + (2.0 ** -19 if cap else 0)) + 2.0 ** -20
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_scores_at_the_end_of_their_range(fmt):
+    """Scores of almost 2^26 of either sign: a row's weights share a factor of up to 2^4, and values of 2^80 stay in range."""
+    E, lens = H.pkg(), [600]
+    cache, table = H.filled(lens, 16, 1, 64, fmt, 74)
+    slots = torch.from_numpy(H.slots_of(table, 0, 0, 600, 16)).to(DEV)
+    k, v = (torch.zeros((600, 1, 64), device=DEV) for _ in range(2))
+    k[:, 0, 0] = 2.0 + torch.arange(600, device=DEV) % 14
+    v[:] = (1.0 + torch.arange(600, device=DEV) % 14)[:, None, None] * 2.0 ** 80
+    E.engram_kv_write(cache, k, v, slots)
+    rng = np.random.default_rng(75)
+    q = torch.zeros((400, 2, 64), dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = torch.from_numpy(rng.uniform(1, 4.3e6, (400, 2)) * rng.choice([-1, 1], (400, 2))).to(DEV)
+    out = E.engram_prompt_attention(cache, q, P.dev([0, 400]), P.dev(table), P.dev(lens), scale=1.0, causal=False)
+    want = torch.where(q[..., :1] > 0, 14.0, 1.0).double() * 2.0 ** 80
+    far = q[..., :1].abs() > 100.0                           # the next key's score is that far below: its weight is nothing
+    assert bool(far.float().mean() > 0.99)
+    assert bool(((out.double() - want).abs() <= 2.0 ** -7 * want)[far.expand_as(out)].all())   # the weight's rounding, and the output's
