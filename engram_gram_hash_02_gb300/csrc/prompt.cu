@@ -36,6 +36,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   const int R = pair_rows(p.D);
   pdl_wait();
   pdl_trigger();
+  if (a.join)
+    for (int k = threadIdx.x; k < a.ctas * 8; k += kPlanThreads) a.counters[k] = 0;
   auto bounds = [&](int b, int& s0, int& n, int& len) {
     const int c0 = __ldcg(p.cu + b), c1 = __ldcg(p.cu + b + 1), raw = __ldcg(p.lens + b);
     s0 = (int)min((int64_t)max(c0, 0), p.T);
@@ -238,33 +240,33 @@ Layout layout_of(int32_t G, int32_t D, int64_t T, int32_t B, int ctas) {
   l.max_entries = (T * G + R - 1) / R + B;
   l.slot_floats = R * (D + 2);
   l.header = kAttnZeroBytes;
-  l.starts = l.header + 256;
+  l.counters = l.header + 256;
+  l.starts = l.counters + round256((size_t)ctas * 8 * sizeof(uint32_t));
   l.offsets = l.starts + round256((size_t)ctas * sizeof(Start));
   l.entries = l.offsets + round256(((size_t)B + 1) * sizeof(int32_t));
   l.parts = l.entries + round256((size_t)l.max_entries * sizeof(Entry));
   l.all = l.parts + (size_t)2 * ctas * l.slot_floats * sizeof(float);
   return l;
 }
-int ctas_of(int sms) { return sms < (int)(kAttnZeroBytes / 32) ? sms : (int)(kAttnZeroBytes / 32); }   // eight counters each
 
 }  // namespace
 }  // namespace prompt
 
 size_t prompt_workspace_bytes(int32_t Hk, int32_t G, int32_t D, bool fp8, int64_t T, int32_t B, int sms) {
-  return prompt::layout_of(G, D, T, B, prompt::ctas_of(sms)).all;
+  return prompt::layout_of(G, D, T, B, sms).all;
 }
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   using namespace prompt;
   Args a{};
   a.p = p;
-  a.ctas = ctas_of(num_sms());
+  a.ctas = num_sms();
   const Layout l = layout_of(p.G, p.D, p.T, p.B, a.ctas);
   a.header = reinterpret_cast<Header*>(p.workspace + l.header);
   a.starts = reinterpret_cast<Start*>(p.workspace + l.starts);
   a.offsets = reinterpret_cast<int32_t*>(p.workspace + l.offsets);
   a.entries = reinterpret_cast<Entry*>(p.workspace + l.entries);
-  a.counters = reinterpret_cast<uint32_t*>(p.workspace);
+  a.counters = reinterpret_cast<uint32_t*>(p.workspace + l.counters);
   a.parts = reinterpret_cast<float*>(p.workspace + l.parts);
   a.slot_floats = l.slot_floats;
   a.max_entries = l.max_entries;

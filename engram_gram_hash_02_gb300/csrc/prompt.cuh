@@ -84,9 +84,9 @@ struct Header {
 struct Start {                                        // a CTA's first entry
   int32_t head, entry;
 };
-// workspace behind the zeroed counters
+// workspace behind its zeroed start, which is the one-token calls' and stays as it is
 struct Layout {
-  size_t header, starts, offsets, entries, parts, all;
+  size_t header, counters, starts, offsets, entries, parts, all;
   int64_t max_entries;
   int32_t slot_floats;
 };
@@ -98,7 +98,7 @@ struct Args {
   Start* starts;
   int32_t* offsets;                                   // [B + 1] first entries of the sequences
   Entry* entries;
-  uint32_t* counters;                                 // [CTA][8 warps], zero between calls
+  uint32_t* counters;                                 // [CTA][8 warps], zeroed by the list kernel: a call that gave up leaves any
   float* parts;
   int64_t max_entries;
   int32_t slot_floats;
@@ -795,7 +795,6 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               __threadfence();
               asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(last) : "l"(counter) : "memory");
               last = last == (uint32_t)(s.c_last - s.c_first);
-              if (last) *counter = 0;                 // the next call finds it zero
               __threadfence();
             }
             if (__shfl_sync(0xFFFFFFFFu, last, 0) && valid)

@@ -44,7 +44,7 @@ extern "C" {
 /* bits of the device err_flag word */
 #define ENGRAM_ERR_RAW_ID 1        /* raw input id outside [0, raw_vocab): used pad_id */
 #define ENGRAM_ERR_ROW_ID 2        /* row id outside [0, num_rows): wrote a zero row */
-#define ENGRAM_ERR_PIPE_TIMEOUT 4  /* a pipeline wait (GEMM, gate) ran past its time limit */
+#define ENGRAM_ERR_PIPE_TIMEOUT 4  /* a pipeline wait (GEMM, gate, prompts) ran past its time limit */
 #define ENGRAM_ERR_SLOT 8          /* cache slot past the cache: not written, read as zeros */
 #define ENGRAM_ERR_PAGE 16         /* page number outside [0, num_pages): its keys are not attended */
 #define ENGRAM_ERR_POSITION 32     /* position outside the rotation table: the nearest row was used */
@@ -677,7 +677,10 @@ size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  *               cache hides its tokens. table_width * page_size counts up to 2^31 - 256 tokens
  *   scores      NULL or a form of scores
  *   out         bf16 rows [T, q_heads, head_dim]       lse  device fp32 [T, q_heads], or NULL
- *   workspace   as engram_paged_attention (the same zeroed start); one may serve all the attention calls in order
+ *   workspace   device, 256-byte aligned, engram_prompt_workspace_bytes; one may serve all the attention calls in order. Its
+ *               first ENGRAM_ATTENTION_ZERO_BYTES are the one-token calls': they are neither read nor written here
+ *   err_flag    ENGRAM_ERR_SEQ_LEN and ENGRAM_ERR_PAGE as engram_paged_attention; ENGRAM_ERR_PIPE_TIMEOUT if a wait inside the
+ *               kernel ran past its limit: out and lse are invalid then, and the workspace serves the next call as before
  * T * q_heads / kv_heads < 2^31. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
  * (a code times a power of two; below 2^-133 rounded), and weights 2^(s_j log2(e) - m), m the running maximum or up to
  * 30 behind it, are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32:
@@ -706,6 +709,7 @@ size_t engram_shared_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  *                 like cu_seqlens. A sequence that is in no group has no prefix. Groups may not share sequences
  *   q             bf16 rows [batch, q_heads, head_dim]
  *   out, lse, scores, err_flag  as engram_paged_attention2; over all of a sequence's keys
+ *                 (and ENGRAM_ERR_PIPE_TIMEOUT as engram_prompt_attention)
  *   workspace     engram_shared_workspace_bytes; its zeroed start as engram_paged_attention
  * The prefix's part is summed as in engram_prompt_attention, the own part as in engram_paged_attention; they are
  * joined in fp32. Three launches, or four (engram_prompt_attention's, then engram_paged_attention's).

@@ -157,3 +157,24 @@ def test_scores_at_the_end_of_their_range(fmt):
     far = q[..., :1].abs() > 100.0                           # the next key's score is that far below: its weight is nothing
     assert bool(far.float().mean() > 0.99)
     assert bool(((out.double() - want).abs() <= 2.0 ** -7 * want)[far.expand_as(out)].all())   # the weight's rounding, and the output's
+
+
+@pytest.mark.parametrize("new,old", [([64] * 100, [300] * 100), ([70], [2930])])
+def test_prompts_do_not_depend_on_the_workspaces_start(new, old):
+    """The zeroed start belongs to the one-token calls: prompts neither read nor write it, so that a call that gave up (a wait past
+    its limit) leaves nothing behind for the next one. What else a workspace holds does not count either."""
+    E = H.pkg()
+    lens = [n + m for n, m in zip(new, old)]
+    cache, table = H.filled(lens, 16, 4, 128, "bf16", 70)
+    T = sum(new)
+    q = randn(71, (T, 8, 128))
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    want, want_lse = E.engram_prompt_attention(cache, q, *args, lse=True)
+    P.check_prompt(cache, table, new, lens, q, want, want_lse, 128 ** -0.5)
+    for byte in (0x01, 0xA5, 0xFF):
+        ws = torch.full((E.prompt_workspace_bytes(cache, 8, T, len(new)),), byte, dtype=torch.uint8, device=DEV)
+        out, lse = torch.full_like(q, float("nan")), torch.full_like(want_lse, float("nan"))
+        for _ in range(2):
+            E.engram_prompt_attention(cache, q, *args, out=out, lse=lse, workspace=ws)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert bool((ws[:ZERO] == byte).all())
