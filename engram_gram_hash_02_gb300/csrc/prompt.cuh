@@ -37,6 +37,7 @@
 #pragma once
 
 #include "attn.cuh"
+#include "ring.h"
 #include "tc_common.cuh"
 
 namespace engram {
@@ -333,6 +334,7 @@ struct Ctl {
   uint64_t s_full[2], p_full[2], o_final[2], o_done;
   uint64_t seg_full[2], seg_empty[2];
   uint64_t drained;
+  int32_t asked[2], asked_q;                          // what loaders request next, on their way out (place | parity << 8); Q's last phase
   Segment seg[2];
   alignas(16) uint32_t live[kMeta][4];                // which keys of a tile are there
   uint32_t v_bad[kMeta][kMaxHelpers][4];              // keys whose values are not all finite (in tiles that some row sees partly)
@@ -341,6 +343,21 @@ struct Ctl {
 };
 constexpr int smem_bytes(bool fp8) { return 1024 + kQBytes + slots_of(fp8) * kSlotBytes + (fp8 ? kStages * kStageBytes : 0) + 8 * staging_bytes(fp8) + (int)sizeof(Ctl); }
 static_assert(smem_bytes(false) <= kSmemBudget && smem_bytes(true) <= kSmemBudget, "one CTA's shared memory");
+
+// A block that leaves because a wait has run out: what it has issued may still run, and boxes may be on their way to shared memory
+// that is another block's next. A commit behind the MMAs and everyone's last requests are waited for, with a limit
+template <bool kFp8>
+__device__ __noinline__ void drain(Ctl* ctl, int loaders, bool q_box) {
+  volatile int32_t never = 0;
+  mbar_init(smem_u32(&ctl->drained), 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  tc_commit(smem_u32(&ctl->drained));
+  wait_inline(smem_u32(&ctl->drained), 0, &never, nullptr);
+  if (q_box) wait_inline(smem_u32(&ctl->q_full), ctl->asked_q & 1u, &never, nullptr);
+  for (int k = 0; k < loaders; ++k)
+    for (int i = 0; i < (kFp8 ? kStages : slots_of(kFp8)); ++i)
+      wait_inline(smem_u32(kFp8 ? &ctl->st_full[i] : &ctl->full[i]), last_request(i, ctl->asked[k] & 0xFF, (uint32_t)ctl->asked[k] >> 8), &never, nullptr);
+}
 
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 // ---- two values at once; the largest of three ------------------------------------------------------------------
@@ -431,6 +448,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
     }
     mbar_init(smem_u32(&ctl->o_done), 1);
     ctl->abort_flag = 0;
+    ctl->asked_q = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -1149,6 +1167,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
       }
       cp_async_commit();
       cp_async_wait<0>();
+      if (lane == 0) ctl->asked[loader] = kFp8 ? stage | st_phase << 8 : slot | phase << 8;
     } else {
       // -------------------------------------------------------------- Q; rows to convert, to fetch or to look through
       const int w = warp < 12 ? warp - 10 : warp - 10 - loaders;
@@ -1164,6 +1183,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           if (w == 0 && elect_one()) {
             const int blocks = (D + 63) / 64;
             const uint32_t bar = smem_u32(&ctl->q_full);
+            ctl->asked_q = (int)q_n;
             mbar_expect_tx(bar, (uint32_t)(s.nt * blocks * kBlockBytes));
             for (int t = 0; t < s.nt; ++t)
               for (int k = 0; k < blocks; ++k)
@@ -1421,16 +1441,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
-    if (*abort_flag) {
-      // what has been issued may still run: a commit behind it, waited for with a limit
-      if (elect_one()) {
-        volatile int32_t never = 0;
-        mbar_init(smem_u32(&ctl->drained), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tc_commit(smem_u32(&ctl->drained));
-        wait_inline(smem_u32(&ctl->drained), 0, &never, nullptr);
-      }
-    }
+    if (*abort_flag && elect_one()) drain<kFp8>(ctl, a.box > 0 ? loaders : 0, a.q_box != 0);
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
