@@ -265,6 +265,12 @@ int check_prompt(const char* fn, const EngramKVCache* c, const EngramPagedSeqs* 
   p->D = c->head_dim;
   p->cap = capacity(s, c);
   p->scale_log2 = (float)((double)scale * kLog2e);
+  // Capped scores are formed with scale / cap, which is to be finite (0 times it, too): beyond 2^120 the tanh of any product but
+  // the smallest 2^-118 is 1
+  if (p->form.cap2 > 0.f) {
+    const float most = fminf(0x1p120f / p->form.cap_inv, 0x1p127f);
+    p->scale_log2 = fminf(fmaxf(p->scale_log2, -most), most);
+  }
   return ENGRAM_OK;
 }
 

@@ -178,3 +178,15 @@ def test_prompts_do_not_depend_on_the_workspaces_start(new, old):
             E.engram_prompt_attention(cache, q, *args, out=out, lse=lse, workspace=ws)
             assert torch.equal(out, want) and torch.equal(lse, want_lse)
         assert bool((ws[:ZERO] == byte).all())
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_a_cap_far_below_the_scale(slopes):
+    """scale / cap is past what 32 bits hold: every score is 0 or +-cap, which is next to nothing, and all weights are equal."""
+    E, new, lens = H.pkg(), [60, 7], [60, 300]
+    cache, table = H.filled(lens, 16, 2, 64, "bf16", 68)
+    q = randn(69, (67, 4, 64))
+    q[::3] = 0.0
+    out, lse = E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(lens), scale=2.0 ** 70, cap=2.0 ** -60, causal=False,
+                                         slopes=torch.zeros(4, device=DEV) if slopes else None, lse=True)
+    P.check_prompt(cache, table, new, lens, torch.zeros_like(q), out, lse, 1.0, causal=False)
