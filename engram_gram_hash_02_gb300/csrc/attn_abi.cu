@@ -168,6 +168,9 @@ int check_workspace(const char* fn, const void* workspace, size_t ws_bytes, size
   return ENGRAM_OK;
 }
 
+// rows of a key head: a pair of tiles from any of them on is counted in 32 bits
+constexpr int64_t kMaxPromptRows = ((int64_t)1 << 31) - 256;
+
 constexpr double kLog2e = 1.4426950408889634;
 
 // `to` stays zero (no form) without one; returns whether there is one in `*any`
@@ -248,7 +251,7 @@ int check_prompt(const char* fn, const EngramKVCache* c, const EngramPagedSeqs* 
   ENGRAM_CHECK_ARG(!p->q.f32, "%s: q must be bf16", fn);
   ENGRAM_CHECK_ARG(p->q.heads % c->kv_heads == 0, "%s: q_heads (%d) must be a multiple of kv_heads (%d)", fn, p->q.heads, c->kv_heads);
   const int32_t G = p->q.heads / c->kv_heads;
-  ENGRAM_CHECK_ARG(T * G < (int64_t)1 << 31, "%s: T * q_heads / kv_heads must be below 2^31", fn);
+  ENGRAM_CHECK_ARG(T * G <= kMaxPromptRows, "%s: T * q_heads / kv_heads must be at most 2^31 - 256", fn);
   ENGRAM_CHECK_ARG((cu != nullptr || s->batch == 0) && aligned(cu, 4), "%s: %s must be a non-NULL, aligned int32 array", fn, starts);
   ENGRAM_CHECK_ARG(isfinite(scale), "%s: scale must be finite", fn);
   bool any;
@@ -479,7 +482,7 @@ int engram_attention_step2(const EngramNormRope* nr, const EngramKVCache* cache,
 }
 
 size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int64_t T, int32_t batch) {
-  if (!sized(cache, q_heads) || T < 0 || T >= (int64_t)1 << 31 || T * (q_heads / cache->kv_heads) >= (int64_t)1 << 31 || batch < 0) return 0;
+  if (!sized(cache, q_heads) || T < 0 || T >= (int64_t)1 << 31 || T * (q_heads / cache->kv_heads) > kMaxPromptRows || batch < 0) return 0;
   return prompt_bytes(cache, q_heads, T, batch);
 }
 
@@ -523,7 +526,7 @@ int engram_prompt_attention(const EngramKVCache* cache, const EngramPagedSeqs* s
 }
 
 size_t engram_shared_workspace_bytes(const EngramKVCache* cache, int32_t q_heads, int32_t batch, int32_t groups) {
-  if (!sized(cache, q_heads) || batch < 0 || groups < 0 || (int64_t)batch * (q_heads / cache->kv_heads) >= (int64_t)1 << 31) return 0;
+  if (!sized(cache, q_heads) || batch < 0 || groups < 0 || (int64_t)batch * (q_heads / cache->kv_heads) > kMaxPromptRows) return 0;
   return shared_bytes(cache, q_heads, batch, groups).all;
 }
 

@@ -681,7 +681,7 @@ size_t engram_prompt_workspace_bytes(const EngramKVCache* cache, int32_t q_heads
  *               first ENGRAM_ATTENTION_ZERO_BYTES are the one-token calls': they are neither read nor written here
  *   err_flag    ENGRAM_ERR_SEQ_LEN and ENGRAM_ERR_PAGE as engram_paged_attention; ENGRAM_ERR_PIPE_TIMEOUT if a wait inside the
  *               kernel ran past its limit: out and lse are invalid then, and the workspace serves the next call as before
- * T * q_heads / kv_heads < 2^31. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
+ * T * q_heads / kv_heads is at most 2^31 - 256. Products take bf16 operands with fp32 accumulation: FP8 rows enter as bf16, exactly
  * (a code times a power of two; below 2^-133 rounded), and weights 2^(s_j log2(e) - m), m the running maximum or up to
  * 30 behind it, are rounded to bf16 (2^-8 of themselves at most). Scores, maxima, sums and lse are fp32:
  * values times the number of keys seen should stay below 2^97, or 2^92 where scores are beyond 2^20, and scores below 2^26 in
