@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), a.box == 0 ? helpers : kFp8 ? helpers / 2 : loaders);
+      mbar_init(smem_u32(&ctl->full[s]), a.box == 0 ? helpers + loaders : kFp8 ? helpers / 2 : loaders);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -1138,6 +1138,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
               }
             }
+            // Rows one by one: nothing to bring, but the slot is not full without this warp. What waits for a slot has a part in filling
+            // it, everywhere: a barrier that went on without this warp would be two phases ahead of its wait, and parity does not
+            // tell that from the phase before
+            if (a.box == 0 && lane == 0) arrive(ctl->full[slot]);
             if (kFp8 && a.box > 0) {
               if (++stage == kStages) { stage = 0; st_phase ^= 1u; }
             } else if (++slot == kSlots) {

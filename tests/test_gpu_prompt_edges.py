@@ -190,3 +190,24 @@ def test_a_cap_far_below_the_scale(slopes):
     out, lse = E.engram_prompt_attention(cache, q, P.dev(cu_of(new)), P.dev(table), P.dev(lens), scale=2.0 ** 70, cap=2.0 ** -60, causal=False,
                                          slopes=torch.zeros(4, device=DEV) if slopes else None, lse=True)
     P.check_prompt(cache, table, new, lens, torch.zeros_like(q), out, lse, 1.0, causal=False)
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 240), ("fp8", 256), ("bf16", 64), ("fp8", 128)])
+def test_rows_one_by_one_in_short_pieces_many_times(fmt, D):
+    """Pages that do not divide into boxes, key tiles in ones and twos: no wait is left behind, and every call gives the same bits."""
+    E = H.pkg()
+    new = [2, 27, 1, 1, 0, 44, 23, 32, 0, 2, 0, 35, 11, 2, 33, 1]
+    lens = [n + m for n, m in zip(new, [27, 388, 141, 372, 278, 152, 140, 378, 383, 111, 0, 2, 385, 187, 22, 184])]
+    cache, table = H.filled(lens, 7, 3, D, fmt, 76, "padded")
+    T = sum(new)
+    q = randn(77, (T, 48, D))
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    err = word()
+    ws = E.prompt_workspace(cache, 48, T, len(new))
+    out, lse = E.engram_prompt_attention(cache, q, *args, lse=True, workspace=ws, err=err)
+    P.check_prompt(cache, table, new, lens, q, out, lse, D ** -0.5)
+    again, again_lse = torch.empty_like(out), torch.empty_like(lse)
+    plan = E.PromptAttentionPlan(cache, q, *args, out=again, lse=again_lse, workspace=ws, err=err)
+    for _ in range(2000):
+        plan.run()
+    assert int(err) == 0 and torch.equal(again, out) and torch.equal(again_lse, lse)
