@@ -331,7 +331,8 @@ struct Ctl {
   uint64_t q_full, q_empty;
   uint64_t k_meta[kMeta];                             // of key tiles, in turn: `live` is there
   uint64_t v_go[kMeta], v_meta[kMeta];                // of value tiles that some row sees partly: requested; looked through
-  uint64_t s_full[2], p_full[2], o_final[2], o_done;
+  uint64_t s_full[2], p_full[2], o_done;
+  uint64_t o_final[2][2];                             // [tile][segments in turn]: the segment's sums are
   uint64_t seg_full[2], seg_empty[2];
   uint64_t drained;
   int32_t asked[2], asked_q;                          // what loaders request next, on their way out (place | parity << 8); Q's last phase
@@ -442,7 +443,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
       mbar_init(smem_u32(&ctl->p_full[i]), 4);
-      mbar_init(smem_u32(&ctl->o_final[i]), 1);
+      mbar_init(smem_u32(&ctl->o_final[0][i]), 1);
+      mbar_init(smem_u32(&ctl->o_final[1][i]), 1);
       mbar_init(smem_u32(&ctl->seg_full[i]), 1);
       mbar_init(smem_u32(&ctl->seg_empty[i]), 8 + 1 + loaders + helpers);
     }
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     const uint32_t o_t = lanes + kOCol + (uint32_t)(tile * 128);
     uint32_t used[2] = {0, 0};                        // tiles that went through the S buffers
-    uint32_t finals = 0, dones = 0, keys_n = 0, pc = 0;   // o_final and o_done phases; key tiles; those some row sees partly
+    uint32_t dones = 0, keys_n = 0, pc = 0;           // o_done phases; key tiles; those some row sees partly
     bool ok = true;
     while (ok && next_segment(true)) {
       const Segment& s = ctl->seg[seg_n & 1];         // read where it lies: registers are for the scores
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
         }
         if (!ok) break;
         // ---- the segment's result
-        if (!wait_warp(ctl->o_final[tile], finals)) { ok = false; break; }
+        if (!wait_warp(ctl->o_final[tile][seg_n & 1], seg_n >> 1)) { ok = false; break; }
         tc_fence_after();
         const int64_t token = (int64_t)s.s0 + (valid ? (int)fast_div((uint32_t)r, a.div_g) : 0);
         const int h = s.head * G + g;
@@ -821,11 +823,13 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
           }
         }
         tc_fence_before();
-        ++finals;
       }
-      // The second tile's warps stay with a segment of one tile: a barrier's phases are told apart by their parity alone
+      // The second tile's warps stay with a segment of one tile until its sums are final, so that every barrier is at the phase that
+      // they have counted when they go on: one's phases are told apart by parity alone. (Not by its scores, tile by tile: nobody
+      // waits for these warps there, and while they still join the last segment's rows the scores may be many phases ahead.
+      // The segment after next is not handed out without them, so that of two barriers for sums neither is.)
       if (!kWide && !mine) {
-        for (int n = 1; ok && n < s.tiles; n += 2) ok = wait_warp(ctl->s_full[1], used[1] + (n >> 1));
+        ok = wait_warp(ctl->o_final[1][seg_n & 1], seg_n >> 1);
         for (int n = 0; n < s.tiles; ++n) pc += partly_seen(s, n);
       }
       if (s.nt == 2) {
@@ -922,7 +926,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
                   qk(t, t, slot, 0);
                   commit(ctl->s_full[t]);
                 } else {
-                  commit(ctl->o_final[t]);
+                  commit(ctl->o_final[t][seg_n & 1]);
                 }
               }
               if (!ok) break;
@@ -963,7 +967,10 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
               }
               if (!ok) break;
               commit(ctl->o_done);
-              if (n + 1 == T) commit(ctl->o_final[0]);
+              if (n + 1 == T) {
+                commit(ctl->o_final[0][seg_n & 1]);
+                if (!kWide) commit(ctl->o_final[1][seg_n & 1]);
+              }
               if (n + 2 < T) ok = keys(n + 2);
             }
             used[0] += (T + 1) >> 1;

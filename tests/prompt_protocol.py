@@ -39,7 +39,7 @@ class Kernel:
         self.q_full, self.q_empty = Barrier("q_full", 1 if q_box else self.helpers), Barrier("q_empty", 1)
         self.k_meta, self.v_go, self.v_meta = bars("k_meta", META, 1), bars("v_go", META, 1), bars("v_meta", META, self.helpers)
         self.s_full, self.p_full = bars("s_full", 2, 1), bars("p_full", 2, 2)
-        self.o_first, self.o_second, self.o_done = bars("o_first", 2, 1), Barrier("o_second", 1), Barrier("o_done", 1)
+        self.o_final, self.o_done = [bars("o_final", 2, 1) for _ in range(2)], Barrier("o_done", 1)
         self.seg_full, self.seg_empty = bars("seg_full", 2, 1), bars("seg_empty", 2, 4 + 1 + self.loaders + self.helpers)
         self.commits, self.landing = [], []
 
@@ -177,7 +177,7 @@ class Kernel:
                                 yield f, x
                             commit(self.s_full[t])
                         else:
-                            commit(self.o_first[k & 1] if t == 0 else self.o_second)
+                            commit(self.o_final[t][k & 1])
                     if n + 1 < T:
                         commit(ke)
                         if n + 2 == T:
@@ -204,7 +204,9 @@ class Kernel:
                         commit(e)
                     commit(self.o_done)
                     if n + 1 == T:
-                        commit(self.o_first[k & 1])
+                        commit(self.o_final[0][k & 1])
+                        if not self.wide:
+                            commit(self.o_final[1][k & 1])
                     if n + 2 < T:
                         yield from keys(n + 2)
                 st["used"] = [st["used"][0] + (T + 1) // 2, st["used"][1] + T // 2]
@@ -213,7 +215,7 @@ class Kernel:
         yield from self.each_segment(segment)
 
     def softmax(self, tile):
-        st = dict(used=[0, 0], kn=0, pc=0, dones=0, seconds=0)
+        st = dict(used=[0, 0], kn=0, pc=0, dones=0)
 
         def segment(k, s):
             T, nt = s["T"], s["nt"]
@@ -233,11 +235,7 @@ class Kernel:
                         st["pc"] += 1
                     yield None
                     self.p_full[buf].arrive()
-                if tile == 0:
-                    yield self.o_first[k & 1], k >> 1
-                else:
-                    yield self.o_second, st["seconds"]
-                    st["seconds"] += 1
+                yield self.o_final[tile][k & 1], k >> 1
                 for _ in range(self.rng.choice([0, 0, 3, 60])):   # outputs, a join
                     yield None
             elif not self.wide:
@@ -245,7 +243,7 @@ class Kernel:
                     for n in range(1, T, 2):
                         yield self.s_full[1], st["used"][1] + (n >> 1)
                 else:
-                    yield self.o_first[k & 1], k >> 1
+                    yield self.o_final[1][k & 1], k >> 1
                 st["pc"] += sum(s["partly"])
             if nt == 2:
                 st["used"] = [u + T for u in st["used"]]

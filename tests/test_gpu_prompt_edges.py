@@ -211,3 +211,23 @@ def test_rows_one_by_one_in_short_pieces_many_times(fmt, D):
     for _ in range(2000):
         plan.run()
     assert int(err) == 0 and torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
+@pytest.mark.parametrize("fmt,page", [("bf16", 16), ("fp8", 16), ("bf16", 5)])
+def test_two_tiles_with_long_joins_before_one_tile_many_times(fmt, page):
+    """Long sequences of two tiles, cut many times and joined by one block's warps, each followed by ones of a single tile."""
+    E = H.pkg()
+    new, old = [64, 9, 70, 5] * 10, [6000, 900, 2500, 1300] * 10
+    lens = [n + m for n, m in zip(new, old)]
+    cache, table = H.filled(lens, page, 4, 64, fmt, 78)
+    T = sum(new)
+    q = randn(79, (T, 16, 64))
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    err = word()
+    out, lse = E.engram_prompt_attention(cache, q, *args, lse=True, err=err)
+    P.check_prompt(cache, table, new, lens, q, out, lse, 0.125, rows=np.arange(0, T, 13))
+    again, again_lse = torch.empty_like(out), torch.empty_like(lse)
+    plan = E.PromptAttentionPlan(cache, q, *args, out=again, lse=again_lse, err=err)
+    for _ in range(500):
+        plan.run()
+    assert int(err) == 0 and torch.equal(again, out) and torch.equal(again_lse, lse)
