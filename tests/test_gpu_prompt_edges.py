@@ -231,3 +231,36 @@ def test_two_tiles_with_long_joins_before_one_tile_many_times(fmt, page):
     for _ in range(500):
         plan.run()
     assert int(err) == 0 and torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
+@pytest.mark.parametrize("Hq", [8, 6])                       # queries as boxes, and row by row
+def test_outputs_in_the_place_of_queries(Hq):
+    """Whole pairs, cut ones and rows that see nothing; a batch that shares a prefix."""
+    E, new, lens = H.pkg(), [700, 3, 90, 20], [700, 4000, 5000, 10]
+    cache, table = H.filled(lens, 16, 2, 128, "bf16", 80)
+    T = sum(new)
+    q = randn(81, (T, Hq, 128))
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    want = E.engram_prompt_attention(cache, q, *args)
+    same = q.clone()
+    assert E.engram_prompt_attention(cache, same, *args, out=same) is same and torch.equal(same, want)
+    q = randn(82, (3, Hq, 128))
+    args = P.dev(table[2:3]), P.dev([5000]), P.dev([0, 3]), P.dev(table[[0, 1, 3]]), P.dev([700, 0, 10])
+    want = E.engram_shared_attention(cache, q, *args)
+    same = q.clone()
+    assert E.engram_shared_attention(cache, same, *args, out=same) is same and torch.equal(same, want)
+
+
+def test_views_that_repeat_rows():
+    """Strides of zero, which no tensor map takes: one query row for all heads, one key head's rows for all."""
+    E, new, lens = H.pkg(), [150, 40], [300, 40]
+    cache, table = H.filled(lens, 16, 1, 64, "bf16", 83)
+    args = P.dev(cu_of(new)), P.dev(table), P.dev(lens)
+    q = randn(84, (190, 1, 64)).expand(190, 8, 64)
+    wide = E.KVCache(cache.k.expand(-1, 4, -1, -1), cache.v.expand(-1, 4, -1, -1))
+    full = E.KVCache(wide.k.contiguous(), wide.v.contiguous())
+    want, want_lse = E.engram_prompt_attention(full, q.contiguous(), *args, lse=True)
+    P.check_prompt(full, table, new, lens, q, want, want_lse, 0.125)
+    for c, x in ((wide, q), (wide, q.contiguous()), (full, q)):
+        out, lse = E.engram_prompt_attention(c, x, *args, lse=True)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -34,3 +34,11 @@ def test_requested_boxes_land_before_a_block_leaves():
     for request, said, bars in (("tma_load_4d(", "ctl->asked[", ("kFp8 ? &ctl->st_full", "&ctl->full")), ("tma_load_3d(", "ctl->asked_q", ("&ctl->q_full",))):
         assert said in roles[roles.rindex(request) - 600:] and said in leaving, request
         assert all(f"wait_inline(smem_u32({b}" in leaving or f": {b}" in leaving for b in bars), request
+
+
+@pytest.mark.parametrize("name", ["prompt.cu", "prompt.cuh", "prompt_bf16.cu", "prompt_fp8.cu", "attention_form_bf16.cu", "attention_form_fp8.cu"])
+def test_no_non_coherent_loads(name):
+    """Kernels start while their predecessor on the stream still runs; that load path is for data that nothing writes meanwhile."""
+    with open(os.path.join(CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.findall(r"__ldg\b|ld\.global\.nc|__restrict__", code)
