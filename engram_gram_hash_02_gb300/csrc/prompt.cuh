@@ -26,14 +26,20 @@
 //
 // Keys outside of a row's interval are masked in S. P is zero there, but 0 * inf is not: in a value tile that some row sees
 // only in part, infinities and NaN are replaced by zeros, and the softmax warps add their products to the rows that see
-// them.
+// them. A row that sees nothing is left out of that, and is zero by a select.
 //
-// Roundings below 32 bits: P to bf16 (2^-8 of itself at most). The sums take P before that.
+// A barrier tells its phases apart by parity alone, so nobody may wait for a phase that lies two away from where the barrier is:
+// whoever waits for a slot has a part in filling it, and whoever waits for scores or sums in what comes next. (A model of all
+// waits and arrivals is among the tests.)
 //
-// Measured (one GB300, 8192 tokens of one prompt, 32 / 8 heads of 128): bf16 467 us, 1.18 PFLOP/s, the tensor pipe 56 % busy; a
-// cap 811 us, slopes 675, FP8 720. Heads of 256 (16 / 2): 592 us, bound by key and value tiles from L2 for every 128 rows
+// Roundings below 32 bits: P to bf16, once (2^-8 of itself at most): it is an operand of the tensor cores beside V, which is bf16,
+// and two bf16 for it would be a second P V. The sums take P before that.
+//
+// Measured (one GB300, 8192 tokens of one prompt, 32 / 8 heads of 128): bf16 462 us, 1.19 PFLOP/s, the tensor pipe 56 % busy; a
+// cap 817 us, slopes 647, FP8 717. Heads of 256 (16 / 2): 606 us, bound by key and value tiles from L2 for every 128 rows
 // (without softmax and MMAs 425). Without the softmax heads of 128 take 363 us: its latency per tile is what bounds them, and over FP8 the
-// codes' conversion beside it.
+// codes' conversion beside it. (What stands elsewhere in the kernel moves the hot loops' code: up to 4 % between builds that differ
+// in nothing that runs.)
 #pragma once
 
 #include "attn.cuh"
@@ -563,8 +569,8 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1) prompt_kernel(const __gri
             tmem_st_wait();
           }
           // Scores at a time: half a tile; a quarter over FP8 where 144 registers do not hold the form or the wide loop beside
-          // half a tile's (8192 tokens capped at 30: 998 us against 1086; heads of 256: 1027 against 1100; elsewhere halves are
-          // better, bf16 467 against 499)
+          // half a tile's (8192 tokens capped at 30: 1000 us against 1086; heads of 256: 1035 against 1100; elsewhere halves are
+          // better, bf16 462 against 499)
           constexpr int kCols = kFp8 && (kWide || kForm) ? 32 : 64;
           // In a loop: unrolled over a whole tile, instruction fetches took a third of the time. The
           // exponentials are formed with the maximum so far, while the half's own is found: o, the sum and P are in units of
